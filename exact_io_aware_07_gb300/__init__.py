@@ -14,11 +14,18 @@ Entry points (same names as the C ABI):
     fa_fwd_splitkv(q, k, v, o, lse, causal, scale, num_splits, workspace, stream=None)
     fa_fwd_splitkv_noalloc(q, k, v, o, lse, causal, scale, num_splits, stream=None)
     fa_bwd(q, k, v, o, lse, dout, dq, dk, dv, causal, scale, workspace, stream=None)
-    fa_fwd_splitkv_workspace_bytes, fa_fwd_splitkv_count, fa_fwd_fp8_workspace_bytes, fa_bwd_workspace_bytes
+    fa_page_plan(ctx_lens, new_lens, free_pages, free_head, block_table, seq_lens, cu_new, slot_map,
+                 free_head_out, num_pages, stream=None)
+    fa_kv_append(k_new, v_new, slot_map, k_pages, v_pages, stream=None)
+    fa_fwd_prefix_paged(q, k_pages, v_pages, prefix_table, prefix_len, block_table, seq_lens, cu_new, max_new,
+                        o, lse, causal, scale, workspace=None, stream=None)
+    fa_fwd_splitkv_workspace_bytes, fa_fwd_splitkv_count, fa_fwd_fp8_workspace_bytes, fa_bwd_workspace_bytes,
+    fa_fwd_prefix_paged_workspace_bytes
     fa_status_string(code), fa_device_status(stream=None), fa_selftest_wait_timeout(us, stream=None)
     fa_fwd_launch_shape(B, H, T, d, causal, num_sms), fa_ex2_rate(stream=None), fa_version()
-and the convenience wrappers ``attention``, ``attention_gqa``, ``attention_splitkv``
-and ``attention_bwd`` that allocate their outputs (and workspaces) with PyTorch.
+and the convenience wrappers ``attention``, ``attention_gqa``, ``attention_splitkv``,
+``attention_bwd``, ``page_plan`` and ``attention_prefix_paged`` that allocate their
+outputs (and workspaces) with PyTorch.
 """
 from __future__ import annotations
 
@@ -33,6 +40,8 @@ __all__ = [
     "fa_fwd_splitkv_count", "fa_status_string", "fa_device_status", "FA_NOALLOC_SCRATCH_BYTES",
     "fa_fwd_launch_shape", "fa_selftest_wait_timeout", "fa_ex2_rate", "fa_version",
     "attention", "attention_splitkv", "load_library", "STATUS", "FA_MAX_SPLITS",
+    "fa_page_plan", "page_plan", "fa_kv_append", "fa_fwd_prefix_paged", "fa_fwd_prefix_paged_workspace_bytes",
+    "attention_prefix_paged", "PAGE",
 ]
 
 STATUS = {
@@ -40,12 +49,14 @@ STATUS = {
     4: "FA_ERR_UNSUPPORTED_HEAD_DIM", 5: "FA_ERR_BAD_SCALE", 6: "FA_ERR_NO_DEVICE_SUPPORT",
     7: "FA_ERR_LAUNCH", 8: "FA_ERR_DEVICE_TIMEOUT", 9: "FA_ERR_BAD_ARG", 10: "FA_ERR_BAD_POINTER",
     11: "FA_ERR_ALIAS", 12: "FA_ERR_CUDA", 13: "FA_ERR_WORKSPACE", 14: "FA_ERR_BAD_PAGE",
+    15: "FA_ERR_BAD_LENGTH", 16: "FA_ERR_NO_PAGES",
 }
 FA_MAX_SPLITS = 256
 EXPORTED = ["fa_fwd", "fa_fwd_gqa", "fa_fwd_paged", "fa_fwd_fp8", "fa_fwd_fp8_workspace_bytes", "fa_bwd",
             "fa_bwd_workspace_bytes", "fa_fwd_splitkv", "fa_fwd_splitkv_noalloc", "fa_fwd_splitkv_workspace_bytes",
             "fa_fwd_splitkv_count", "fa_status_string", "fa_device_status", "fa_fwd_launch_shape", "fa_selftest_wait_timeout", "fa_ex2_rate",
-            "fa_version"]
+            "fa_version", "fa_page_plan", "fa_kv_append", "fa_fwd_prefix_paged", "fa_fwd_prefix_paged_workspace_bytes"]
+PAGE = 128  # keys per page of a paged cache
 FA_NOALLOC_SCRATCH_BYTES = 32 << 20
 
 
@@ -103,6 +114,15 @@ def load_library(path: str | None = None) -> ctypes.CDLL:
     lib.fa_selftest_wait_timeout.restype = i
     lib.fa_ex2_rate.argtypes = [ctypes.POINTER(ctypes.c_double), vp]
     lib.fa_ex2_rate.restype = i
+    ll = ctypes.c_longlong
+    lib.fa_page_plan.argtypes = [vp] * 9 + [i] * 5 + [vp]
+    lib.fa_page_plan.restype = i
+    lib.fa_kv_append.argtypes = [vp] * 5 + [i, i, i, ll, ll, i, vp]
+    lib.fa_kv_append.restype = i
+    lib.fa_fwd_prefix_paged.argtypes = [vp] * 9 + [i] * 8 + [f, i, i, vp, ctypes.c_size_t, vp]
+    lib.fa_fwd_prefix_paged.restype = i
+    lib.fa_fwd_prefix_paged_workspace_bytes.argtypes = [i] * 5
+    lib.fa_fwd_prefix_paged_workspace_bytes.restype = ctypes.c_size_t
     lib.fa_version.argtypes = []
     lib.fa_version.restype = ctypes.c_char_p
     if path == lib_path():
@@ -244,6 +264,145 @@ def fa_fwd_paged(q, k_pages, v_pages, block_table, o, lse, causal: bool, scale: 
                                        ctypes.c_void_p(_stream_handle(stream)))
     if code:
         raise FAError(code, "fa_fwd_paged")
+
+
+def _check_ints(**tensors):
+    import torch
+
+    for name, (t, shape) in tensors.items():
+        if t.dtype != torch.int32 or tuple(t.shape) != shape or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous int32 tensor of shape {shape}")
+
+
+def _check_pools(k_pages, v_pages):
+    """(num_pages, Hkv, d) of two page pools."""
+    import torch
+
+    for name, t in (("k_pages", k_pages), ("v_pages", v_pages)):
+        if t.dtype != torch.bfloat16 or t.dim() != 4 or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous bf16 4-D tensor")
+    num_pages, Hkv, page, d = k_pages.shape
+    if page != PAGE or v_pages.shape != k_pages.shape:
+        raise ValueError(f"pages must be (num_pages, Hkv, {PAGE}, d)")
+    return num_pages, Hkv, d
+
+
+def fa_page_plan(ctx_lens, new_lens, free_pages, free_head, block_table, seq_lens, cu_new, slot_map, free_head_out,
+                 num_pages: int, stream=None) -> None:
+    """Block table and slot map of a step, from the requests' lengths (all int32 CUDA tensors).
+
+    ctx_lens, new_lens: (B), the tokens each request holds and adds; free_pages (any number of page numbers) and
+    free_head (1), how many of them are taken.  Updates block_table (B, max_pages) in place; writes seq_lens (B),
+    cu_new (B + 1), slot_map (max_tokens; -1 behind the last new token) and free_head_out (1).
+    """
+    if block_table.dim() != 2 or slot_map.dim() != 1 or free_pages.dim() != 1:
+        raise ValueError("block_table must be (B, max_pages), slot_map and free_pages one-dimensional")
+    B, max_pages = block_table.shape
+    _check_ints(ctx_lens=(ctx_lens, (B,)), new_lens=(new_lens, (B,)), free_pages=(free_pages, tuple(free_pages.shape)),
+                free_head=(free_head, (1,)), block_table=(block_table, (B, max_pages)), seq_lens=(seq_lens, (B,)),
+                cu_new=(cu_new, (B + 1,)), slot_map=(slot_map, tuple(slot_map.shape)),
+                free_head_out=(free_head_out, (1,)))
+    code = load_library().fa_page_plan(ctx_lens.data_ptr(), new_lens.data_ptr(), free_pages.data_ptr(),
+                                       free_head.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(),
+                                       cu_new.data_ptr(), slot_map.data_ptr(), free_head_out.data_ptr(), B, max_pages,
+                                       int(num_pages), free_pages.numel(), slot_map.numel(),
+                                       ctypes.c_void_p(_stream_handle(stream)))
+    if code:
+        raise FAError(code, "fa_page_plan")
+
+
+def page_plan(ctx_lens, new_lens, free_pages, free_head, block_table, max_tokens: int, num_pages: int, stream=None):
+    """Allocates and returns (seq_lens, cu_new, slot_map, free_head_out) of ``fa_page_plan``, which updates
+    ``block_table`` in place; ``max_tokens`` is the length of the slot map."""
+    import torch
+
+    B = ctx_lens.shape[0]
+    seq, cu, slots, head = (torch.empty(n, dtype=torch.int32, device=ctx_lens.device)
+                            for n in (B, B + 1, max_tokens, 1))
+    fa_page_plan(ctx_lens, new_lens, free_pages, free_head, block_table, seq, cu, slots, head, num_pages, stream)
+    return seq, cu, slots, head
+
+
+def fa_kv_append(k_new, v_new, slot_map, k_pages, v_pages, stream=None) -> None:
+    """Writes new keys and values (N, Hkv, d) bf16 into the page pools (num_pages, Hkv, 128, d) by slot_map (N) int32
+    (negative: skipped).  The heads of a token must be contiguous; tokens may be any multiple of 8 elements apart."""
+    import torch
+
+    num_pages, Hkv, d = _check_pools(k_pages, v_pages)
+    N = slot_map.shape[0] if slot_map.dim() == 1 else -1
+    for name, t in (("k_new", k_new), ("v_new", v_new)):
+        if t.dtype != torch.bfloat16 or tuple(t.shape) != (N, Hkv, d) or t.stride(2) != 1 or \
+                (Hkv > 1 and t.stride(1) != d):
+            raise ValueError(f"{name} must be a bf16 (N, Hkv, d) tensor with contiguous heads, like the pages and slot_map")
+    _check_ints(slot_map=(slot_map, (N,)))
+    code = load_library().fa_kv_append(k_new.data_ptr(), v_new.data_ptr(), slot_map.data_ptr(), k_pages.data_ptr(),
+                                       v_pages.data_ptr(), N, Hkv, d, k_new.stride(0), v_new.stride(0), num_pages,
+                                       ctypes.c_void_p(_stream_handle(stream)))
+    if code:
+        raise FAError(code, "fa_kv_append")
+
+
+def fa_fwd_prefix_paged_workspace_bytes(N: int, B: int, H: int, Hkv: int, d: int) -> int:
+    return int(load_library().fa_fwd_prefix_paged_workspace_bytes(N, B, H, Hkv, d))
+
+
+def fa_fwd_prefix_paged(q, k_pages, v_pages, prefix_table, prefix_len: int, block_table, seq_lens, cu_new,
+                        max_new: int, o, lse, causal: bool, scale: float, workspace=None, stream=None) -> None:
+    """New tokens' attention over a shared prefix and each request's own pages.
+
+    q, o: bf16 (N, H, d), request b's tokens at rows cu_new[b] .. cu_new[b + 1] - 1; k_pages, v_pages: bf16
+    (num_pages, Hkv, 128, d); prefix_table: int32, the pages of the ``prefix_len`` keys all requests share (None when
+    there are none); block_table (B, max_pages), seq_lens (B: own keys with the new ones) and cu_new (B + 1): int32;
+    ``max_new``: the largest number of new tokens of a request; lse: fp32 (N, H).  ``workspace``: a CUDA tensor of at
+    least ``fa_fwd_prefix_paged_workspace_bytes`` bytes (allocated here when None).
+    """
+    import torch
+
+    num_pages, Hkv, d = _check_pools(k_pages, v_pages)
+    for name, t in (("q", q), ("o", o)):
+        if t.dtype != torch.bfloat16 or t.dim() != 3 or t.shape[2] != d or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous bf16 (N, H, d) tensor")
+    if o.shape != q.shape:
+        raise ValueError("q and o must have the same shape")
+    N, H, _ = q.shape
+    if lse.dtype != torch.float32 or tuple(lse.shape) != (N, H) or not lse.is_contiguous():
+        raise ValueError("lse must be a contiguous fp32 (N, H) tensor")
+    if block_table.dim() != 2:
+        raise ValueError("block_table must be (B, max_pages)")
+    B, max_pages = block_table.shape
+    _check_ints(block_table=(block_table, (B, max_pages)), seq_lens=(seq_lens, (B,)), cu_new=(cu_new, (B + 1,)))
+    if prefix_table is not None:
+        _check_ints(prefix_table=(prefix_table, (prefix_table.numel(),)))
+    if prefix_len > 0 and (prefix_table is None or prefix_table.numel() * PAGE < prefix_len):
+        raise ValueError("prefix_table must hold ceil(prefix_len / 128) pages")
+    if workspace is None:
+        workspace = torch.empty(max(1, fa_fwd_prefix_paged_workspace_bytes(N, B, H, Hkv, d)), dtype=torch.uint8,
+                                device=q.device)
+    nbytes = workspace.numel() * workspace.element_size()
+    code = load_library().fa_fwd_prefix_paged(q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(),
+                                              prefix_table.data_ptr() if prefix_len > 0 else None,
+                                              block_table.data_ptr(), seq_lens.data_ptr(), cu_new.data_ptr(),
+                                              o.data_ptr(), lse.data_ptr(), N, B, H, Hkv, d, int(prefix_len),
+                                              int(max_new), int(bool(causal)), float(scale), num_pages, max_pages,
+                                              workspace.data_ptr(), nbytes, ctypes.c_void_p(_stream_handle(stream)))
+    if code:
+        raise FAError(code, "fa_fwd_prefix_paged")
+
+
+def attention_prefix_paged(q, k_pages, v_pages, prefix_table, prefix_len: int, block_table, seq_lens, cu_new,
+                           max_new: int, causal: bool = True, scale: float | None = None, stream=None):
+    """Allocates O, LSE and the workspace and runs ``fa_fwd_prefix_paged``; ``scale`` defaults to 1/sqrt(d).  Rows
+    behind the last request's come back as zeros with an LSE of -infinity."""
+    import torch
+
+    N, H, d = q.shape
+    if scale is None:
+        scale = 1.0 / math.sqrt(d)
+    o = torch.zeros_like(q)
+    lse = torch.full((N, H), float("-inf"), dtype=torch.float32, device=q.device)
+    fa_fwd_prefix_paged(q, k_pages, v_pages, prefix_table, prefix_len, block_table, seq_lens, cu_new, max_new, o, lse,
+                        causal, scale, None, stream)
+    return o, lse
 
 
 def fa_fwd_fp8_workspace_bytes(B: int, H: int, T: int, d: int) -> int:

@@ -13,6 +13,7 @@
 
 #include "fa.h"
 #include "fa_kernel.h"
+#include "fa_pages.h"
 
 namespace {
 
@@ -114,6 +115,26 @@ fa_status check_device_range(const void* p, size_t bytes, int dev) {
 bool overlaps(const void* a, size_t na, const void* b, size_t nb) {
   const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
   return x < y + nb && y < x + na;
+}
+
+struct Range {
+  const void* p;
+  size_t n;
+};
+
+// Every range is device memory of device `dev`, and no output overlaps an input or another output.
+fa_status check_ranges(const Range* ins, int num_ins, const Range* outs, int num_outs, int dev) {
+  fa_status st;
+  for (int i = 0; i < num_ins; ++i)
+    if ((st = check_device_range(ins[i].p, ins[i].n, dev)) != FA_OK) return st;
+  for (int a = 0; a < num_outs; ++a) {
+    if ((st = check_device_range(outs[a].p, outs[a].n, dev)) != FA_OK) return st;
+    for (int i = 0; i < num_ins; ++i)
+      if (overlaps(outs[a].p, outs[a].n, ins[i].p, ins[i].n)) return FA_ERR_ALIAS;
+    for (int b = 0; b < a; ++b)
+      if (overlaps(outs[a].p, outs[a].n, outs[b].p, outs[b].n)) return FA_ERR_ALIAS;
+  }
+  return FA_OK;
 }
 
 // Checks that need no device: pointers, sizes, head size, scale, mask flag, alignment.
@@ -715,6 +736,137 @@ fa_status fa_bwd(const void* q, const void* k, const void* v, const void* o, con
   return FA_OK;
 }
 
+fa_status fa_page_plan(const int* ctx_lens, const int* new_lens, const int* free_pages, const int* free_head,
+                       int* block_table, int* seq_lens, int* cu_new, int* slot_map, int* free_head_out, int B,
+                       int max_pages, int num_pages, int num_free, int max_tokens, cudaStream_t stream) {
+  if (!ctx_lens || !new_lens || !free_head || !block_table || !seq_lens || !cu_new || !slot_map || !free_head_out)
+    return FA_ERR_NULL_PTR;
+  if (B < 1 || max_pages < 1 || num_pages < 1 || num_free < 0 || max_tokens < 1) return FA_ERR_BAD_SHAPE;
+  if (num_free > 0 && !free_pages) return FA_ERR_NULL_PTR;
+  if (static_cast<long long>(B) * max_pages > INT_MAX / fa::kPage || num_pages > INT_MAX / fa::kPage)
+    return FA_ERR_BAD_SHAPE;
+  const Range ins[4] = {{ctx_lens, size_t(B) * 4}, {new_lens, size_t(B) * 4}, {free_head, 4},
+                        {free_pages, size_t(num_free) * 4}};
+  const Range outs[5] = {{block_table, size_t(B) * max_pages * 4}, {seq_lens, size_t(B) * 4},
+                         {cu_new, (size_t(B) + 1) * 4}, {slot_map, size_t(max_tokens) * 4}, {free_head_out, 4}};
+  for (const Range& r : ins)
+    if (reinterpret_cast<uintptr_t>(r.p) % 4 != 0) return FA_ERR_MISALIGNED;
+  for (const Range& r : outs)
+    if (reinterpret_cast<uintptr_t>(r.p) % 4 != 0) return FA_ERR_MISALIGNED;
+  int dev = 0, num_sms = 0;
+  fa_status st = current_device(&dev, &num_sms);
+  if (st != FA_OK) return st;
+  if ((st = check_ranges(ins, num_free > 0 ? 4 : 3, outs, 5, dev)) != FA_OK) return st;
+  const fa::PlanParams p{ctx_lens, new_lens, free_pages, free_head,     block_table, seq_lens,  cu_new,
+                         slot_map, free_head_out, B,    max_pages, num_pages, num_free, max_tokens};
+  if (fa::launch_page_plan(p, num_sms, stream) != cudaSuccess) {
+    cudaGetLastError();
+    return FA_ERR_LAUNCH;
+  }
+  return FA_OK;
+}
+
+fa_status fa_kv_append(const void* k_new, const void* v_new, const int* slot_map, void* k_pages, void* v_pages, int N,
+                       int Hkv, int d, long long k_stride, long long v_stride, int num_pages, cudaStream_t stream) {
+  if (!k_new || !v_new || !slot_map || !k_pages || !v_pages) return FA_ERR_NULL_PTR;
+  if (N < 1 || Hkv < 1 || num_pages < 1) return FA_ERR_BAD_SHAPE;
+  if (d != 64 && d != 128) return FA_ERR_UNSUPPORTED_HEAD_DIM;
+  const long long width = static_cast<long long>(Hkv) * d;
+  if (static_cast<long long>(num_pages) * Hkv >= INT_MAX || num_pages > INT_MAX / fa::kPage || width > INT_MAX ||
+      static_cast<long long>(N) > (1ll << 40) / width)
+    return FA_ERR_BAD_SHAPE;
+  for (const void* x : {k_new, v_new, static_cast<const void*>(k_pages), static_cast<const void*>(v_pages)})
+    if (reinterpret_cast<uintptr_t>(x) % 16 != 0) return FA_ERR_MISALIGNED;
+  if (reinterpret_cast<uintptr_t>(slot_map) % 4 != 0) return FA_ERR_MISALIGNED;
+  for (long long s : {k_stride, v_stride})
+    if (N > 1) {
+      if (s % 8 != 0) return FA_ERR_MISALIGNED;
+      if (s < width || s > (1ll << 40)) return FA_ERR_BAD_SHAPE;
+    }
+  if (N == 1) k_stride = v_stride = width;
+  int dev = 0, num_sms = 0;
+  fa_status st = current_device(&dev, &num_sms);
+  if (st != FA_OK) return st;
+  const size_t pool = static_cast<size_t>(num_pages) * fa::kPage * width * 2;
+  const Range ins[3] = {{k_new, (static_cast<size_t>(N - 1) * k_stride + width) * 2},
+                        {v_new, (static_cast<size_t>(N - 1) * v_stride + width) * 2}, {slot_map, size_t(N) * 4}};
+  const Range outs[2] = {{k_pages, pool}, {v_pages, pool}};
+  if ((st = check_ranges(ins, 3, outs, 2, dev)) != FA_OK) return st;
+  const fa::AppendParams p{static_cast<const __nv_bfloat16*>(k_new), static_cast<const __nv_bfloat16*>(v_new), slot_map,
+                           static_cast<__nv_bfloat16*>(k_pages), static_cast<__nv_bfloat16*>(v_pages), k_stride,
+                           v_stride, N, Hkv, d, num_pages};
+  if (fa::launch_kv_append(p, num_sms, stream) != cudaSuccess) {
+    cudaGetLastError();
+    return FA_ERR_LAUNCH;
+  }
+  return FA_OK;
+}
+
+size_t fa_fwd_prefix_paged_workspace_bytes(int N, int B, int H, int Hkv, int d) {
+  if (N < 1 || B < 1 || H < 1 || Hkv < 1 || H % Hkv != 0 || (d != 64 && d != 128)) return 0;
+  return 256;
+}
+
+fa_status fa_fwd_prefix_paged(const void* q, const void* k_pages, const void* v_pages, const int* prefix_table,
+                              const int* block_table, const int* seq_lens, const int* cu_new, void* o, float* lse,
+                              int N, int B, int H, int Hkv, int d, int prefix_len, int max_new, int causal,
+                              float scale, int num_pages, int max_pages, void* workspace, size_t workspace_bytes,
+                              cudaStream_t stream) {
+  if (!q || !k_pages || !v_pages || !block_table || !seq_lens || !cu_new || !o || !lse) return FA_ERR_NULL_PTR;
+  if (prefix_len > 0 && !prefix_table) return FA_ERR_NULL_PTR;
+  if (N < 1 || B < 1 || H < 1 || Hkv < 1 || H % Hkv != 0 || H / Hkv > 128 || prefix_len < 0 || max_new < 1 ||
+      num_pages < 1 || max_pages < 1)
+    return FA_ERR_BAD_SHAPE;
+  if (static_cast<long long>(N) * H > INT_MAX || static_cast<long long>(num_pages) * Hkv >= INT_MAX ||
+      num_pages > INT_MAX / fa::kPage || max_pages > INT_MAX / fa::kPage || prefix_len > (1 << 30))
+    return FA_ERR_BAD_SHAPE;
+  if (d != 64 && d != 128) return FA_ERR_UNSUPPORTED_HEAD_DIM;
+  if (!std::isfinite(scale) || !(scale > 0.f)) return FA_ERR_BAD_SCALE;
+  if (causal != 0 && causal != 1) return FA_ERR_BAD_ARG;
+  for (const void* x : {q, k_pages, v_pages, static_cast<const void*>(o), static_cast<const void*>(lse)})
+    if (reinterpret_cast<uintptr_t>(x) % 16 != 0) return FA_ERR_MISALIGNED;
+  for (const int* x : {prefix_table, block_table, seq_lens, cu_new})
+    if (reinterpret_cast<uintptr_t>(x) % 4 != 0) return FA_ERR_MISALIGNED;
+  const size_t need = fa_fwd_prefix_paged_workspace_bytes(N, B, H, Hkv, d);
+  if (!workspace || workspace_bytes < need) return FA_ERR_WORKSPACE;
+  if (reinterpret_cast<uintptr_t>(workspace) % 16 != 0) return FA_ERR_MISALIGNED;
+  int dev = 0, num_sms = 0;
+  fa_status st = current_device(&dev, &num_sms);
+  if (st != FA_OK) return st;
+  const size_t q_bytes = static_cast<size_t>(N) * H * d * 2, lse_bytes = static_cast<size_t>(N) * H * 4;
+  const size_t pool = static_cast<size_t>(num_pages) * Hkv * fa::kPage * d * 2;
+  const size_t prefix_pages = (static_cast<size_t>(prefix_len) + fa::kPage - 1) / fa::kPage;
+  const Range ins[7] = {{q, q_bytes}, {k_pages, pool}, {v_pages, pool}, {block_table, size_t(B) * max_pages * 4},
+                        {seq_lens, size_t(B) * 4}, {cu_new, (size_t(B) + 1) * 4}, {prefix_table, prefix_pages * 4}};
+  const Range outs[3] = {{o, q_bytes}, {lse, lse_bytes}, {workspace, need}};
+  if ((st = check_ranges(ins, prefix_len > 0 ? 7 : 6, outs, 3, dev)) != FA_OK) return st;
+  fa::PrefixParams p{};
+  p.q = static_cast<const __nv_bfloat16*>(q);
+  p.k_pages = static_cast<const __nv_bfloat16*>(k_pages);
+  p.v_pages = static_cast<const __nv_bfloat16*>(v_pages);
+  p.prefix_table = prefix_table;
+  p.block_table = block_table;
+  p.seq_lens = seq_lens;
+  p.cu_new = cu_new;
+  p.o = static_cast<__nv_bfloat16*>(o);
+  p.lse = lse;
+  p.N = N;
+  p.B = B;
+  p.H = H;
+  p.Hkv = Hkv;
+  p.group = H / Hkv;
+  p.prefix_len = prefix_len;
+  p.causal = causal;
+  p.num_pages = num_pages;
+  p.max_pages = max_pages;
+  p.scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634074);
+  if (fa::launch_fa_fwd_prefix(d, p, stream) != cudaSuccess) {
+    cudaGetLastError();
+    return FA_ERR_LAUNCH;
+  }
+  return FA_OK;
+}
+
 static_assert(FA_NOALLOC_SCRATCH_BYTES == fa::kNoAllocScratchBytes, "fa.h and the kernel disagree on the scratch size");
 
 const char* fa_status_string(fa_status s) {
@@ -733,6 +885,8 @@ const char* fa_status_string(fa_status s) {
     case FA_ERR_ALIAS: return "an output overlaps an input or the other output";
     case FA_ERR_CUDA: return "a CUDA runtime or driver call failed";
     case FA_ERR_BAD_PAGE: return "a block-table entry named a page outside the pool (its keys read as zeros)";
+    case FA_ERR_BAD_LENGTH: return "a request length was negative or did not fit its block table or the batch";
+    case FA_ERR_NO_PAGES: return "the list of free pages ran out";
     case FA_ERR_WORKSPACE: return "the workspace is missing or smaller than the size its *_workspace_bytes() gives";
   }
   return "unknown status";
@@ -740,14 +894,20 @@ const char* fa_status_string(fa_status s) {
 
 fa_status fa_device_status(cudaStream_t stream, int* out) {
   if (!out) return FA_ERR_NULL_PTR;
-  unsigned int word = 0, bwd = 0;
+  unsigned int word = 0, bwd = 0, pages = 0, prefix = 0;
   if (fa::read_and_clear_status(stream, &word) != cudaSuccess ||
-      fa::read_and_clear_bwd_status(stream, &bwd) != cudaSuccess) {
+      fa::read_and_clear_bwd_status(stream, &bwd) != cudaSuccess ||
+      fa::read_and_clear_pages_status(stream, &pages) != cudaSuccess ||
+      fa::read_and_clear_prefix_status(stream, &prefix) != cudaSuccess) {
     cudaGetLastError();
     return FA_ERR_CUDA;
   }
-  word |= bwd;
-  *out = (word & 2u) ? FA_ERR_BAD_PAGE : (word & 1u) ? FA_ERR_DEVICE_TIMEOUT : FA_OK;
+  word |= bwd | pages | prefix;
+  *out = (word & fa::kStatusBadPage)     ? FA_ERR_BAD_PAGE
+         : (word & fa::kStatusTimeout)   ? FA_ERR_DEVICE_TIMEOUT
+         : (word & fa::kStatusNoPages)   ? FA_ERR_NO_PAGES
+         : (word & fa::kStatusBadLength) ? FA_ERR_BAD_LENGTH
+                                         : FA_OK;
   return FA_OK;
 }
 

@@ -70,7 +70,9 @@ typedef enum {
   FA_ERR_ALIAS = 11,                /* O or LSE overlaps an input or each other */
   FA_ERR_CUDA = 12,                 /* a CUDA runtime or driver query failed */
   FA_ERR_WORKSPACE = 13,            /* a workspace is missing or smaller than its *_workspace_bytes() */
-  FA_ERR_BAD_PAGE = 14              /* (device) a block-table entry was outside the page pool */
+  FA_ERR_BAD_PAGE = 14,             /* (device) a block-table entry was outside the page pool */
+  FA_ERR_BAD_LENGTH = 15,           /* (device) a request length was negative or did not fit its table or batch */
+  FA_ERR_NO_PAGES = 16              /* (device) the list of free pages ran out */
 } fa_status;
 
 /* Largest number of key splits fa_fwd_splitkv accepts. */
@@ -289,14 +291,126 @@ size_t fa_fwd_splitkv_workspace_bytes(int B, int H, int T, int d, int num_splits
  */
 int fa_fwd_splitkv_count(int B, int H, int T, int d, int causal, int num_splits);
 
+/*
+ * ---- One step of a paged cache: plan, append, attend ----
+ *
+ * Three calls that take a batch of requests one step further: fa_page_plan gives
+ * the new tokens of every request their places in the page pool, fa_kv_append
+ * writes their keys and values there, fa_fwd_prefix_paged attends.  All lengths
+ * are device memory, so that the calls can be captured into a CUDA graph once and
+ * replayed while the requests grow.  Pages hold 128 keys and are laid out as for
+ * fa_fwd_paged; a slot is 128 * page + row.  (Sources: "FlashAttention and Fused
+ * Kernels: Attention Without the n x n Matrix", sections "Paged caches" and
+ * "Flash-Decoding: split the cache, not the queries".  The plan, the append and
+ * the shared prefix are additions; the pages only name the block table.)
+ *
+ * The new tokens of all requests stand one behind the other: request b's are
+ * rows cu_new[b] .. cu_new[b + 1] - 1 of the batch.
+ */
+
+/*
+ * Block tables and slot maps from request lengths.
+ *   ctx_lens      : (B) int32, tokens each request already holds in its own pages.
+ *   new_lens      : (B) int32, tokens it adds now (0 allowed).
+ *   free_pages    : (num_free) int32, page numbers that may be taken, in this order
+ *                   (may be NULL when num_free is 0).
+ *   free_head     : (1) int32, how many of them earlier steps have taken.
+ *   block_table   : (B, max_pages) int32, updated: entries below ceil(ctx / 128)
+ *                   are kept, the entries that the new tokens need beyond them are
+ *                   taken from the free list, request by request; the rest is left
+ *                   as it was.
+ *   seq_lens      : (B) int32, written: ctx + new.
+ *   cu_new        : (B + 1) int32, written: the running sum of the new lengths, from 0.
+ *   slot_map      : (max_tokens) int32, written: the slot of every new token; -1 behind
+ *                   the last one.
+ *   free_head_out : (1) int32, written: free_head plus the pages taken.
+ *   num_pages     : pages of the pool (block-table entries are checked against it).
+ * One kernel.  Device errors (fa_device_status): FA_ERR_BAD_LENGTH for a length that
+ * is negative or does not fit max_pages pages (that request adds no token) and for
+ * more than max_tokens new tokens (those beyond get no slot); FA_ERR_NO_PAGES when
+ * the list runs out, FA_ERR_BAD_PAGE for a page outside the pool (in both, the tokens
+ * of that page get slot -1; the entry of a new page becomes -1).
+ * Errors: FA_ERR_NULL_PTR, FA_ERR_MISALIGNED (4 bytes), FA_ERR_BAD_POINTER,
+ * FA_ERR_ALIAS (an output overlaps an input or another output), FA_ERR_BAD_SHAPE for
+ * B, max_pages, max_tokens or num_pages < 1, num_free < 0, B * max_pages * 128 or
+ * num_pages * 128 above 2^31 - 1.
+ */
+fa_status fa_page_plan(const int* ctx_lens, const int* new_lens, const int* free_pages, const int* free_head,
+                       int* block_table, int* seq_lens, int* cu_new, int* slot_map, int* free_head_out,
+                       int B, int max_pages, int num_pages, int num_free, int max_tokens, cudaStream_t stream);
+
+/*
+ * Writes new keys and values into the page pools.
+ *   k_new, v_new : bf16, row t at k_new + t * k_stride: Hkv heads of d values,
+ *                  contiguous (so both may be columns of one projection's output).
+ *   k_stride,
+ *   v_stride     : elements from one token to the next, a multiple of 8; at least Hkv * d
+ *                  (any value when N is 1).
+ *   slot_map     : (N) int32, the slot of every token; a negative one skips the token.
+ *                  A slot past the pool skips it too and sets FA_ERR_BAD_PAGE in the
+ *                  device status word.  Slots >= 0 must differ from each other (a plan's
+ *                  do); of two tokens with one slot, each 16 bytes of the row hold one's.
+ *   k_pages,
+ *   v_pages      : (num_pages, Hkv, 128, d) bf16; only the rows of the slots are written.
+ *   N, Hkv       : tokens and K/V heads, >= 1; d: 64 or 128.
+ * One kernel.  Errors: as fa_fwd_paged for the shared arguments; FA_ERR_MISALIGNED also
+ * for a stride that is not a multiple of 8; FA_ERR_BAD_SHAPE also for a stride that is
+ * too small; FA_ERR_ALIAS when a pool overlaps an input or the other pool.
+ */
+fa_status fa_kv_append(const void* k_new, const void* v_new, const int* slot_map, void* k_pages, void* v_pages,
+                       int N, int Hkv, int d, long long k_stride, long long v_stride, int num_pages,
+                       cudaStream_t stream);
+
+/*
+ * Attention of new tokens over a prefix that all requests share and over each
+ * request's own keys, both in pages of one pool.  Row (n, h) of the batch, token i
+ * of request b, sees the prefix's prefix_len keys and of its own seq_lens[b] keys
+ * all (causal = 0) or those up to its own place, key seq_lens[b] - new_b + i
+ * (causal = 1; new_b = cu_new[b + 1] - cu_new[b]; the new tokens are the last of
+ * the own keys).  The prefix's keys are read once for all rows that share a K/V head,
+ * not once per request.
+ *   q, o         : (N, H, d) bf16; d 64 or 128.
+ *   lse          : (N, H) fp32, natural log.  A row that sees no key gets O = 0 and
+ *                  LSE = -infinity.  Rows from cu_new[B] on are left as they were.
+ *   k_pages,
+ *   v_pages      : (num_pages, Hkv, 128, d) bf16, as for fa_fwd_paged, but rows past
+ *                  the end of a sequence may hold anything (infinities and NaN too).
+ *   prefix_table : (ceil(prefix_len / 128)) int32, the prefix's pages (may be NULL when
+ *                  prefix_len is 0).  prefix_len >= 0 need not be a multiple of 128.
+ *   block_table  : (B, max_pages) int32; entries 0 .. ceil(seq_lens[b] / 128) - 1 are read.
+ *   seq_lens     : (B) int32, own keys with the new ones; 0 allowed.
+ *   cu_new       : (B + 1) int32, from 0, not decreasing, at most N.
+ *   max_new      : the largest number of new tokens of a request, >= 1; it only chooses
+ *                  tile shapes (a request with more is worked correctly, in more tiles).
+ *   Hkv          : divides H, with H / Hkv <= 128.
+ *   workspace    : device memory of at least fa_fwd_prefix_paged_workspace_bytes(N, B, H,
+ *                  Hkv, d) bytes, 16-byte aligned; nothing in it needs to be set.  Calls
+ *                  that may run at the same time need workspaces of their own.
+ * Device errors (fa_device_status): FA_ERR_BAD_PAGE for a page outside the pool (it reads
+ * as zeros), FA_ERR_BAD_LENGTH for a length outside the table or the batch (cut to fit).
+ * The result does not depend on scheduling: equal calls give equal bits.
+ * Errors: as fa_fwd_paged for the shared arguments; FA_ERR_WORKSPACE; FA_ERR_BAD_SHAPE also
+ * for N, B, max_pages or max_new < 1, prefix_len < 0, H / Hkv > 128, and sizes whose key
+ * tiles cannot be counted in 31 bits.
+ */
+fa_status fa_fwd_prefix_paged(const void* q, const void* k_pages, const void* v_pages, const int* prefix_table,
+                              const int* block_table, const int* seq_lens, const int* cu_new, void* o, float* lse,
+                              int N, int B, int H, int Hkv, int d, int prefix_len, int max_new, int causal,
+                              float scale, int num_pages, int max_pages, void* workspace, size_t workspace_bytes,
+                              cudaStream_t stream);
+
+/* Workspace fa_fwd_prefix_paged needs; 0 for sizes out of range. */
+size_t fa_fwd_prefix_paged_workspace_bytes(int N, int B, int H, int Hkv, int d);
+
 /* A static, human-readable name for a status code. */
 const char* fa_status_string(fa_status s);
 
 /*
  * Reads and clears the device status word that kernels of this library set
  * when a bounded wait runs out.  Synchronises `stream` first.  *out receives
- * FA_OK, FA_ERR_DEVICE_TIMEOUT or FA_ERR_BAD_PAGE (fa_fwd_paged met a page
- * outside its pool; reported first).  Returns FA_ERR_CUDA if the copy fails.
+ * FA_OK, or of what was recorded the first of FA_ERR_BAD_PAGE (a page outside its
+ * pool), FA_ERR_DEVICE_TIMEOUT, FA_ERR_NO_PAGES and FA_ERR_BAD_LENGTH.  Returns
+ * FA_ERR_CUDA if the copy fails.
  */
 fa_status fa_device_status(cudaStream_t stream, int* out);
 
