@@ -157,16 +157,18 @@ fa_status validate_host(const void* q, const void* k, const void* v, const void*
 // 3-D view (inner, rows, B*H) of a contiguous tensor: a box (box_bytes of the inner
 // dimension x box_rows rows x 1) never crosses from one head into the next, rows past
 // `rows` read as zeros and are not written.  bf16 (d, T, B*H) views, or byte views for
-// e4m3 tensors.  128-byte boxes use the 128-byte swizzle, narrower ones none.
+// e4m3 tensors.  128-byte boxes use the 128-byte swizzle, narrower ones none.  box_planes:
+// planes of the outermost dimension a box spans.
 bool encode_tensor_map(CUtensorMap* map, const void* base, int BH, int rows, int inner, bool bytes, int box_rows,
-                       int box_bytes) {
+                       int box_bytes, int box_planes = 1) {
   const DriverFns& fns = driver_fns();
   if (!fns.encode_tiled) return false;
   const cuuint64_t es = bytes ? 1 : 2;
   const cuuint64_t dims[3] = {static_cast<cuuint64_t>(inner), static_cast<cuuint64_t>(rows),
                               static_cast<cuuint64_t>(BH)};
   const cuuint64_t strides[2] = {static_cast<cuuint64_t>(inner) * es, static_cast<cuuint64_t>(rows) * inner * es};
-  const cuuint32_t box[3] = {static_cast<cuuint32_t>(box_bytes / es), static_cast<cuuint32_t>(box_rows), 1};
+  const cuuint32_t box[3] = {static_cast<cuuint32_t>(box_bytes / es), static_cast<cuuint32_t>(box_rows),
+                              static_cast<cuuint32_t>(box_planes)};
   const cuuint32_t elem_strides[3] = {1, 1, 1};
   return fns.encode_tiled(map, bytes ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
                           const_cast<void*>(base), dims, strides, box, elem_strides, CU_TENSOR_MAP_INTERLEAVE_NONE,
@@ -438,6 +440,37 @@ fa_status launch_splitkv(Prepared& pr, int d, int num_splits, float* ws, cudaStr
   }
   return FA_OK;
 }
+
+// Workspace of fa_fwd_prefix_paged: byte offsets of its parts (each a multiple of 256).
+struct PrefixWorkspace {
+  size_t cum, tok, slab_o, slab_lse, own_o, own_lse, prefix_o, prefix_lse, bytes;
+  int slab_rows;
+};
+
+PrefixWorkspace prefix_workspace(int N, int B, int H, int Hkv, int d) {
+  PrefixWorkspace w{};
+  size_t at = 1024;  // the header words and the first request of every SM (64 + kPrefixMaxCtas words)
+  auto take = [&at](size_t bytes) {
+    const size_t here = at;
+    at += (bytes + 255) / 256 * 256;
+    return here;
+  };
+  const size_t rows = static_cast<size_t>(N) * H;
+  const long long item = (static_cast<long long>(N) * (H / Hkv) + 31) / 32 * 32;  // rows an item can have
+  w.slab_rows = static_cast<int>(std::min<long long>(256, item));
+  const size_t slabs = static_cast<size_t>(fa::kPrefixMaxCtas) * 2 * w.slab_rows;
+  w.cum = take(static_cast<size_t>(B) * 4);
+  w.tok = take(static_cast<size_t>(N) * 16);
+  w.slab_o = take(slabs * d * 4);
+  w.slab_lse = take(slabs * 4);
+  w.own_o = take(rows * d * 4);
+  w.own_lse = take(rows * 4);
+  w.prefix_o = take(rows * d * 4);
+  w.prefix_lse = take(rows * 4);
+  w.bytes = at;
+  return w;
+}
+static_assert(1024 >= (64 + fa::kPrefixMaxCtas) * 4, "workspace header");
 
 }  // namespace
 
@@ -804,7 +837,7 @@ fa_status fa_kv_append(const void* k_new, const void* v_new, const int* slot_map
 
 size_t fa_fwd_prefix_paged_workspace_bytes(int N, int B, int H, int Hkv, int d) {
   if (N < 1 || B < 1 || H < 1 || Hkv < 1 || H % Hkv != 0 || (d != 64 && d != 128)) return 0;
-  return 256;
+  return prefix_workspace(N, B, H, Hkv, d).bytes;
 }
 
 fa_status fa_fwd_prefix_paged(const void* q, const void* k_pages, const void* v_pages, const int* prefix_table,
@@ -821,6 +854,13 @@ fa_status fa_fwd_prefix_paged(const void* q, const void* k_pages, const void* v_
       num_pages > INT_MAX / fa::kPage || max_pages > INT_MAX / fa::kPage || prefix_len > (1 << 30))
     return FA_ERR_BAD_SHAPE;
   if (d != 64 && d != 128) return FA_ERR_UNSUPPORTED_HEAD_DIM;
+  // tokens of a 128-row tile, and the most places the work can take on the line that the SMs share
+  const int full = 128 / (H / Hkv), tp = std::min(full, N), ts = std::min(full, max_new);
+  const double places =
+      static_cast<double>(Hkv) *
+      ((N / (2 * tp) + 1.0) * (fa::prefix_item_cost() + fa::prefix_tile_cost() * (prefix_len / fa::kPage + 1.0)) +
+       (N / (2 * ts) + static_cast<double>(B)) * (fa::prefix_item_cost() + fa::prefix_tile_cost() * static_cast<double>(max_pages)));
+  if (places > INT_MAX) return FA_ERR_BAD_SHAPE;
   if (!std::isfinite(scale) || !(scale > 0.f)) return FA_ERR_BAD_SCALE;
   if (causal != 0 && causal != 1) return FA_ERR_BAD_ARG;
   for (const void* x : {q, k_pages, v_pages, static_cast<const void*>(o), static_cast<const void*>(lse)})
@@ -841,9 +881,6 @@ fa_status fa_fwd_prefix_paged(const void* q, const void* k_pages, const void* v_
   const Range outs[3] = {{o, q_bytes}, {lse, lse_bytes}, {workspace, need}};
   if ((st = check_ranges(ins, prefix_len > 0 ? 7 : 6, outs, 3, dev)) != FA_OK) return st;
   fa::PrefixParams p{};
-  p.q = static_cast<const __nv_bfloat16*>(q);
-  p.k_pages = static_cast<const __nv_bfloat16*>(k_pages);
-  p.v_pages = static_cast<const __nv_bfloat16*>(v_pages);
   p.prefix_table = prefix_table;
   p.block_table = block_table;
   p.seq_lens = seq_lens;
@@ -860,7 +897,31 @@ fa_status fa_fwd_prefix_paged(const void* q, const void* k_pages, const void* v_
   p.num_pages = num_pages;
   p.max_pages = max_pages;
   p.scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634074);
-  if (fa::launch_fa_fwd_prefix(d, p, stream) != cudaSuccess) {
+  p.timeout_ns = kWaitLimitNs;
+  p.ctas = std::min(num_sms, fa::kPrefixMaxCtas);
+  p.tiles_p = static_cast<int>(prefix_pages);
+  p.tp = tp;
+  p.ts = ts;
+  const PrefixWorkspace w = prefix_workspace(N, B, H, Hkv, d);
+  char* base = static_cast<char*>(workspace);
+  p.hdr = reinterpret_cast<int*>(base);
+  p.start = p.hdr + 64;
+  p.cum = reinterpret_cast<unsigned int*>(base + w.cum);
+  p.tok = reinterpret_cast<int4*>(base + w.tok);
+  p.slab_rows = w.slab_rows;
+  p.slab_o = reinterpret_cast<float4*>(base + w.slab_o);
+  p.slab_lse = reinterpret_cast<float*>(base + w.slab_lse);
+  p.own_o = reinterpret_cast<float4*>(base + w.own_o);
+  p.own_lse = reinterpret_cast<float*>(base + w.own_lse);
+  p.prefix_o = reinterpret_cast<float4*>(base + w.prefix_o);
+  p.prefix_lse = reinterpret_cast<float*>(base + w.prefix_lse);
+  CUtensorMap tqp, tqs, tk, tv;
+  if (!encode_tensor_map(&tqp, q, N, H, d, false, p.group, 128, p.tp) ||
+      !encode_tensor_map(&tqs, q, N, H, d, false, p.group, 128, p.ts) ||
+      !encode_tensor_map(&tk, k_pages, num_pages * Hkv, fa::kPage, d, false, fa::kPage, 128) ||
+      !encode_tensor_map(&tv, v_pages, num_pages * Hkv, fa::kPage, d, false, fa::kPage, 128))
+    return FA_ERR_CUDA;
+  if (fa::launch_fa_fwd_prefix(d, tqp, tqs, tk, tv, p, stream) != cudaSuccess) {
     cudaGetLastError();
     return FA_ERR_LAUNCH;
   }

@@ -40,9 +40,6 @@ cudaError_t launch_kv_append(const AppendParams& p, int num_sms, cudaStream_t st
 cudaError_t read_and_clear_pages_status(cudaStream_t stream, unsigned int* out);
 
 struct PrefixParams {
-  const __nv_bfloat16* q;
-  const __nv_bfloat16* k_pages;
-  const __nv_bfloat16* v_pages;
   const int* prefix_table;
   const int* block_table;
   const int* seq_lens;
@@ -52,9 +49,31 @@ struct PrefixParams {
   int N, B, H, Hkv, group;
   int prefix_len, causal;
   int num_pages, max_pages;
-  float scale_log2;  // scale * log2(e)
+  float scale_log2;               // scale * log2(e)
+  unsigned long long timeout_ns;  // bound on every in-kernel wait
+  int ctas;     // blocks of the attention kernel: one per SM, at most kPrefixMaxCtas
+  int tiles_p;  // 128-key tiles of the prefix
+  int tp, ts;   // tokens of a 128-row tile over the prefix / over own keys
+  // workspace
+  int* hdr;             // kHdr* words
+  int* start;           // [ctas] the request a block's own keys begin with
+  unsigned int* cum;    // [B] place of the request's first item
+  int4* tok;            // [N] place of the token's own item (K/V head 0), its tiles, the tiles the token's row
+                        // tile sees, the token's number within the item
+  int slab_rows;        // rows of a slab
+  float4* slab_o;       // [ctas][2][d / 4][slab_rows] parts of cut items, four columns each
+  float* slab_lse;      // [ctas][2][slab_rows], base-2
+  float4* own_o;        // [Hkv][d / 4][N * group] parts of whole items of own keys
+  float* own_lse;       // [Hkv][N * group]
+  float4* prefix_o;     // the same of the prefix
+  float* prefix_lse;
 };
-cudaError_t launch_fa_fwd_prefix(int d, const PrefixParams& p, cudaStream_t stream);
+constexpr int kPrefixMaxCtas = 160;
+unsigned int prefix_tile_cost();  // places a key tile and an item take (see fa_prefix.cu)
+unsigned int prefix_item_cost();
+// qp, qs: bf16 (d, H, N) with boxes of 64 columns x group heads x tp / ts tokens; k, v: the page pools.
+cudaError_t launch_fa_fwd_prefix(int d, const CUtensorMap& qp, const CUtensorMap& qs, const CUtensorMap& k,
+                                 const CUtensorMap& v, const PrefixParams& p, cudaStream_t stream);
 cudaError_t read_and_clear_prefix_status(cudaStream_t stream, unsigned int* out);
 
 }  // namespace fa
