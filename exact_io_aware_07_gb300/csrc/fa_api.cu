@@ -177,6 +177,21 @@ bool encode_tensor_map(CUtensorMap* map, const void* base, int BH, int rows, int
                           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// A page pool (num_pages, Hkv, 128, d) as (64, 128, d / 64, num_pages * Hkv): a box holds `box_rows` keys of one page
+// and head, their 64-column halves one behind the other, in the 128-byte swizzle.
+bool encode_page_map(CUtensorMap* map, const void* base, int planes, int d, int box_rows) {
+  const DriverFns& fns = driver_fns();
+  if (!fns.encode_tiled) return false;
+  const cuuint64_t row = static_cast<cuuint64_t>(d) * 2;
+  const cuuint64_t dims[4] = {64, fa::kPage, static_cast<cuuint64_t>(d / 64), static_cast<cuuint64_t>(planes)};
+  const cuuint64_t strides[3] = {row, 128, row * fa::kPage};
+  const cuuint32_t box[4] = {64, static_cast<cuuint32_t>(box_rows), static_cast<cuuint32_t>(d / 64), 1};
+  const cuuint32_t elem_strides[4] = {1, 1, 1, 1};
+  return fns.encode_tiled(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides, box,
+                          elem_strides, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                          CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // Encoded descriptors, reused when the same tensor comes back (encoding reads no
 // memory, so a cached descriptor is exactly what encoding again would give).
 struct MapCacheEntry {
@@ -449,7 +464,7 @@ struct PrefixWorkspace {
 
 PrefixWorkspace prefix_workspace(int N, int B, int H, int Hkv, int d) {
   PrefixWorkspace w{};
-  size_t at = 1024;  // the header words and the first request of every SM (64 + kPrefixMaxCtas words)
+  size_t at = 6144;  // the header words and the first request of every worker
   auto take = [&at](size_t bytes) {
     const size_t here = at;
     at += (bytes + 255) / 256 * 256;
@@ -458,8 +473,9 @@ PrefixWorkspace prefix_workspace(int N, int B, int H, int Hkv, int d) {
   const size_t rows = static_cast<size_t>(N) * H;
   const long long item = (static_cast<long long>(N) * (H / Hkv) + 31) / 32 * 32;  // rows an item can have
   w.slab_rows = static_cast<int>(std::min<long long>(256, item));
-  const size_t slabs = static_cast<size_t>(fa::kPrefixMaxCtas) * 2 * w.slab_rows;
-  w.cum = take(static_cast<size_t>(B) * 4);
+  // rows of the slabs of cut items: two per many-row worker (block), two of 128 / 8, / 4 or / 2 rows per team
+  const size_t slabs = static_cast<size_t>(fa::kPrefixMaxCtas) * 2 * (w.slab_rows + 128);
+  w.cum = take(static_cast<size_t>(B) * 8);
   w.tok = take(static_cast<size_t>(N) * 16);
   w.slab_o = take(slabs * d * 4);
   w.slab_lse = take(slabs * 4);
@@ -470,7 +486,7 @@ PrefixWorkspace prefix_workspace(int N, int B, int H, int Hkv, int d) {
   w.bytes = at;
   return w;
 }
-static_assert(1024 >= (64 + fa::kPrefixMaxCtas) * 4, "workspace header");
+static_assert(6144 >= (64 + fa::kPrefixMaxCtas * (1 + 8)) * 4, "workspace header");
 
 }  // namespace
 
@@ -854,12 +870,11 @@ fa_status fa_fwd_prefix_paged(const void* q, const void* k_pages, const void* v_
       num_pages > INT_MAX / fa::kPage || max_pages > INT_MAX / fa::kPage || prefix_len > (1 << 30))
     return FA_ERR_BAD_SHAPE;
   if (d != 64 && d != 128) return FA_ERR_UNSUPPORTED_HEAD_DIM;
-  // tokens of a 128-row tile, and the most places the work can take on the line that the SMs share
-  const int full = 128 / (H / Hkv), tp = std::min(full, N), ts = std::min(full, max_new);
-  const double places =
-      static_cast<double>(Hkv) *
-      ((N / (2 * tp) + 1.0) * (fa::prefix_item_cost() + fa::prefix_tile_cost() * (prefix_len / fa::kPage + 1.0)) +
-       (N / (2 * ts) + static_cast<double>(B)) * (fa::prefix_item_cost() + fa::prefix_tile_cost() * static_cast<double>(max_pages)));
+  // tokens of a 128-row tile; the most places the work can take on the lines that the SMs share
+  const int group = H / Hkv, tp = std::min(128 / group, N);
+  const double page = fa::prefix_page_cost(), item = fa::prefix_item_cost();
+  const double places = static_cast<double>(Hkv) * ((N / (2 * tp) + 1.0) * (item + page * (prefix_len / fa::kPage + 1.0)) +
+                                                    (N / (2 * tp) + static_cast<double>(B)) * (item + page * max_pages));
   if (places > INT_MAX) return FA_ERR_BAD_SHAPE;
   if (!std::isfinite(scale) || !(scale > 0.f)) return FA_ERR_BAD_SCALE;
   if (causal != 0 && causal != 1) return FA_ERR_BAD_ARG;
@@ -881,6 +896,7 @@ fa_status fa_fwd_prefix_paged(const void* q, const void* k_pages, const void* v_
   const Range outs[3] = {{o, q_bytes}, {lse, lse_bytes}, {workspace, need}};
   if ((st = check_ranges(ins, prefix_len > 0 ? 7 : 6, outs, 3, dev)) != FA_OK) return st;
   fa::PrefixParams p{};
+  p.q = static_cast<const __nv_bfloat16*>(q);
   p.prefix_table = prefix_table;
   p.block_table = block_table;
   p.seq_lens = seq_lens;
@@ -891,7 +907,7 @@ fa_status fa_fwd_prefix_paged(const void* q, const void* k_pages, const void* v_
   p.B = B;
   p.H = H;
   p.Hkv = Hkv;
-  p.group = H / Hkv;
+  p.group = group;
   p.prefix_len = prefix_len;
   p.causal = causal;
   p.num_pages = num_pages;
@@ -899,9 +915,13 @@ fa_status fa_fwd_prefix_paged(const void* q, const void* k_pages, const void* v_
   p.scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634074);
   p.timeout_ns = kWaitLimitNs;
   p.ctas = std::min(num_sms, fa::kPrefixMaxCtas);
+  // rows of the few-row items: the fewest that hold a request of max_new tokens; when that is more than 64 rows
+  // (prompt chunks), a decoding request
+  const long long most = static_cast<long long>(std::min(max_new, N)) * group, rows = most <= 64 ? most : group;
+  p.few_rows = rows <= 8 || rows > 64 ? 8 : rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
+  p.teams = p.few_rows <= 16 ? 8 : p.few_rows == 32 ? 4 : 2;
   p.tiles_p = static_cast<int>(prefix_pages);
   p.tp = tp;
-  p.ts = ts;
   const PrefixWorkspace w = prefix_workspace(N, B, H, Hkv, d);
   char* base = static_cast<char*>(workspace);
   p.hdr = reinterpret_cast<int*>(base);
@@ -909,19 +929,19 @@ fa_status fa_fwd_prefix_paged(const void* q, const void* k_pages, const void* v_
   p.cum = reinterpret_cast<unsigned int*>(base + w.cum);
   p.tok = reinterpret_cast<int4*>(base + w.tok);
   p.slab_rows = w.slab_rows;
-  p.slab_o = reinterpret_cast<float4*>(base + w.slab_o);
+  p.slab_o = reinterpret_cast<float*>(base + w.slab_o);
   p.slab_lse = reinterpret_cast<float*>(base + w.slab_lse);
-  p.own_o = reinterpret_cast<float4*>(base + w.own_o);
+  p.own_o = reinterpret_cast<float*>(base + w.own_o);
   p.own_lse = reinterpret_cast<float*>(base + w.own_lse);
-  p.prefix_o = reinterpret_cast<float4*>(base + w.prefix_o);
+  p.prefix_o = reinterpret_cast<float*>(base + w.prefix_o);
   p.prefix_lse = reinterpret_cast<float*>(base + w.prefix_lse);
-  CUtensorMap tqp, tqs, tk, tv;
-  if (!encode_tensor_map(&tqp, q, N, H, d, false, p.group, 128, p.tp) ||
-      !encode_tensor_map(&tqs, q, N, H, d, false, p.group, 128, p.ts) ||
-      !encode_tensor_map(&tk, k_pages, num_pages * Hkv, fa::kPage, d, false, fa::kPage, 128) ||
-      !encode_tensor_map(&tv, v_pages, num_pages * Hkv, fa::kPage, d, false, fa::kPage, 128))
+  fa::PrefixMaps t;
+  const int planes = num_pages * Hkv;
+  if (!encode_tensor_map(&t.q, q, N, H, d, false, group, 128, tp) ||
+      !encode_page_map(&t.k, k_pages, planes, d, fa::kPage) || !encode_page_map(&t.v, v_pages, planes, d, fa::kPage) ||
+      !encode_page_map(&t.k16, k_pages, planes, d, 16) || !encode_page_map(&t.v16, v_pages, planes, d, 16))
     return FA_ERR_CUDA;
-  if (fa::launch_fa_fwd_prefix(d, tqp, tqs, tk, tv, p, stream) != cudaSuccess) {
+  if (fa::launch_fa_fwd_prefix(d, t, p, stream) != cudaSuccess) {
     cudaGetLastError();
     return FA_ERR_LAUNCH;
   }

@@ -40,6 +40,7 @@ cudaError_t launch_kv_append(const AppendParams& p, int num_sms, cudaStream_t st
 cudaError_t read_and_clear_pages_status(cudaStream_t stream, unsigned int* out);
 
 struct PrefixParams {
+  const __nv_bfloat16* q;
   const int* prefix_table;
   const int* block_table;
   const int* seq_lens;
@@ -51,29 +52,34 @@ struct PrefixParams {
   int num_pages, max_pages;
   float scale_log2;               // scale * log2(e)
   unsigned long long timeout_ns;  // bound on every in-kernel wait
-  int ctas;     // blocks of the attention kernel: one per SM, at most kPrefixMaxCtas
-  int tiles_p;  // 128-key tiles of the prefix
-  int tp, ts;   // tokens of a 128-row tile over the prefix / over own keys
+  int ctas;      // blocks of the attention kernel: one per SM, at most kPrefixMaxCtas
+  int teams;     // few-row teams per block: 8, 4 or 2
+  int few_rows;  // rows of a few-row item at most: 8, 16 (one warp), 32 or 64
+  int tiles_p;   // 128-key tiles of the prefix
+  int tp;        // tokens of a 128-row tile
   // workspace
-  int* hdr;             // kHdr* words
-  int* start;           // [ctas] the request a block's own keys begin with
-  unsigned int* cum;    // [B] place of the request's first item
-  int4* tok;            // [N] place of the token's own item (K/V head 0), its tiles, the tiles the token's row
-                        // tile sees, the token's number within the item
-  int slab_rows;        // rows of a slab
-  float4* slab_o;       // [ctas][2][d / 4][slab_rows] parts of cut items, four columns each
-  float* slab_lse;      // [ctas][2][slab_rows], base-2
-  float4* own_o;        // [Hkv][d / 4][N * group] parts of whole items of own keys
-  float* own_lse;       // [Hkv][N * group]
-  float4* prefix_o;     // the same of the prefix
+  int* hdr;           // kHdr* words
+  int* start;         // [ctas][ctas * teams] the request a many-row, few-row worker's own keys begin with
+  unsigned int* cum;  // [2][B] place of the request's first item on the many-row, few-row line
+  int4* tok;          // [N] place of the token's own item (K/V head 0), its units, the units that the token's row
+                      // tile sees, the token's number in the item | kTokFew | places of a unit << 16
+  int slab_rows;      // rows of a many-row slab
+  float* slab_o;      // [ctas][2][slab_rows][d], then [ctas * teams][2][few_rows][d]: parts of cut items
+  float* slab_lse;    // the same rows, base-2
+  float* own_o;       // [N * H][d] parts of whole items of own keys
+  float* own_lse;
+  float* prefix_o;    // the same of the prefix
   float* prefix_lse;
 };
 constexpr int kPrefixMaxCtas = 160;
-unsigned int prefix_tile_cost();  // places a key tile and an item take (see fa_prefix.cu)
+// q: bf16 (d, H, N) with boxes of 64 columns x group heads x tp tokens; k, v: the page pools as (64, 128 rows, d / 64,
+// num_pages * Hkv) in boxes of whole pages, k16, v16: of 16 rows.
+struct PrefixMaps {
+  CUtensorMap q, k, v, k16, v16;
+};
+unsigned int prefix_page_cost();  // the most places a page and an item take on a line (see fa_prefix.cu)
 unsigned int prefix_item_cost();
-// qp, qs: bf16 (d, H, N) with boxes of 64 columns x group heads x tp / ts tokens; k, v: the page pools.
-cudaError_t launch_fa_fwd_prefix(int d, const CUtensorMap& qp, const CUtensorMap& qs, const CUtensorMap& k,
-                                 const CUtensorMap& v, const PrefixParams& p, cudaStream_t stream);
+cudaError_t launch_fa_fwd_prefix(int d, const PrefixMaps& t, const PrefixParams& p, cudaStream_t stream);
 cudaError_t read_and_clear_prefix_status(cudaStream_t stream, unsigned int* out);
 
 }  // namespace fa

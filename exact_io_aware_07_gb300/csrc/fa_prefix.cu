@@ -9,16 +9,20 @@
 //
 // Three kernels on the stream, each starting its set-up while the one before it ends:
 //   fa_prefix_plan_kernel  lays out the work from the device lengths,
-//   fa_prefix_kernel       one block per SM, tcgen05 products over its share of the key tiles,
+//   fa_prefix_kernel       one block per SM, the attention over its share of the keys,
 //   fa_prefix_join_kernel  joins the parts of every row.
 //
-// The work is a list of items: (K/V head, up to two row tiles of 128 rows, the 128-key tiles of one
-// source).  The items of the prefix come first: rows are the (token, query head) pairs of the whole
-// batch, `group` rows per token, so a K/V tile is loaded once for up to 256 rows.  Then the items of
-// every request's own keys.  Every key tile takes kTileCost places on a line, every item kItemCost
-// more, and SM c works the tiles whose places begin in [c Q, (c + 1) Q), Q = the line's length over
-// the number of SMs: all SMs get the same share whatever the lengths, and at most two items of an SM
-// are cut (its first and its last).
+// The work is a list of items: (K/V head, rows, the keys of one source), rows being (token, query head)
+// pairs, `group` of them per token.  Over the prefix an item holds rows of any requests, over own keys
+// those of one request.  There are two kinds, and every block works one of them:
+//   many rows: up to 256 rows on tcgen05 products, keys in tiles of 128 (bound by the tensor core);
+//   few rows:  up to 8, 16, 32 or 64 rows (a decoding request, a few drafted tokens) on warp-level products,
+//              keys in steps of 16, by teams of one, two or four warps (bound by loading the keys).
+// The items of a kind stand on a line, a key tile or step and an item taking so many places each, and the
+// kind's workers (blocks, or teams) get equal stretches of it: worker w the tiles whose places begin in
+// [w Q, (w + 1) Q).  So all workers have the same share whatever the lengths, and at most two items of a
+// worker are cut, its first and its last.  The blocks are shared out between the kinds by their cost.
+#include <limits.h>
 #include <math.h>
 
 #include "fa_pages.h"
@@ -28,15 +32,35 @@ namespace fa {
 
 static __device__ unsigned int g_prefix_status;  // kStatus* bits
 
-constexpr unsigned int kTileCost = 4, kItemCost = 4;
-enum { kHdrTotal, kHdrShare, kHdrPrefix, kHdrBlocks, kHdrTokens };  // words of p.hdr
+// Places on the lines.  Many rows: an item, and a key tile of an item with up to 128 and more rows; few rows: an
+// item, and one per step.  kManyTime / kFewTime: time of a place of either kind on one SM, for sharing out the SMs.
+constexpr unsigned int kItemCost = 4, kTileCost128 = 6, kTileCost256 = 8;
+constexpr unsigned int kFewItemCost = 4, kFewLeast = 4;  // (at least kFewLeast places for a team)
+constexpr float kManyTime = 0.2f, kFewTime = 0.08f;
+constexpr int kStep = 16;  // keys per step of the few-row kind
+// words of p.hdr (two each where the lines have their own: many rows, few rows)
+enum { kHdrTotal = 0, kHdrShare = 2, kHdrLead = 4, kHdrMany = 6, kHdrBlocks, kHdrTokens };
+constexpr int kTokFew = 1 << 15;  // in a token's fourth word: its item is on the few-row line
 
-__device__ __forceinline__ unsigned int item_cost(int tiles) { return tiles ? kItemCost + kTileCost * tiles : 0u; }
-// First tile of an item of `tiles` tiles beginning at c0 whose place is not before x.
-__device__ __forceinline__ int tile_from(unsigned int x, unsigned int c0, int tiles) {
-  if (x <= c0 + kItemCost) return 0;
-  const unsigned int j = (x - c0 - kItemCost + kTileCost - 1) / kTileCost;
-  return j < static_cast<unsigned int>(tiles) ? static_cast<int>(j) : tiles;
+__device__ __forceinline__ unsigned int tile_cost(int rows) { return rows <= 128 ? kTileCost128 : kTileCost256; }
+// A line's item: its first place, places before its first unit (tile or step), places per unit, units.
+struct Item {
+  unsigned int c0, lead, unit;
+  int units;
+  __device__ __forceinline__ unsigned int cost() const { return units ? lead + unit * units : 0u; }
+  // first unit whose place is not before x
+  __device__ __forceinline__ int from(unsigned int x) const {
+    if (x <= c0 + lead) return 0;
+    const unsigned int j = (x - c0 - lead + unit - 1) / unit;
+    return j < static_cast<unsigned int>(units) ? static_cast<int>(j) : units;
+  }
+  __device__ __forceinline__ int worker(int unit_index, unsigned int share) const {
+    return static_cast<int>((c0 + lead + unit * unit_index) / share);
+  }
+};
+__device__ __forceinline__ Item many_item(unsigned int c0, int tiles, unsigned int tile) { return Item{c0, kItemCost, tile, tiles}; }
+__device__ __forceinline__ Item few_item(unsigned int c0, int keys) {
+  return Item{c0, kFewItemCost, 1u, (keys + kStep - 1) / kStep};
 }
 
 struct Request {
@@ -49,91 +73,124 @@ __device__ __forceinline__ Request make_request(const PrefixParams& p, int cu0, 
   r.len = min(max(seq, 0), p.max_pages * kPage);
   return r;
 }
+__device__ __forceinline__ bool is_few(const PrefixParams& p, const Request& r) { return r.added * p.group <= p.few_rows; }
 __device__ __forceinline__ int tiles_of(int keys) { return (keys + kPage - 1) / kPage; }
 // Own keys that the tokens before the request's token `end` (exclusive) can see at most.
 __device__ __forceinline__ int visible(const PrefixParams& p, const Request& r, int end) {
   return p.causal ? max(0, min(r.len, r.len - r.added + end)) : r.len;
 }
-__device__ __forceinline__ int block_tiles(const PrefixParams& p, const Request& r, int blk) {
-  return tiles_of(visible(p, r, min(r.added, (blk + 1) * 2 * p.ts)));
+// The item (of K/V head 0, at c0) of a many-row request's block of 2 tp tokens.
+__device__ __forceinline__ Item block_item(const PrefixParams& p, const Request& r, int blk, unsigned int c0) {
+  const int end = min(r.added, (blk + 1) * 2 * p.tp);
+  return many_item(c0, tiles_of(visible(p, r, end)), tile_cost((end - blk * 2 * p.tp) * p.group));
+}
+// Items of the prefix: many-row blocks of 2 tp tokens (each counted as a full one unless it is the only one), or
+// one few-row item, per K/V head.
+__device__ __forceinline__ Item prefix_item(const PrefixParams& p, int tokens, unsigned int index) {
+  Item it = tokens * p.group <= p.few_rows ? few_item(0, p.prefix_len)
+                                           : many_item(0, p.tiles_p, tile_cost(min(2 * p.tp, tokens) * p.group));
+  it.c0 = index * it.cost();
+  return it;
 }
 
 // ---------------------------------------------------------------- plan
-// Every block forms the running sum of the requests' costs, kPlanThreads requests at a time; block 0
-// writes it out with the share Q and the request each SM begins with, and the blocks share out the
-// tokens, whose item (place, cost, visible tiles, row) the join needs.
+// Every block forms the running sums of the requests' places on both lines, kPlanThreads requests at a time;
+// block 0 writes them out with the shares and the request each worker begins with, and the blocks share out the
+// tokens, whose item the join needs.
 constexpr int kPlanThreads = 512;
 
 __global__ void __launch_bounds__(kPlanThreads) fa_prefix_plan_kernel(const PrefixParams p) {
-  __shared__ unsigned int s_cum[kPlanThreads + 1];
+  __shared__ unsigned int s_cum[2][kPlanThreads];
   __shared__ int s_first[kPlanThreads], s_added[kPlanThreads], s_len[kPlanThreads];
-  __shared__ unsigned int s_warp[kPlanThreads / 32];
+  __shared__ unsigned long long s_warp[kPlanThreads / 32];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   pdl_launch_dependents();
   pdl_wait();
   const int end = p.cu_new[p.B], tokens = min(max(end, 0), p.N);
-  const int blocks = (tokens + 2 * p.tp - 1) / (2 * p.tp);
-  const unsigned int prefix_cost = static_cast<unsigned int>(p.Hkv) * blocks * item_cost(p.tiles_p);
+  const bool few_prefix = tokens * p.group <= p.few_rows;
+  const int blocks = few_prefix ? 1 : (tokens + 2 * p.tp - 1) / (2 * p.tp);
+  const unsigned int prefix_cost = tokens == 0 ? 0u : static_cast<unsigned int>(p.Hkv) * blocks * prefix_item(p, tokens, 0).cost();
+  const unsigned int lead[2] = {few_prefix ? 0u : prefix_cost, few_prefix ? prefix_cost : 0u};
   bool bad = end > p.N || end < 0 || p.cu_new[0] != 0;
-  const bool one = p.B <= kPlanThreads;  // a single round: the sum is known before it is used
-  unsigned int total = 0, share = 1;
+  const bool one = p.B <= kPlanThreads;  // a single round: the sums are known before they are used
+  unsigned int total[2] = {0, 0}, share[2] = {1, 1};
+  int many = 0;  // blocks that work the many-row line
+  auto share_out = [&] {
+    const float a = kManyTime * total[0], b = kFewTime * total[1];
+    many = total[0] == 0 ? 0 : total[1] == 0 ? p.ctas : max(1, min(p.ctas - 1, __float2int_rn(p.ctas * a / (a + b))));
+    share[0] = max(1u, (total[0] + max(many, 1) - 1) / max(many, 1));
+    const unsigned int teams = max(1, (p.ctas - many) * p.teams);
+    share[1] = max(kFewLeast, (total[1] + teams - 1) / teams);
+  };
   for (int pass = one ? 1 : 0; pass < 2; ++pass) {  // pass 0 only sums
-    unsigned int carry = prefix_cost;
+    unsigned long long carry = lead[0] | static_cast<unsigned long long>(lead[1]) << 32;  // many-row, few-row << 32
     for (int b0 = 0; b0 < p.B; b0 += kPlanThreads) {
       const int b = b0 + tid, count = min(kPlanThreads, p.B - b0);
       Request r{0, 0, 0};
-      unsigned int mine = 0;
+      unsigned long long mine = 0;
       if (b < p.B) {
         const int c0 = p.cu_new[b], c1 = p.cu_new[b + 1], seq = p.seq_lens[b];
         bad |= c1 < c0 || seq < 0 || seq > p.max_pages * kPage;
         r = make_request(p, c0, c1, seq);
-        for (int blk = 0; blk * 2 * p.ts < r.added; ++blk) mine += item_cost(block_tiles(p, r, blk));
-        mine *= p.Hkv;
+        if (!is_few(p, r)) {
+          unsigned int sum = 0;
+          for (int blk = 0; blk * 2 * p.tp < r.added; ++blk) sum += block_item(p, r, blk, 0).cost();
+          mine = sum * p.Hkv;
+        } else if (r.added > 0) {
+          mine = static_cast<unsigned long long>(few_item(0, visible(p, r, r.added)).cost() * p.Hkv) << 32;
+        }
       }
-      unsigned int sum = mine;
+      unsigned long long sum = mine;
 #pragma unroll
       for (int w = 1; w < 32; w <<= 1) {
-        const unsigned int t = __shfl_up_sync(0xffffffffu, sum, w);
+        const unsigned long long t = __shfl_up_sync(0xffffffffu, sum, w);
         if (lane >= w) sum += t;
       }
       if (lane == 31) s_warp[warp] = sum;
       __syncthreads();
-      unsigned int before = 0, all = 0;
+      unsigned long long before = 0, all = 0;
 #pragma unroll
       for (int w = 0; w < kPlanThreads / 32; ++w) {
-        const unsigned int t = s_warp[w];
+        const unsigned long long t = s_warp[w];
         before += w < warp ? t : 0u;
         all += t;
       }
-      const unsigned int cum = carry + before + sum - mine;
+      const unsigned long long cum = carry + before + sum - mine;
+      const unsigned int begin[2] = {static_cast<unsigned int>(carry), static_cast<unsigned int>(carry >> 32)};
       carry += all;
       if (pass == 1) {
-        s_cum[tid] = cum;
+        s_cum[0][tid] = static_cast<unsigned int>(cum);
+        s_cum[1][tid] = static_cast<unsigned int>(cum >> 32);
         s_first[tid] = r.first;
         s_added[tid] = r.added;
         s_len[tid] = r.len;
-        if (blockIdx.x == 0 && b < p.B) p.cum[b] = cum;
+        if (blockIdx.x == 0 && b < p.B) {
+          p.cum[b] = static_cast<unsigned int>(cum);
+          p.cum[p.B + b] = static_cast<unsigned int>(cum >> 32);
+        }
         if (one) {
-          total = carry;
-          share = max(1u, (total + p.ctas - 1) / p.ctas);
+          total[0] = static_cast<unsigned int>(carry);
+          total[1] = static_cast<unsigned int>(carry >> 32);
+          share_out();
         }
       }
       __syncthreads();
       if (pass == 0) continue;
-      const unsigned int c_begin = s_cum[0];
-      if (blockIdx.x == 0)  // the request that holds place max(c * share, prefix_cost) of SM c
-        for (int c = tid; c < p.ctas; c += kPlanThreads) {
-          const unsigned int x = max(static_cast<unsigned int>(c) * share, prefix_cost);
-          if (x < c_begin || x >= carry) continue;
+      if (blockIdx.x == 0)  // the request that holds the first own place of every worker
+        for (int w = tid; w < p.ctas * (1 + p.teams); w += kPlanThreads) {
+          const int kind = w >= p.ctas, worker = kind ? w - p.ctas : w;
+          const unsigned long long at = static_cast<unsigned long long>(worker) * share[kind];
+          const unsigned int x = static_cast<unsigned int>(max(at, static_cast<unsigned long long>(lead[kind])));
+          if (at >= total[kind] || x < begin[kind] || x >= static_cast<unsigned int>(kind ? carry >> 32 : carry)) continue;
           int lo = 0, hi = count;  // the last request beginning at or before x
           while (hi - lo > 1) {
             const int mid = (lo + hi) >> 1;
-            if (s_cum[mid] <= x)
+            if (s_cum[kind][mid] <= x)
               lo = mid;
             else
               hi = mid;
           }
-          p.start[c] = b0 + lo;
+          p.start[w] = b0 + lo;
         }
       const int n_begin = b0 == 0 ? 0 : s_first[0], n_end = s_first[count - 1] + s_added[count - 1];
       for (int n = n_begin + blockIdx.x * kPlanThreads + tid; n < n_end; n += gridDim.x * kPlanThreads) {
@@ -149,24 +206,34 @@ __global__ void __launch_bounds__(kPlanThreads) fa_prefix_plan_kernel(const Pref
         const int i = n - q.first;
         int4 t = make_int4(0, 0, 0, 0);  // no own key
         if (i >= 0 && i < q.added) {
-          const int blk = i / (2 * p.ts);
-          unsigned int c0 = s_cum[lo];
-          for (int k = 0; k < blk; ++k) c0 += p.Hkv * item_cost(block_tiles(p, q, k));
-          const int tile = i / p.ts;
-          t = make_int4(static_cast<int>(c0), block_tiles(p, q, blk),
-                        tiles_of(visible(p, q, min(q.added, (tile + 1) * p.ts))), i - blk * 2 * p.ts);
+          if (is_few(p, q)) {
+            const Item it = few_item(s_cum[1][lo], visible(p, q, q.added));
+            t = make_int4(static_cast<int>(it.c0), it.units, it.units, i | kTokFew);
+          } else {
+            const int blk = i / (2 * p.tp);
+            unsigned int c0 = s_cum[0][lo];
+            for (int k = 0; k < blk; ++k) c0 += p.Hkv * block_item(p, q, k, 0).cost();
+            const Item it = block_item(p, q, blk, c0);
+            t = make_int4(static_cast<int>(c0), it.units, tiles_of(visible(p, q, min(q.added, (i / p.tp + 1) * p.tp))),
+                          (i - blk * 2 * p.tp) | static_cast<int>(it.unit) << 16);
+          }
         }
         p.tok[n] = t;
       }
       __syncthreads();
     }
-    total = carry;
-    share = max(1u, (total + p.ctas - 1) / p.ctas);
+    total[0] = static_cast<unsigned int>(carry);
+    total[1] = static_cast<unsigned int>(carry >> 32);
+    share_out();
   }
   if (blockIdx.x == 0 && tid == 0) {
-    p.hdr[kHdrTotal] = static_cast<int>(total);
-    p.hdr[kHdrShare] = static_cast<int>(share);
-    p.hdr[kHdrPrefix] = static_cast<int>(prefix_cost);
+    p.hdr[kHdrTotal] = static_cast<int>(total[0]);
+    p.hdr[kHdrTotal + 1] = static_cast<int>(total[1]);
+    p.hdr[kHdrShare] = static_cast<int>(share[0]);
+    p.hdr[kHdrShare + 1] = static_cast<int>(share[1]);
+    p.hdr[kHdrLead] = static_cast<int>(lead[0]);
+    p.hdr[kHdrLead + 1] = static_cast<int>(lead[1]);
+    p.hdr[kHdrMany] = many;
     p.hdr[kHdrBlocks] = blocks;
     p.hdr[kHdrTokens] = tokens;
   }
@@ -174,12 +241,36 @@ __global__ void __launch_bounds__(kPlanThreads) fa_prefix_plan_kernel(const Pref
 }
 
 // ---------------------------------------------------------------- attention
-// Roles (one block per SM): warps 0-3 and 4-7 the softmax of slot 0 and slot 1 (a thread has one of
-// 128 rows), warp 8 the producer (lays out the SM's pieces, issues the TMA loads), warp 9 the
-// tcgen05.mma issuer.  A piece is the SM's share of an item, in one of two forms:
+// One lane loads a box of a page pool ((64, 128 rows, d / 64, planes) view: the 64-column halves of the box's rows one
+// behind the other) and adds its bytes to what `bar` expects.
+__device__ __forceinline__ void load_rows_elect(uint32_t dst, const void* tmap, int row, int plane, uint32_t bar, uint32_t bytes) {
+  asm volatile(
+      "{\n\t.reg .pred e;\n\t.reg .b64 st;\n\telect.sync _|e, 0xffffffff;\n\t"
+      "@e mbarrier.arrive.expect_tx.shared::cta.b64 st, [%4], %5;\n\t"
+      "@e cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {0, %2, 0, %3}], [%4];\n\t}"
+      :: "r"(dst), "l"(reinterpret_cast<uint64_t>(tmap)), "r"(row), "r"(plane), "r"(bar), "r"(bytes) : "memory");
+}
+// The same rows of two pools, to dst and dst + half.
+__device__ __forceinline__ void load_rows2_elect(uint32_t dst, uint32_t half, const void* tmap0, const void* tmap1, int row,
+                                                 int plane, uint32_t bar) {
+  asm volatile(
+      "{\n\t.reg .pred e;\n\t.reg .b64 st;\n\telect.sync _|e, 0xffffffff;\n\t"
+      "@e mbarrier.arrive.expect_tx.shared::cta.b64 st, [%6], %7;\n\t"
+      "@e cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%2, {0, %4, 0, %5}], [%6];\n\t"
+      "@e cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%1], [%3, {0, %4, 0, %5}], [%6];\n\t}"
+      :: "r"(dst), "r"(dst + half), "l"(reinterpret_cast<uint64_t>(tmap0)), "l"(reinterpret_cast<uint64_t>(tmap1)),
+         "r"(row), "r"(plane), "r"(bar), "r"(2 * half) : "memory");
+}
+
+// Many rows.  Roles: warps 0-3 and 4-7 the softmax of slot 0 and slot 1 (a thread has one of 128 rows),
+// warp 8 the producer (lays out the block's pieces, issues the TMA loads), warp 9 the tcgen05.mma
+// issuer.  A piece is the block's share of an item, in one of two forms:
 //   two row tiles: each slot holds one, both visit every key tile (a tile is loaded once);
-//   one row tile (a decoding request has `group` rows): the slots take its key tiles in turn, so that
-//   one's softmax overlaps the other's products, and slot 0 joins both results at the end.
+//   one row tile: the slots take its key tiles in turn, so that one's softmax overlaps the other's
+//   products, and slot 0 joins both results at the end.
 // Tensor Memory (512 columns): S_0 [0,128), S_1 [128,256), O_0, O_1 from 256; P_i (bf16 pairs) over S_i.
 constexpr int BM = 128, BN = 128;
 constexpr int PRODUCER_WARP = 8, MMA_WARP = 9, THREADS = 320;
@@ -200,7 +291,6 @@ struct __align__(16) Piece {
   int tile_rows;     // rows of a full row tile
   int pad0, pad1;
 };
-enum { kDstOutput, kDstSlab0, kDstSlab1, kDstOwn, kDstPrefix };
 
 template <int D>
 struct PLayout {
@@ -222,14 +312,45 @@ static_assert(PLayout<64>::SMEM_BYTES <= 232448 && PLayout<128>::SMEM_BYTES <= 2
 __device__ __forceinline__ float u2f(uint32_t x) { return __uint_as_float(x); }
 __device__ __forceinline__ uint32_t f2u(float x) { return __float_as_uint(x); }
 
+// Where a row's part goes: `out` (the row itself, in bf16) or `part`, and the LSE at `lse` (natural for the
+// row itself, base-2 for a part).  slab: the worker's slab for cut items (slab_o / slab_lse at its first row).
+enum { kDstOutput, kDstSlab0, kDstSlab1, kDstOwn, kDstPrefix };
+struct RowOut {
+  __nv_bfloat16* out;
+  float* part;
+  float* lse;
+};
 template <int D>
-__global__ void __launch_bounds__(THREADS, 1)
-fa_prefix_kernel(const __grid_constant__ CUtensorMap tmQp, const __grid_constant__ CUtensorMap tmQs,
-                 const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
-                 const PrefixParams p) {
+__device__ __forceinline__ RowOut row_out(const PrefixParams& p, int dst, size_t slab_row, int g, int t0, int row) {
+  RowOut w{nullptr, nullptr, nullptr};
+  if (dst == kDstSlab0 || dst == kDstSlab1) {
+    w.part = p.slab_o + (slab_row + row) * D;
+    w.lse = p.slab_lse + slab_row + row;
+    return w;
+  }
+  const int t = row / p.group;
+  const size_t orow = static_cast<size_t>(t0 + t) * p.H + g * p.group + (row - t * p.group);
+  if (dst == kDstOutput) {
+    w.out = p.o + orow * D;
+    w.lse = p.lse + orow;
+  } else {
+    w.part = (dst == kDstOwn ? p.own_o : p.prefix_o) + orow * D;
+    w.lse = (dst == kDstOwn ? p.own_lse : p.prefix_lse) + orow;
+  }
+  return w;
+}
+// First slab row of worker `w` of a kind for its first (0) or last (1) cut item.
+__device__ __forceinline__ size_t many_slab(const PrefixParams& p, int w, int which) {
+  return (static_cast<size_t>(w) * 2 + which) * p.slab_rows;
+}
+__device__ __forceinline__ size_t few_slab(const PrefixParams& p, int w, int which) {
+  return static_cast<size_t>(p.ctas) * 2 * p.slab_rows + (static_cast<size_t>(w) * 2 + which) * p.few_rows;
+}
+
+template <int D>
+__device__ __forceinline__ void many_rows(const CUtensorMap& tmQ, const CUtensorMap& tmK, const CUtensorMap& tmV,
+                                          const PrefixParams& p, uint8_t* smem) {
   using L = PLayout<D>;
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t sbase = smem_u32(smem);
   const uint32_t kv_smem = sbase + L::KV_OFF;
   const uint32_t bar = sbase + L::BAR_OFF;
@@ -271,22 +392,14 @@ fa_prefix_kernel(const __grid_constant__ CUtensorMap tmQp, const __grid_constant
     tmem_alloc(smem_u32(tmem_slot), 512);
     tmem_relinquish();
   }
-  if (warp == PRODUCER_WARP && lane == 0) {
-    tma_prefetch_desc(&tmQp);
-    tma_prefetch_desc(&tmQs);
-    tma_prefetch_desc(&tmK);
-    tma_prefetch_desc(&tmV);
-  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   const Waiter W{abort_flag, p.timeout_ns, &g_prefix_status};
-  pdl_launch_dependents();
-  pdl_wait();
 
   if (warp == PRODUCER_WARP) {
-    const unsigned int total = p.hdr[kHdrTotal], share = p.hdr[kHdrShare], prefix_cost = p.hdr[kHdrPrefix];
+    const unsigned int total = p.hdr[kHdrTotal], share = p.hdr[kHdrShare], prefix_cost = p.hdr[kHdrLead];
     const int blocks = p.hdr[kHdrBlocks], tokens = p.hdr[kHdrTokens];
     const unsigned int x0 = blockIdx.x * share, x1 = min(total, x0 + share);
     int stage = 0, np = 0;
@@ -308,11 +421,7 @@ fa_prefix_kernel(const __grid_constant__ CUtensorMap tmQp, const __grid_constant
         pg = p.num_pages;
       }
       if (!wait_all(W, bar_kv_empty + 8 * stage, phase ^ 1)) return false;
-      mbar_arrive_expect_tx_elect(bar_kv_full + 8 * stage, L::TILE_BYTES);
-#pragma unroll
-      for (int b = 0; b < L::BOXES; ++b)
-        tma_load_3d_elect(kv_smem + stage * L::TILE_BYTES + b * BOX_BYTES, map, b * 64, 0, pg * p.Hkv + g,
-                          bar_kv_full + 8 * stage);
+      load_rows_elect(kv_smem + stage * L::TILE_BYTES, map, 0, pg * p.Hkv + g, bar_kv_full + 8 * stage, L::TILE_BYTES);
       issued |= 1u << stage;
       issued_parity = (issued_parity & ~(1u << stage)) | (phase << stage);
       if (++stage == L::STAGES) {
@@ -335,9 +444,10 @@ fa_prefix_kernel(const __grid_constant__ CUtensorMap tmQp, const __grid_constant
       ++np;
       return true;
     };
-    // Emits this SM's tiles [j0, j1) of an item: tokens [t0, t0 + count) in row tiles of tile_tokens.
-    auto emit = [&](bool own, const int* table, int g, int t0, int count, int tile_tokens, int tiles, int tiles0, int j0,
-                    int j1, int keys, int lim0, int step) -> bool {
+    // Emits this block's tiles [j0, j1) of an item: tokens [t0, t0 + count) in row tiles of tp tokens.
+    auto emit = [&](bool own, const int* table, int g, int t0, int count, int tiles, int tiles0, int j0, int j1, int keys,
+                    int lim0, int step) -> bool {
+      const int tile_tokens = p.tp;
       Piece q;
       q.n = j1 - j0;
       q.mode = count > tile_tokens ? 2 : 1;
@@ -356,13 +466,12 @@ fa_prefix_kernel(const __grid_constant__ CUtensorMap tmQp, const __grid_constant
       const int k = np;
       if (!publish(q)) return false;
       if (!wait_all(W, bar_q_empty, (k & 1) ^ 1)) return false;
-      const CUtensorMap* qm = own ? &tmQs : &tmQp;
       const uint32_t box = static_cast<uint32_t>(q.tile_rows) * 128;
       mbar_arrive_expect_tx_elect(bar_q_full, box * L::BOXES * q.mode);
       for (int i = 0; i < q.mode; ++i)
 #pragma unroll
         for (int b = 0; b < L::BOXES; ++b)
-          tma_load_3d_elect(sbase + i * L::TILE_BYTES + b * BOX_BYTES, qm, b * 64, g * p.group, t0 + i * tile_tokens,
+          tma_load_3d_elect(sbase + i * L::TILE_BYTES + b * BOX_BYTES, &tmQ, b * 64, g * p.group, t0 + i * tile_tokens,
                             bar_q_full);
       if (q.mode == 1) {  // K_0 K_1 V_0 K_2 V_1 K_3 ...
         if (!kv_load(&tmK, table, j0, g) || (q.n > 1 && !kv_load(&tmK, table, j0 + 1, g))) return false;
@@ -376,22 +485,22 @@ fa_prefix_kernel(const __grid_constant__ CUtensorMap tmQp, const __grid_constant
     };
 
     if (x0 < x1 && x0 < prefix_cost) {  // items of the prefix: head by head, block of rows by block
-      const unsigned int cost = item_cost(p.tiles_p);
       const int items = p.Hkv * blocks;
-      for (int it = x0 / cost; ok && it < items && it * cost < x1; ++it) {
-        const unsigned int c0 = it * cost;
-        const int j0 = tile_from(x0, c0, p.tiles_p), j1 = tile_from(x1, c0, p.tiles_p);
+      for (int at = x0 / prefix_item(p, tokens, 0).cost(); ok && at < items; ++at) {
+        const Item it = prefix_item(p, tokens, at);
+        if (it.c0 >= x1) break;
+        const int j0 = it.from(x0), j1 = it.from(x1);
         if (j0 >= j1) continue;
-        const int g = it / blocks, t0 = (it - g * blocks) * 2 * p.tp;
-        ok = emit(false, p.prefix_table, g, t0, min(2 * p.tp, tokens - t0), p.tp, p.tiles_p, p.tiles_p, j0, j1,
-                  p.prefix_len, p.prefix_len, 0);
+        const int g = at / blocks, t0 = (at - g * blocks) * 2 * p.tp;
+        ok = emit(false, p.prefix_table, g, t0, min(2 * p.tp, tokens - t0), p.tiles_p, p.tiles_p, j0, j1, p.prefix_len,
+                  p.prefix_len, 0);
       }
     }
     if (ok && x0 < x1 && x1 > prefix_cost) {  // items of own keys: requests, blocks of tokens, heads
       int b = p.start[blockIdx.x], base = b - 32;
       int r_cu0 = 0, r_cu1 = 0, r_seq = 0;
       unsigned int r_cum = 0;
-      for (bool more = true; ok && more && b < p.B; ++b) {
+      for (; ok && b < p.B; ++b) {
         if (b >= base + 32) {  // 32 requests at a time, one per lane
           base = b;
           const int l = min(b + lane, p.B - 1);
@@ -404,26 +513,23 @@ fa_prefix_kernel(const __grid_constant__ CUtensorMap tmQp, const __grid_constant
                                        __shfl_sync(0xffffffffu, r_seq, b - base));
         unsigned int c0 = __shfl_sync(0xffffffffu, r_cum, b - base);
         if (c0 >= x1) break;
+        if (is_few(p, r)) continue;
         const int* table = p.block_table + static_cast<size_t>(b) * p.max_pages;
-        for (int t = 0; ok && t < r.added; t += 2 * p.ts) {
-          const int count = min(2 * p.ts, r.added - t), tiles = tiles_of(visible(p, r, t + count));
-          const unsigned int cost = item_cost(tiles);
-          if (c0 >= x1) {
-            more = false;
-            break;
-          }
-          if (tiles == 0 || c0 + p.Hkv * cost <= x0) {
-            c0 += p.Hkv * cost;
-            continue;
-          }
-          const int tiles0 = tiles_of(visible(p, r, min(r.added, t + p.ts)));
-          for (int g = x0 > c0 ? (x0 - c0) / cost : 0; ok && g < p.Hkv && c0 + g * cost < x1; ++g) {
-            const int j0 = tile_from(x0, c0 + g * cost, tiles), j1 = tile_from(x1, c0 + g * cost, tiles);
+        for (int blk = 0; ok && blk * 2 * p.tp < r.added && c0 < x1; ++blk) {
+          Item it = block_item(p, r, blk, c0);
+          const unsigned int cost = it.cost();
+          c0 += p.Hkv * cost;
+          if (it.units == 0 || c0 <= x0) continue;
+          const int t = blk * 2 * p.tp, count = min(2 * p.tp, r.added - t);
+          const int tiles0 = tiles_of(visible(p, r, min(r.added, t + p.tp)));
+          const int g0 = x0 > it.c0 ? (x0 - it.c0) / cost : 0;
+          it.c0 += g0 * cost;
+          for (int g = g0; ok && g < p.Hkv && it.c0 < x1; ++g, it.c0 += cost) {
+            const int j0 = it.from(x0), j1 = it.from(x1);
             if (j0 < j1)
-              ok = emit(true, table, g, r.first + t, count, p.ts, tiles, tiles0, j0, j1, r.len,
+              ok = emit(true, table, g, r.first + t, count, it.units, tiles0, j0, j1, r.len,
                         p.causal ? r.len - r.added + t + 1 : r.len, p.causal);
           }
-          c0 += p.Hkv * cost;
         }
       }
     }
@@ -583,7 +689,7 @@ fa_prefix_kernel(const __grid_constant__ CUtensorMap tmQp, const __grid_constant
     const uint32_t t_s = tmem + lane_off + i * 128, t_o = tmem + lane_off + 256 + i * D;
     const uint32_t my_s_full = bar_s_full + 8 * i, my_p_full = bar_p_full + 8 * i;
     const uint32_t my_o_full = bar_o_full + 8 * i;
-    const int tok = rt / p.group, hh = rt - tok * p.group;  // the row's token within its tile, its head within the group
+    const int tok = rt / p.group;  // the row's token within its tile
     const float sl2 = p.scale_log2;
     uint32_t sf_phase = 0, of_phase = 0, x_phase = 0;
     bool ok = true;
@@ -710,25 +816,8 @@ fa_prefix_kernel(const __grid_constant__ CUtensorMap tmQp, const __grid_constant
         const float lse2 = l == 0.f ? -INFINITY : m_run + log2f(l);
         a0 *= inv;
         a1 *= inv;
-        const int row = row0 + rt;  // within the item
-        float4* part = nullptr;     // the row's first four columns; the next four `stride` further on
-        size_t stride = 0;
-        __nv_bfloat16* out = nullptr;
-        if (dst == kDstOutput) {
-          const size_t orow = static_cast<size_t>(t0 + row0 / p.group + tok) * p.H + g * p.group + hh;
-          out = p.o + orow * D;
-          if (live) p.lse[orow] = lse2 * LN2;
-        } else if (dst == kDstSlab0 || dst == kDstSlab1) {
-          const size_t slab = blockIdx.x * 2 + (dst - kDstSlab0);
-          stride = p.slab_rows;
-          part = p.slab_o + slab * (D / 4) * stride + row;
-          if (live) p.slab_lse[slab * stride + row] = lse2;
-        } else {
-          stride = static_cast<size_t>(p.N) * p.group;
-          const size_t at = static_cast<size_t>(t0) * p.group + row;
-          part = (dst == kDstOwn ? p.own_o : p.prefix_o) + static_cast<size_t>(g) * (D / 4) * stride + at;
-          if (live) (dst == kDstOwn ? p.own_lse : p.prefix_lse)[g * stride + at] = lse2;
-        }
+        const RowOut to = row_out<D>(p, dst, many_slab(p, blockIdx.x, dst == kDstSlab1), g, t0, row0 + rt);
+        if (live) *to.lse = to.out ? lse2 * LN2 : lse2;
 #pragma unroll
         for (int c = 0; c < D / 32; ++c) {
           uint32_t ov[32];
@@ -743,16 +832,16 @@ fa_prefix_kernel(const __grid_constant__ CUtensorMap tmQp, const __grid_constant
             for (int e = 0; e < 32; ++e) ov[e] = f2u(u2f(ov[e]) * a0);
           }
           if (!live) continue;
-          if (out) {
+          if (to.out) {
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-              *reinterpret_cast<uint4*>(out + c * 32 + e * 8) =
+              *reinterpret_cast<uint4*>(to.out + c * 32 + e * 8) =
                   make_uint4(pack_bf16x2(u2f(ov[8 * e]), u2f(ov[8 * e + 1])), pack_bf16x2(u2f(ov[8 * e + 2]), u2f(ov[8 * e + 3])),
                              pack_bf16x2(u2f(ov[8 * e + 4]), u2f(ov[8 * e + 5])), pack_bf16x2(u2f(ov[8 * e + 6]), u2f(ov[8 * e + 7])));
           } else {
 #pragma unroll
             for (int e = 0; e < 8; ++e)
-              part[(c * 8 + e) * stride] =
+              *reinterpret_cast<float4*>(to.part + c * 32 + e * 4) =
                   make_float4(u2f(ov[4 * e]), u2f(ov[4 * e + 1]), u2f(ov[4 * e + 2]), u2f(ov[4 * e + 3]));
           }
         }
@@ -775,86 +864,545 @@ fa_prefix_kernel(const __grid_constant__ CUtensorMap tmQp, const __grid_constant
   }
 }
 
-// ---------------------------------------------------------------- join
-// A block joins 32 rows of one K/V head: lane = row, every warp 8 columns.  The parts of a row follow
-// from the places of its two items: an item inside one SM's share has one part, in the buffer of its
-// source; one that is cut has a part in a slab of every SM that worked some of its tiles.
-template <int D>
-__global__ void __launch_bounds__(D * 4) fa_prefix_join_kernel(const PrefixParams p) {
-  const int lane = threadIdx.x & 31, col = threadIdx.x >> 5;  // columns 8 col .. 8 col + 7
-  const int blocks_per_head = (p.N * p.group + 31) / 32;
-  const int g = blockIdx.x / blocks_per_head;
-  const long long r = static_cast<long long>(blockIdx.x - g * blocks_per_head) * 32 + lane;  // row of head g
-  pdl_wait();
-  const int tokens = p.hdr[kHdrTokens];
-  const int n = static_cast<int>(r / p.group);
-  if (n >= tokens) return;
-  const unsigned int share = p.hdr[kHdrShare];
-  const int4 t = p.tok[n];
-  const size_t rows = static_cast<size_t>(p.N) * p.group;
-  float m = -INFINITY, sum = 0.f, acc[8];
-#pragma unroll
-  for (int e = 0; e < 8; ++e) acc[e] = 0.f;
-  auto add = [&](float lse2, const float4* part, size_t stride) {
-    const float4 a = part[2 * col * stride], b = part[(2 * col + 1) * stride];
-    if (lse2 == -INFINITY) return;
-    const float m2 = fmaxf(m, lse2), f = exp2f(m - m2), w = exp2f(lse2 - m2);
-    m = m2;
-    sum = sum * f + w;
-    acc[0] = acc[0] * f + w * a.x;
-    acc[1] = acc[1] * f + w * a.y;
-    acc[2] = acc[2] * f + w * a.z;
-    acc[3] = acc[3] * f + w * a.w;
-    acc[4] = acc[4] * f + w * b.x;
-    acc[5] = acc[5] * f + w * b.y;
-    acc[6] = acc[6] * f + w * b.z;
-    acc[7] = acc[7] * f + w * b.w;
-  };
-  // parts of the item at c0 with `tiles` tiles, `seen` of them visible to this row, row `at` of the item
-  auto join = [&](unsigned int c0, int tiles, int seen, int at, const float4* whole, const float* whole_lse) {
-    const int c_first = (c0 + kItemCost) / share, c_last = (c0 + kItemCost + kTileCost * (tiles - 1)) / share;
-    if (c_first == c_last) {
-      add(whole_lse[g * rows + r], whole + static_cast<size_t>(g) * (D / 4) * rows + r, rows);
-      return;
-    }
-    for (int c = c_first; c <= c_last; ++c) {
-      const int j0 = tile_from(c * share, c0, tiles), j1 = tile_from((c + 1) * share, c0, tiles);
-      if (j0 >= seen) break;
-      if (j0 >= j1) continue;
-      const size_t slab = c * 2 + (j0 == 0);
-      add(p.slab_lse[slab * p.slab_rows + at], p.slab_o + slab * (D / 4) * p.slab_rows + at, p.slab_rows);
-    }
-  };
-  const int hh = static_cast<int>(r - static_cast<long long>(n) * p.group);
-  if (p.tiles_p > 0) {
-    const int blk = n / (2 * p.tp), blocks = p.hdr[kHdrBlocks];
-    join((static_cast<unsigned int>(g) * blocks + blk) * item_cost(p.tiles_p), p.tiles_p, p.tiles_p,
-         (n - blk * 2 * p.tp) * p.group + hh, p.prefix_o, p.prefix_lse);
-  }
-  if (t.z > 0) {
-    const unsigned int c0 = static_cast<unsigned int>(t.x) + g * item_cost(t.y);
-    if (p.tiles_p == 0 && (c0 + kItemCost) / share == (c0 + kItemCost + kTileCost * (t.y - 1)) / share)
-      return;  // the attention kernel wrote this row
-    join(c0, t.y, t.z, t.w * p.group + hh, p.own_o, p.own_lse);
-  }
-  const float inv = sum == 0.f ? 0.f : 1.f / sum;
-  const size_t orow = static_cast<size_t>(n) * p.H + g * p.group + hh;
-  *reinterpret_cast<uint4*>(p.o + orow * D + col * 8) =
-      make_uint4(pack_bf16x2(acc[0] * inv, acc[1] * inv), pack_bf16x2(acc[2] * inv, acc[3] * inv),
-                 pack_bf16x2(acc[4] * inv, acc[5] * inv), pack_bf16x2(acc[6] * inv, acc[7] * inv));
-  if (col == 0) p.lse[orow] = sum == 0.f ? -INFINITY : (m + log2f(sum)) * LN2;
+// ---------------------------------------------------------------- few rows
+// A team of R warps works items of up to 8 NT R rows, warp t of it rows 8 NT t .., keys in steps of 16.  A 128-row
+// tcgen05 tile would spend its softmax on empty rows; here the products are warp-level and transposed, keys (or
+// columns of V) as the 16 rows of mma.sync m16n8k16 and query rows as its 8 columns:
+//   S^T (16 keys x 8 rows) = K Q^T,   O^T (16 columns x 8 rows) += V^T P^T,
+// so that eight rows cost one product per 16 x 16 of K and V and half the accumulators that rows as M would.  P^T
+// becomes the second product's operand by an 8 x 8 transpose in registers (movmatrix); the softmax state stays in
+// registers too, and a warp meets no other but at its team's ring of K/V steps, which the team's first warp fills by
+// TMA.  The 8 / R teams of a block are independent, so one's item start (request, table and query loads) and end hide
+// behind the others' keys in flight.
+constexpr int FEW_WARPS = 8;
+
+template <int D, int R>
+struct FLayout {
+  static constexpr int STEP_BYTES = 2 * kStep * D * 2;  // K, then V; 64 columns per box of 16 rows x 128 bytes
+  static constexpr int BOX = kStep * 128;
+  static constexpr int TEAMS = FEW_WARPS / R;
+  static constexpr int FIT = 224 * 1024 / (TEAMS * STEP_BYTES);
+  static constexpr int STAGES = FIT < 16 ? FIT : 16;
+  static constexpr int BAR_OFF = 224 * 1024;  // full[TEAMS][STAGES], empty[TEAMS][STAGES]
+  static constexpr int MISC_OFF = BAR_OFF + 2 * TEAMS * STAGES * 8;
+  static constexpr int SMEM_BYTES = MISC_OFF + 16 + 1024;
+};
+
+// Warp-level products: D (16 x 8) += A (16 x 16) B (16 x 8), bf16 in, fp32 out.
+__device__ __forceinline__ void mma_16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// Four 8 x 8 matrices of 16-bit values; lane l gives the address of row l % 8 of matrix l / 8.
+__device__ __forceinline__ void ldmatrix_x4(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ void ldmatrix_x4_trans(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
 }
 
-template <int D>
-static cudaError_t launch(const CUtensorMap& qp, const CUtensorMap& qs, const CUtensorMap& k, const CUtensorMap& v,
-                          const PrefixParams& p, cudaStream_t stream) {
-  using L = PLayout<D>;
+// Transpose of an 8 x 8 matrix of 16-bit values (lane l: row l / 4, columns 2 (l % 4) and the next).
+__device__ __forceinline__ uint32_t transpose_8x8(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+
+struct FewPiece {
+  const int* table;
+  int entries;              // of the table
+  int g, t0, rows, j0, j1;  // K/V head, first token, rows, steps
+  int keys, lim0, step;     // keys of the source; token i sees min(keys, lim0 + i * step) of them
+  int dst;
+};
+
+// The pieces of a stretch [x0, x1) of the few-row line, in order (all lanes of a warp together).
+struct FewWalk {
+  unsigned int x0, x1, lead, cost;
+  int tokens, at, items;  // items of the prefix on this line
+  int b, base, g;
+  bool have;
+  Request r;
+  Item it;
+  int cu0, cu1, seq;  // of request base + lane
+  unsigned int cum;
+
+  __device__ __forceinline__ void start(const PrefixParams& p, unsigned int from, unsigned int to, int first) {
+    x0 = from;
+    x1 = to;
+    lead = p.hdr[kHdrLead + 1];
+    tokens = p.hdr[kHdrTokens];
+    items = lead > 0 ? p.Hkv : 0;
+    at = x0 < lead ? static_cast<int>(x0 / (lead / p.Hkv)) : items;
+    b = first - 1;
+    base = b - 32;
+    have = false;
+    g = 0;
+    cost = 0;
+  }
+  __device__ __forceinline__ bool next(const PrefixParams& p, int lane, FewPiece& q) {
+    while (at < items) {
+      const Item i = prefix_item(p, tokens, at);
+      const int j0 = i.from(x0), j1 = i.from(x1);
+      if (i.c0 >= x1) return false;
+      const int head = at++;
+      if (j0 >= j1) continue;
+      q = FewPiece{p.prefix_table, p.tiles_p, head, 0, tokens * p.group, j0, j1, p.prefix_len, p.prefix_len, 0,
+                   j0 > 0 ? kDstSlab0 : j1 < i.units ? kDstSlab1 : kDstPrefix};
+      return true;
+    }
+    if (x1 <= lead) return false;
+    for (;;) {
+      if (have && g < p.Hkv) {
+        if (it.c0 >= x1) return false;
+        const int j0 = it.from(x0), j1 = it.from(x1), head = g++;
+        it.c0 += cost;
+        if (j0 >= j1) continue;
+        q = FewPiece{p.block_table + static_cast<size_t>(b) * p.max_pages, p.max_pages, head, r.first, r.added * p.group,
+                     j0, j1, r.len, p.causal ? r.len - r.added + 1 : r.len, p.causal,
+                     j0 > 0 ? kDstSlab0 : j1 < it.units ? kDstSlab1 : p.tiles_p > 0 ? kDstOwn : kDstOutput};
+        return true;
+      }
+      have = false;
+      if (++b >= p.B) return false;
+      if (b >= base + 32) {  // 32 requests at a time, one per lane
+        base = b;
+        const int l = min(b + lane, p.B - 1);
+        cu0 = p.cu_new[l];
+        cu1 = p.cu_new[l + 1];
+        seq = p.seq_lens[l];
+        cum = p.cum[p.B + l];
+      }
+      r = make_request(p, __shfl_sync(0xffffffffu, cu0, b - base), __shfl_sync(0xffffffffu, cu1, b - base),
+                       __shfl_sync(0xffffffffu, seq, b - base));
+      const unsigned int c0 = __shfl_sync(0xffffffffu, cum, b - base);
+      if (c0 >= x1) return false;
+      if (r.added == 0 || !is_few(p, r)) continue;
+      it = few_item(c0, visible(p, r, r.added));
+      cost = it.cost();
+      if (cost == 0 || c0 + p.Hkv * cost <= x0) continue;
+      g = x0 > c0 ? static_cast<int>((x0 - c0) / cost) : 0;
+      it.c0 += g * cost;
+      have = true;
+    }
+  }
+};
+
+template <int D, int NT, int R>
+__device__ __forceinline__ void few_rows(const CUtensorMap& tmK, const CUtensorMap& tmV, const PrefixParams& p,
+                                         uint8_t* smem) {
+  using L = FLayout<D, R>;
+  const uint32_t sbase = smem_u32(smem);
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int team = warp / R, mt = warp % R;
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::MISC_OFF);
+  if (threadIdx.x == 0) {
+    for (int t = 0; t < L::TEAMS * L::STAGES; ++t) {
+      mbar_init(sbase + L::BAR_OFF + 8 * t, 1);
+      mbar_init(sbase + L::BAR_OFF + 8 * (L::TEAMS * L::STAGES + t), R);
+    }
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  __syncthreads();
+  if (warp >= FEW_WARPS) return;
+  const Waiter W{abort_flag, p.timeout_ns, &g_prefix_status};
+  const uint32_t ring = sbase + team * L::STAGES * L::STEP_BYTES;
+  const uint32_t bar_full = sbase + L::BAR_OFF + 8 * team * L::STAGES;
+  const uint32_t bar_empty = bar_full + 8 * L::TEAMS * L::STAGES;
+  const int worker = (blockIdx.x - p.hdr[kHdrMany]) * L::TEAMS + team;
+  const unsigned int total = p.hdr[kHdrTotal + 1], share = p.hdr[kHdrShare + 1];
+  const unsigned long long begin = static_cast<unsigned long long>(worker) * share;
+  if (begin >= total) return;
+  const unsigned int x0 = static_cast<unsigned int>(begin);
+  const unsigned int x1 = static_cast<unsigned int>(min(begin + share, static_cast<unsigned long long>(total)));
+  const int first = x1 > static_cast<unsigned int>(p.hdr[kHdrLead + 1]) ? p.start[p.ctas + worker] : 0;
+
+  // the ring's filling side (the team's first warp)
+  FewWalk load;
+  FewPiece lp;
+  int lj = 0, issued = 0, lstage = 0;
+  bool more = mt == 0;
+  const int* held_table = nullptr;  // page numbers of 32 tiles of one table row, one per lane
+  int held_base = -1, held_page = 0;
+  if (mt == 0) {
+    load.start(p, x0, x1, first);
+    lp.j1 = 0;
+  }
+  auto fill = [&]() -> bool {  // loads the stretch's next step, if there is one
+    if (lj >= lp.j1) {
+      if (!load.next(p, lane, lp)) {
+        more = false;
+        return true;
+      }
+      lj = lp.j0;
+    }
+    const int tile = lj / (kPage / kStep);
+    if (lp.table != held_table || (tile & ~31) != held_base) {
+      held_table = lp.table;
+      held_base = tile & ~31;
+      held_page = held_base + lane < lp.entries ? lp.table[held_base + lane] : 0;
+    }
+    int pg = __shfl_sync(0xffffffffu, held_page, tile & 31);
+    if (pg < 0 || pg >= p.num_pages) {  // out of the pool: reads zeros and is reported
+      if (lane == 0) atomicOr(&g_prefix_status, kStatusBadPage);
+      pg = p.num_pages;
+    }
+    if (R > 1 && issued >= L::STAGES &&
+        !wait_all(W, bar_empty + 8 * lstage, (issued / L::STAGES - 1) & 1))
+      return false;
+    load_rows2_elect(ring + lstage * L::STEP_BYTES, L::STEP_BYTES / 2, &tmK, &tmV, (lj % (kPage / kStep)) * kStep,
+                     pg * p.Hkv + lp.g, bar_full + 8 * lstage);
+    ++lj;
+    ++issued;
+    if (++lstage == L::STAGES) lstage = 0;
+    return true;
+  };
+  bool ok = true;
+  // one stage behind when other warps read the ring too, so as not to wait for the slowest at every step
+  for (int t = 0; ok && more && t < L::STAGES - (R > 1); ++t) ok = fill();
+
+  const int row0 = mt * 8 * NT, c0 = 2 * (lane & 3);  // this warp's first row; a thread's columns of a product, c0 and c0 + 1
+  const float sl2 = p.scale_log2;
+  // shared-memory words of a 16 x 16 block of K (rows as they are) and of V (transposed), within a step
+  const int k_row = lane & 15, v_row = ((lane >> 4) << 3) + (lane & 7);
+  uint32_t k_at[4], v_at[4];
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    k_at[c] = ring + k_row * 128 + (((2 * c + (lane >> 4)) ^ (k_row & 7)) << 4);
+    v_at[c] = ring + L::STEP_BYTES / 2 + v_row * 128 + (((2 * c + ((lane >> 3) & 1)) ^ (v_row & 7)) << 4);
+  }
+  const uint32_t ones[4] = {0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u};
+  int stage = 0;
+  uint32_t full_par = 0;
+  FewWalk walk;
+  walk.start(p, x0, x1, first);
+  FewPiece q;
+  while (ok && walk.next(p, lane, q)) {
+    uint32_t qf[D / 16][NT][2];  // Q^T
+    int lim[NT][2], lim_min = q.keys;  // keys the thread's rows see (rows past the last one: all, they are not used)
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      const int r = row0 + 8 * t + lane / 4, tok = r / p.group;
+      const __nv_bfloat16* src = p.q + (static_cast<size_t>(q.t0 + tok) * p.H + q.g * p.group + (r - tok * p.group)) * D + c0;
+#pragma unroll
+      for (int kk = 0; kk < D / 16; ++kk) {
+        qf[kk][t][0] = r < q.rows ? *reinterpret_cast<const uint32_t*>(src + kk * 16) : 0u;
+        qf[kk][t][1] = r < q.rows ? *reinterpret_cast<const uint32_t*>(src + kk * 16 + 8) : 0u;
+      }
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int row = row0 + 8 * t + c0 + e;
+        lim[t][e] = row < q.rows ? min(q.keys, q.lim0 + q.step * (row / p.group)) : q.keys;
+        lim_min = min(lim_min, lim[t][e]);
+      }
+    }
+    lim_min = __reduce_min_sync(0xffffffffu, lim_min);
+    // per row: the reference (base-2 units of the scaled score); the sum of the fp32 weights (LSE; this thread's keys);
+    // the sum of the bf16 weights that the product uses (divides O), kept by a product with ones
+    float o[D / 16][NT][4], m[NT][2], l[NT][2], lr[NT][4];
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        m[t][e] = -INFINITY;
+        l[t][e] = 0.f;
+      }
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        lr[t][e] = 0.f;
+#pragma unroll
+        for (int c = 0; c < D / 16; ++c) o[c][t][e] = 0.f;
+      }
+    }
+    for (int j = q.j0; j < q.j1; ++j) {
+      if (!(ok = wait_all(W, bar_full + 8 * stage, (full_par >> stage) & 1))) break;
+      full_par ^= 1u << stage;
+      const uint32_t at = stage * L::STEP_BYTES;
+      const int k0 = j * kStep;
+      float s[NT][4], s2[NT][4];  // two chains of products
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[t][e] = s2[t][e] = 0.f;
+#pragma unroll
+      for (int kk = 0; kk < D / 16; ++kk) {
+        uint32_t a[4];
+        ldmatrix_x4(a, k_at[kk % 4] + at + (kk / 4) * L::BOX);
+#pragma unroll
+        for (int t = 0; t < NT; ++t) mma_16816(kk & 1 ? s2[t] : s[t], a, qf[kk][t][0], qf[kk][t][1]);
+      }
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[t][e] += s2[t][e];
+      if (k0 + kStep > lim_min) {  // some row does not see all of these keys
+        const int key = k0 + lane / 4;
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            if (key >= lim[t][e]) s[t][e] = -INFINITY;
+            if (key + 8 >= lim[t][e]) s[t][2 + e] = -INFINITY;
+          }
+      }
+      float x[NT][2];
+      bool grows = false;
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          x[t][e] = fmaxf(s[t][e], s[t][2 + e]);
+#pragma unroll
+          for (int w = 4; w <= 16; w <<= 1) x[t][e] = fmaxf(x[t][e], __shfl_xor_sync(0xffffffffu, x[t][e], w));
+          x[t][e] *= sl2;
+          grows |= x[t][e] > m[t][e] + 8.f;
+        }
+      // the references are moved, and the sums and O rescaled, only when a maximum grows by more than 2^8
+      if (__any_sync(0xffffffffu, grows)) {
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const float top = x[t][e] > m[t][e] + 8.f ? x[t][e] : m[t][e];
+            const float f = top == -INFINITY ? 1.f : ex2_approx(m[t][e] - top);
+            m[t][e] = top;
+            l[t][e] *= f;
+            lr[t][e] *= f;
+#pragma unroll
+            for (int c = 0; c < D / 16; ++c) {
+              o[c][t][e] *= f;
+              o[c][t][2 + e] *= f;
+            }
+          }
+      }
+      uint32_t pt[NT][2];  // P^T
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        const float z0 = m[t][0] == -INFINITY ? 0.f : -m[t][0], z1 = m[t][1] == -INFINITY ? 0.f : -m[t][1];
+        const float p0 = ex2_approx(fmaf(s[t][0], sl2, z0)), p1 = ex2_approx(fmaf(s[t][1], sl2, z1));
+        const float p2 = ex2_approx(fmaf(s[t][2], sl2, z0)), p3 = ex2_approx(fmaf(s[t][3], sl2, z1));
+        l[t][0] += p0 + p2;
+        l[t][1] += p1 + p3;
+        pt[t][0] = transpose_8x8(pack_bf16x2(p0, p1));
+        pt[t][1] = transpose_8x8(pack_bf16x2(p2, p3));
+        mma_16816(lr[t], ones, pt[t][0], pt[t][1]);
+      }
+      const int left = q.keys - k0;
+      // value rows behind the source's last key may hold anything: they count as 0 (their weights are 0 too)
+      uint32_t v0 = 0xFFFFFFFFu, v1 = 0xFFFFFFFFu;
+      if (left < kStep) {
+        v0 = (c0 < left ? 0xFFFFu : 0u) | (c0 + 1 < left ? 0xFFFF0000u : 0u);
+        v1 = (c0 + 8 < left ? 0xFFFFu : 0u) | (c0 + 9 < left ? 0xFFFF0000u : 0u);
+      }
+#pragma unroll
+      for (int c = 0; c < D / 16; ++c) {
+        uint32_t a[4];
+        ldmatrix_x4_trans(a, v_at[c % 4] + at + (c / 4) * L::BOX);
+        if (left < kStep) {
+          a[0] &= v0;
+          a[1] &= v0;
+          a[2] &= v1;
+          a[3] &= v1;
+        }
+#pragma unroll
+        for (int t = 0; t < NT; ++t) mma_16816(o[c][t], a, pt[t][0], pt[t][1]);
+      }
+      __syncwarp();
+      if (R > 1 && lane == 0) mbar_arrive(bar_empty + 8 * stage);
+      if (++stage == L::STAGES) stage = 0;
+      if (more && !(ok = fill())) break;
+    }
+    if (!ok) break;
+    const size_t slab = few_slab(p, worker, q.dst == kDstSlab1);
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+#pragma unroll
+        for (int w = 4; w <= 16; w <<= 1) l[t][e] += __shfl_xor_sync(0xffffffffu, l[t][e], w);
+        const int r = row0 + 8 * t + c0 + e;
+        if (r >= q.rows) continue;
+        const float inv = lr[t][e] == 0.f ? 0.f : 1.f / lr[t][e];  // no key seen: O = 0 (a NaN sum stays one)
+        const RowOut to = row_out<D>(p, q.dst, slab, q.g, q.t0, r);
+#pragma unroll
+        for (int c = 0; c < D / 16; ++c)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int col = 16 * c + 8 * h + lane / 4;
+            const float y = o[c][t][2 * h + e] * inv;
+            if (to.out)
+              to.out[col] = __float2bfloat16_rn(y);
+            else
+              to.part[col] = y;
+          }
+        if (lane < 4) {
+          const float lse2 = l[t][e] == 0.f ? -INFINITY : m[t][e] + log2f(l[t][e]);
+          *to.lse = to.out ? lse2 * LN2 : lse2;
+        }
+      }
+  }
+  if (!ok && mt == 0)  // let every copy already issued land before the block exits
+    for (int t = 0; t < L::STAGES && t < issued; ++t)
+      drain_all(W, bar_full + 8 * t, ((issued - 1 - t) / L::STAGES) & 1);
+}
+
+template <int D, int NT, int R>
+__global__ void __launch_bounds__(THREADS, 1)
+fa_prefix_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                 const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmK16,
+                 const __grid_constant__ CUtensorMap tmV16, const PrefixParams p) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  if (threadIdx.x == 0) {
+    tma_prefetch_desc(&tmQ);
+    tma_prefetch_desc(&tmK);
+    tma_prefetch_desc(&tmV);
+    tma_prefetch_desc(&tmK16);
+    tma_prefetch_desc(&tmV16);
+  }
+  pdl_launch_dependents();
+  pdl_wait();
+  if (static_cast<int>(blockIdx.x) < p.hdr[kHdrMany])
+    many_rows<D>(tmQ, tmK, tmV, p, smem);
+  else
+    few_rows<D, NT, R>(tmK16, tmV16, p, smem);
+}
+
+// ---------------------------------------------------------------- join
+// W warps join a row, every lane D / 32 columns.  The parts of a row follow from the places of its two items: an
+// item inside one worker's stretch has one part, in the rows of its source; one that is cut has a part in a slab
+// of every worker that worked some of its units.  The lanes look up 32 workers at a time (warp w of W every W-th).
+template <int D, int W>
+__global__ void __launch_bounds__(256) fa_prefix_join_kernel(const PrefixParams p) {
+  constexpr int C = D / 32;
+  __shared__ float s_acc[W > 1 ? 8 : 1][D], s_m[8], s_sum[8];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = warp % W;
+  const long long orow = static_cast<long long>(blockIdx.x) * (8 / W) + warp / W;  // n * H + h
+  pdl_wait();
+  const int tokens = p.hdr[kHdrTokens];
+  if (orow >= static_cast<long long>(tokens) * p.H) return;  // (W > 1: the same row for the whole block)
+  const int n = static_cast<int>(orow / p.H), h = static_cast<int>(orow - static_cast<long long>(n) * p.H);
+  const int g = h / p.group, hh = h - g * p.group;
+  const int4 t = p.tok[n];
+  float m = -INFINITY, sum = 0.f, acc[C];
+#pragma unroll
+  for (int c = 0; c < C; ++c) acc[c] = 0.f;
+  // adds the parts that the lanes have (lse2 = -infinity: none): row `at` of o
+  auto add = [&](float lse2, size_t at, const float* o, int count) {
+    float top = lse2;
+#pragma unroll
+    for (int w = 16; w; w >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, w));
+    top = fmaxf(top, m);
+    const float f = m == -INFINITY ? 0.f : exp2f(m - top), mine = lse2 == -INFINITY ? 0.f : exp2f(lse2 - top);
+    m = top;
+    float all = mine;
+#pragma unroll
+    for (int w = 16; w; w >>= 1) all += __shfl_xor_sync(0xffffffffu, all, w);
+    sum = sum * f + all;
+#pragma unroll
+    for (int c = 0; c < C; ++c) acc[c] *= f;
+#pragma unroll 8
+    for (int k = 0; k < count; ++k) {
+      const float w = __shfl_sync(0xffffffffu, mine, k);
+      const float* src = o + __shfl_sync(0xffffffffu, at, k) * D + lane * C;
+      if (w == 0.f) continue;  // (also lanes without a part)
+      if (C == 4) {
+        const float4 v = *reinterpret_cast<const float4*>(src);
+        acc[0] += w * v.x;
+        acc[1] += w * v.y;
+        acc[2 % C] += w * v.z;
+        acc[3 % C] += w * v.w;
+      } else {
+        const float2 v = *reinterpret_cast<const float2*>(src);
+        acc[0] += w * v.x;
+        acc[1] += w * v.y;
+      }
+    }
+  };
+  // the item's parts: `seen` of its units visible to this row, row `at` of the item, `few`: its line
+  auto join = [&](const Item& it, bool few, int seen, int at, const float* whole, const float* whole_lse) {
+    const unsigned int share = p.hdr[kHdrShare + few];
+    const int first = it.worker(0, share), last = it.worker(it.units - 1, share);
+    if (first == last) {
+      if (sub == 0) add(lane == 0 ? whole_lse[orow] : -INFINITY, orow, whole, 1);
+      return;
+    }
+    for (int w0 = first; w0 <= last; w0 += 32 * W) {
+      const int w = w0 + lane * W + sub;
+      float lse2 = -INFINITY;
+      size_t row = 0;
+      if (w <= last) {
+        const int j0 = it.from(w * share), j1 = it.from((w + 1) * share);
+        if (j0 < j1 && j0 < seen) {
+          row = (few ? few_slab(p, w, j0 == 0) : many_slab(p, w, j0 == 0)) + at;
+          lse2 = p.slab_lse[row];
+        }
+      }
+      add(lse2, row, p.slab_o, min(32, (last - w0 - sub + W) / W));
+    }
+  };
+  if (p.tiles_p > 0) {
+    const bool few = tokens * p.group <= p.few_rows;
+    const int blocks = p.hdr[kHdrBlocks], blk = few ? 0 : n / (2 * p.tp);
+    join(prefix_item(p, tokens, g * blocks + blk), few, few ? INT_MAX : p.tiles_p, (n - blk * 2 * p.tp) * p.group + hh,
+         p.prefix_o, p.prefix_lse);
+  }
+  if (t.z > 0) {
+    const bool few = t.w & kTokFew;
+    Item it{static_cast<unsigned int>(t.x), few ? kFewItemCost : kItemCost, few ? 1u : static_cast<unsigned int>(t.w) >> 16, t.y};
+    it.c0 += g * it.cost();
+    const unsigned int share = p.hdr[kHdrShare + few];
+    if (p.tiles_p == 0 && it.worker(0, share) == it.worker(it.units - 1, share)) return;  // written already
+    join(it, few, t.z, (t.w & (kTokFew - 1)) * p.group + hh, p.own_o, p.own_lse);
+  }
+  if (W > 1) {  // the warps' sums, one after another in the same order
+    s_m[warp] = m;
+    s_sum[warp] = sum;
+#pragma unroll
+    for (int c = 0; c < C; ++c) s_acc[W > 1 ? warp : 0][lane * C + c] = acc[c];
+    __syncthreads();
+    if (warp > 0) return;
+    float top = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < W; ++w) top = fmaxf(top, s_m[w]);
+    sum = 0.f;
+#pragma unroll
+    for (int c = 0; c < C; ++c) acc[c] = 0.f;
+#pragma unroll
+    for (int w = 0; w < W; ++w) {
+      const float f = s_m[w] == -INFINITY ? (s_sum[w] == 0.f ? 0.f : s_sum[w]) : exp2f(s_m[w] - top);
+      sum += f * s_sum[w];
+#pragma unroll
+      for (int c = 0; c < C; ++c) acc[c] += f * s_acc[W > 1 ? w : 0][lane * C + c];
+    }
+    m = top;
+  }
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;
+  __nv_bfloat16* out = p.o + orow * D + lane * C;
+  if (C == 4)
+    *reinterpret_cast<uint2*>(out) =
+        make_uint2(pack_bf16x2(acc[0] * inv, acc[1] * inv), pack_bf16x2(acc[2 % C] * inv, acc[3 % C] * inv));
+  else
+    *reinterpret_cast<uint32_t*>(out) = pack_bf16x2(acc[0] * inv, acc[1] * inv);
+  if (lane == 0) p.lse[orow] = sum == 0.f ? -INFINITY : (m + log2f(sum)) * LN2;
+}
+
+template <int D, int NT, int R>
+static cudaError_t launch(const PrefixMaps& t, const PrefixParams& p, cudaStream_t stream) {
+  constexpr int kSmem = PLayout<D>::SMEM_BYTES > FLayout<D, R>::SMEM_BYTES ? PLayout<D>::SMEM_BYTES : FLayout<D, R>::SMEM_BYTES;
+  static_assert(kSmem <= 232448 && FLayout<D, R>::STAGES >= 3, "shared memory");
   static bool attr_set[64] = {};
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev < 64 && !attr_set[dev]) {
-    e = cudaFuncSetAttribute(fa_prefix_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::SMEM_BYTES);
+    e = cudaFuncSetAttribute(fa_prefix_kernel<D, NT, R>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
     if (e != cudaSuccess) return e;
     attr_set[dev] = true;
   }
@@ -871,21 +1419,31 @@ static cudaError_t launch(const CUtensorMap& qp, const CUtensorMap& qs, const CU
   if ((e = cudaLaunchKernelEx(&cfg, fa_prefix_plan_kernel, p)) != cudaSuccess) return e;
   cfg.gridDim = dim3(p.ctas);
   cfg.blockDim = dim3(THREADS);
-  cfg.dynamicSmemBytes = L::SMEM_BYTES;
-  if ((e = cudaLaunchKernelEx(&cfg, fa_prefix_kernel<D>, qp, qs, k, v, p)) != cudaSuccess) return e;
-  cfg.gridDim = dim3(p.Hkv * ((p.N * p.group + 31) / 32));
-  cfg.blockDim = dim3(D * 4);
+  cfg.dynamicSmemBytes = kSmem;
+  if ((e = cudaLaunchKernelEx(&cfg, fa_prefix_kernel<D, NT, R>, t.q, t.k, t.v, t.k16, t.v16, p)) != cudaSuccess) return e;
+  const long long rows = static_cast<long long>(p.N) * p.H;
+  const bool wide = rows < 1024;  // few rows: a block for each
+  cfg.gridDim = dim3(static_cast<unsigned int>(wide ? rows : (rows + 7) / 8));
+  cfg.blockDim = dim3(256);
   cfg.dynamicSmemBytes = 0;
-  return cudaLaunchKernelEx(&cfg, fa_prefix_join_kernel<D>, p);
+  return wide ? cudaLaunchKernelEx(&cfg, fa_prefix_join_kernel<D, 8>, p)
+              : cudaLaunchKernelEx(&cfg, fa_prefix_join_kernel<D, 1>, p);
 }
 
-cudaError_t launch_fa_fwd_prefix(int d, const CUtensorMap& qp, const CUtensorMap& qs, const CUtensorMap& k,
-                                 const CUtensorMap& v, const PrefixParams& p, cudaStream_t stream) {
-  return d == 64 ? launch<64>(qp, qs, k, v, p, stream) : launch<128>(qp, qs, k, v, p, stream);
+cudaError_t launch_fa_fwd_prefix(int d, const PrefixMaps& t, const PrefixParams& p, cudaStream_t stream) {
+#define FA_LAUNCH(D)                                                                                    \
+  return p.few_rows == 8    ? launch<D, 1, 1>(t, p, stream)                                             \
+         : p.few_rows == 16 ? launch<D, 2, 1>(t, p, stream)                                             \
+         : p.few_rows == 32 ? launch<D, 2, 2>(t, p, stream)                                             \
+                            : launch<D, 2, 4>(t, p, stream)
+  if (d == 64) FA_LAUNCH(64);
+  FA_LAUNCH(128);
+#undef FA_LAUNCH
 }
 
-unsigned int prefix_tile_cost() { return kTileCost; }
+unsigned int prefix_page_cost() { return kTileCost256; }
 unsigned int prefix_item_cost() { return kItemCost; }
+static_assert(kTileCost256 >= kPage / kStep && kItemCost >= kFewItemCost, "prefix_page_cost, prefix_item_cost");
 
 cudaError_t read_and_clear_prefix_status(cudaStream_t stream, unsigned int* out) {
   cudaError_t e = cudaStreamSynchronize(stream);
