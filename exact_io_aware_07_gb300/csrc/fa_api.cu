@@ -458,13 +458,13 @@ fa_status launch_splitkv(Prepared& pr, int d, int num_splits, float* ws, cudaStr
 
 // Workspace of fa_fwd_prefix_paged: byte offsets of its parts (each a multiple of 256).
 struct PrefixWorkspace {
-  size_t cum, tok, slab_o, slab_lse, own_o, own_lse, prefix_o, prefix_lse, bytes;
+  size_t tok, rank, slab_o, slab_lse, own_o, own_lse, prefix_o, prefix_lse, bytes;
   int slab_rows;
 };
 
-PrefixWorkspace prefix_workspace(int N, int B, int H, int Hkv, int d) {
+PrefixWorkspace prefix_workspace(int N, int H, int Hkv, int d) {
   PrefixWorkspace w{};
-  size_t at = 6144;  // the header words and the first request of every worker
+  size_t at = 256;  // the header words
   auto take = [&at](size_t bytes) {
     const size_t here = at;
     at += (bytes + 255) / 256 * 256;
@@ -475,8 +475,8 @@ PrefixWorkspace prefix_workspace(int N, int B, int H, int Hkv, int d) {
   w.slab_rows = static_cast<int>(std::min<long long>(256, item));
   // rows of the slabs of cut items: two per many-row worker (block), two of 128 / 8, / 4 or / 2 rows per team
   const size_t slabs = static_cast<size_t>(fa::kPrefixMaxCtas) * 2 * (w.slab_rows + 128);
-  w.cum = take(static_cast<size_t>(B) * 8);
   w.tok = take(static_cast<size_t>(N) * 16);
+  w.rank = take(static_cast<size_t>(N) * 4);
   w.slab_o = take(slabs * d * 4);
   w.slab_lse = take(slabs * 4);
   w.own_o = take(rows * d * 4);
@@ -486,7 +486,6 @@ PrefixWorkspace prefix_workspace(int N, int B, int H, int Hkv, int d) {
   w.bytes = at;
   return w;
 }
-static_assert(6144 >= (64 + fa::kPrefixMaxCtas * (1 + 8)) * 4, "workspace header");
 
 }  // namespace
 
@@ -853,7 +852,7 @@ fa_status fa_kv_append(const void* k_new, const void* v_new, const int* slot_map
 
 size_t fa_fwd_prefix_paged_workspace_bytes(int N, int B, int H, int Hkv, int d) {
   if (N < 1 || B < 1 || H < 1 || Hkv < 1 || H % Hkv != 0 || (d != 64 && d != 128)) return 0;
-  return prefix_workspace(N, B, H, Hkv, d).bytes;
+  return prefix_workspace(N, H, Hkv, d).bytes;
 }
 
 fa_status fa_fwd_prefix_paged(const void* q, const void* k_pages, const void* v_pages, const int* prefix_table,
@@ -873,7 +872,8 @@ fa_status fa_fwd_prefix_paged(const void* q, const void* k_pages, const void* v_
   // tokens of a 128-row tile; the most places the work can take on the lines that the SMs share
   const int group = H / Hkv, tp = std::min(128 / group, N);
   const double page = fa::prefix_page_cost(), item = fa::prefix_item_cost();
-  const double places = static_cast<double>(Hkv) * ((N / (2 * tp) + 1.0) * (item + page * (prefix_len / fa::kPage + 1.0)) +
+  const double prefix_places = item + page * (prefix_len / fa::kPage + 1.0);
+  const double places = static_cast<double>(Hkv) * (2.0 * (N / (2 * tp) + 1.0) * prefix_places +
                                                     (N / (2 * tp) + static_cast<double>(B)) * (item + page * max_pages));
   if (places > INT_MAX) return FA_ERR_BAD_SHAPE;
   if (!std::isfinite(scale) || !(scale > 0.f)) return FA_ERR_BAD_SCALE;
@@ -922,12 +922,11 @@ fa_status fa_fwd_prefix_paged(const void* q, const void* k_pages, const void* v_
   p.teams = p.few_rows <= 16 ? 8 : p.few_rows == 32 ? 4 : 2;
   p.tiles_p = static_cast<int>(prefix_pages);
   p.tp = tp;
-  const PrefixWorkspace w = prefix_workspace(N, B, H, Hkv, d);
+  const PrefixWorkspace w = prefix_workspace(N, H, Hkv, d);
   char* base = static_cast<char*>(workspace);
   p.hdr = reinterpret_cast<int*>(base);
-  p.start = p.hdr + 64;
-  p.cum = reinterpret_cast<unsigned int*>(base + w.cum);
   p.tok = reinterpret_cast<int4*>(base + w.tok);
+  p.rank = reinterpret_cast<int*>(base + w.rank);
   p.slab_rows = w.slab_rows;
   p.slab_o = reinterpret_cast<float*>(base + w.slab_o);
   p.slab_lse = reinterpret_cast<float*>(base + w.slab_lse);

@@ -59,10 +59,9 @@ struct PrefixParams {
   int tp;        // tokens of a 128-row tile
   // workspace
   int* hdr;           // kHdr* words
-  int* start;         // [ctas][ctas * teams] the request a many-row, few-row worker's own keys begin with
-  unsigned int* cum;  // [2][B] place of the request's first item on the many-row, few-row line
   int4* tok;          // [N] place of the token's own item (K/V head 0), its units, the units that the token's row
                       // tile sees, the token's number in the item | kTokFew | places of a unit << 16
+  int* rank;          // [N] the token's item of the prefix (K/V head 0); -1: none
   int slab_rows;      // rows of a many-row slab
   float* slab_o;      // [ctas][2][slab_rows][d], then [ctas * teams][2][few_rows][d]: parts of cut items
   float* slab_lse;    // the same rows, base-2

@@ -7,17 +7,21 @@
 // which is the softmax over all keys, so that the prefix can be worked once for the rows of the whole
 // batch and the own keys request by request.
 //
-// Three kernels on the stream, each starting its set-up while the one before it ends:
-//   fa_prefix_plan_kernel  lays out the work from the device lengths,
-//   fa_prefix_kernel       one block per SM, the attention over its share of the keys,
-//   fa_prefix_join_kernel  joins the parts of every row.
+// Two kernels on the stream: fa_prefix_kernel, one block per SM, lays out the work from the device lengths
+// (every block for itself) and works its share of the keys; fa_prefix_join_kernel joins the parts of the rows
+// that have several.
 //
-// The work is a list of items: (K/V head, rows, the keys of one source), rows being (token, query head)
-// pairs, `group` of them per token.  Over the prefix an item holds rows of any requests, over own keys
-// those of one request.  There are two kinds, and every block works one of them:
+// The work is a list of items: (K/V head, rows, keys), rows being (token, query head) pairs, `group` of them
+// per token.  A request is few (up to 8, 16, 32 or 64 rows: a decoding request, a few drafted tokens), big
+// (from kBigRows rows on: a prompt chunk) or between.  The items are
+//   the prefix for blocks of up to 256 rows of any requests (a key tile is loaded once for all of them),
+//   the own keys of a few or between request,
+//   the prefix and then the own keys of up to 256 rows of a big request (it fills row tiles by itself, so its
+//   rows need no second item and no join).
+// There are two kinds of them, and every block works one of them:
 //   many rows: up to 256 rows on tcgen05 products, keys in tiles of 128 (bound by the tensor core);
-//   few rows:  up to 8, 16, 32 or 64 rows (a decoding request, a few drafted tokens) on warp-level products,
-//              keys in steps of 16, by teams of one, two or four warps (bound by loading the keys).
+//   few rows:  the items of few requests (and the prefix, when all rows together are few) on warp-level
+//              products, keys in steps of 16, by teams of one, two or four warps (bound by loading the keys).
 // The items of a kind stand on a line, a key tile or step and an item taking so many places each, and the
 // kind's workers (blocks, or teams) get equal stretches of it: worker w the tiles whose places begin in
 // [w Q, (w + 1) Q).  So all workers have the same share whatever the lengths, and at most two items of a
@@ -34,15 +38,21 @@ static __device__ unsigned int g_prefix_status;  // kStatus* bits
 
 // Places on the lines.  Many rows: an item, and a key tile of an item with up to 128 and more rows; few rows: an
 // item, and one per step.  kManyTime / kFewTime: time of a place of either kind on one SM, for sharing out the SMs.
-constexpr unsigned int kItemCost = 4, kTileCost128 = 6, kTileCost256 = 8;
+constexpr unsigned int kItemCost = 8, kTileCost128 = 6, kTileCost256 = 8;
 constexpr unsigned int kFewItemCost = 4, kFewLeast = 4;  // (at least kFewLeast places for a team)
 constexpr float kManyTime = 0.2f, kFewTime = 0.08f;
-constexpr int kStep = 16;  // keys per step of the few-row kind
+constexpr int kStep = 16;       // keys per step of the few-row kind
+constexpr int kBigRows = 128;   // rows from which a request is big
+constexpr int kMaxFlags = 1024; // row blocks of the batch whose need of the prefix is looked at one by one
 // words of p.hdr (two each where the lines have their own: many rows, few rows)
-enum { kHdrTotal = 0, kHdrShare = 2, kHdrLead = 4, kHdrMany = 6, kHdrBlocks, kHdrTokens };
+enum { kHdrShare = 0, kHdrPrefixItems = 2, kHdrTokens };
 constexpr int kTokFew = 1 << 15;  // in a token's fourth word: its item is on the few-row line
 
-__device__ __forceinline__ unsigned int tile_cost(int rows) { return rows <= 128 ? kTileCost128 : kTileCost256; }
+constexpr int THREADS = 320;
+constexpr int BM = 128, BN = 128;
+constexpr int BOX_BYTES = 128 * 128;  // 128 rows x 64 bf16, 128-byte swizzle
+constexpr float LN2 = 0.693147180559945309f;
+
 // A line's item: its first place, places before its first unit (tile or step), places per unit, units.
 struct Item {
   unsigned int c0, lead, unit;
@@ -58,7 +68,9 @@ struct Item {
     return static_cast<int>((c0 + lead + unit * unit_index) / share);
   }
 };
-__device__ __forceinline__ Item many_item(unsigned int c0, int tiles, unsigned int tile) { return Item{c0, kItemCost, tile, tiles}; }
+__device__ __forceinline__ Item many_item(unsigned int c0, int tiles, int rows) {
+  return Item{c0, kItemCost, rows <= 128 ? kTileCost128 : kTileCost256, tiles};
+}
 __device__ __forceinline__ Item few_item(unsigned int c0, int keys) {
   return Item{c0, kFewItemCost, 1u, (keys + kStep - 1) / kStep};
 }
@@ -74,173 +86,251 @@ __device__ __forceinline__ Request make_request(const PrefixParams& p, int cu0, 
   return r;
 }
 __device__ __forceinline__ bool is_few(const PrefixParams& p, const Request& r) { return r.added * p.group <= p.few_rows; }
+__device__ __forceinline__ bool is_big(const PrefixParams& p, const Request& r) { return r.added * p.group >= kBigRows; }
 __device__ __forceinline__ int tiles_of(int keys) { return (keys + kPage - 1) / kPage; }
 // Own keys that the tokens before the request's token `end` (exclusive) can see at most.
 __device__ __forceinline__ int visible(const PrefixParams& p, const Request& r, int end) {
   return p.causal ? max(0, min(r.len, r.len - r.added + end)) : r.len;
 }
-// The item (of K/V head 0, at c0) of a many-row request's block of 2 tp tokens.
+// The item (of K/V head 0, at c0) of a many-row request's block of 2 tp tokens; a big request's begins with the prefix.
 __device__ __forceinline__ Item block_item(const PrefixParams& p, const Request& r, int blk, unsigned int c0) {
   const int end = min(r.added, (blk + 1) * 2 * p.tp);
-  return many_item(c0, tiles_of(visible(p, r, end)), tile_cost((end - blk * 2 * p.tp) * p.group));
+  return many_item(c0, (is_big(p, r) ? p.tiles_p : 0) + tiles_of(visible(p, r, end)), (end - blk * 2 * p.tp) * p.group);
 }
-// Items of the prefix: many-row blocks of 2 tp tokens (each counted as a full one unless it is the only one), or
-// one few-row item, per K/V head.
+// A request's places on its line.
+__device__ __forceinline__ unsigned int request_cost(const PrefixParams& p, const Request& r) {
+  if (r.added == 0) return 0u;
+  if (is_few(p, r)) return few_item(0, visible(p, r, r.added)).cost() * p.Hkv;
+  unsigned int sum = 0;
+  for (int blk = 0; blk * 2 * p.tp < r.added; ++blk) sum += block_item(p, r, blk, 0).cost();
+  return sum * p.Hkv;
+}
+// The prefix's items: per K/V head one few-row item when all rows of the batch together are few, else one of each
+// needed block of 2 tp tokens (each counted as a full one unless the batch is smaller).
+__device__ __forceinline__ bool few_prefix(const PrefixParams& p, int tokens) { return tokens * p.group <= p.few_rows; }
 __device__ __forceinline__ Item prefix_item(const PrefixParams& p, int tokens, unsigned int index) {
-  Item it = tokens * p.group <= p.few_rows ? few_item(0, p.prefix_len)
-                                           : many_item(0, p.tiles_p, tile_cost(min(2 * p.tp, tokens) * p.group));
+  Item it = few_prefix(p, tokens) ? few_item(0, p.prefix_len) : many_item(0, p.tiles_p, min(2 * p.tp, tokens) * p.group);
   it.c0 = index * it.cost();
   return it;
 }
 
-// ---------------------------------------------------------------- plan
-// Every block forms the running sums of the requests' places on both lines, kPlanThreads requests at a time;
-// block 0 writes them out with the shares and the request each worker begins with, and the blocks share out the
-// tokens, whose item the join needs.
-constexpr int kPlanThreads = 512;
+// ---------------------------------------------------------------- layout of the work
+// Every block forms the running sums of the requests' places on both lines (a thread has a run of requests), finds
+// the requests that its own workers begin with, and the blocks share out the tokens, whose item the join needs.
+struct Layout {                // in shared memory until the roles begin
+  unsigned long long cum[THREADS];  // places before the thread's first request: many rows, few rows << 32
+  int first[THREADS];               // the first new token of it
+  unsigned long long warp[THREADS / 32];
+  unsigned int need[kMaxFlags / 32];  // bit: a block of 2 tp tokens has tokens of requests that are not big
+};
+struct Begin {  // what a worker begins with
+  int b;             // request
+  unsigned int c0;   // its first place
+};
+struct Plan {
+  unsigned int total[2], share[2], lead[2];  // lead: the prefix's places
+  int many, tokens, blocks, items;           // blocks that work many rows; new tokens; row blocks; needed ones
+};
 
-__global__ void __launch_bounds__(kPlanThreads) fa_prefix_plan_kernel(const PrefixParams p) {
-  __shared__ unsigned int s_cum[2][kPlanThreads];
-  __shared__ int s_first[kPlanThreads], s_added[kPlanThreads], s_len[kPlanThreads];
-  __shared__ unsigned long long s_warp[kPlanThreads / 32];
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  pdl_launch_dependents();
-  pdl_wait();
-  const int end = p.cu_new[p.B], tokens = min(max(end, 0), p.N);
-  const bool few_prefix = tokens * p.group <= p.few_rows;
-  const int blocks = few_prefix ? 1 : (tokens + 2 * p.tp - 1) / (2 * p.tp);
-  const unsigned int prefix_cost = tokens == 0 ? 0u : static_cast<unsigned int>(p.Hkv) * blocks * prefix_item(p, tokens, 0).cost();
-  const unsigned int lead[2] = {few_prefix ? 0u : prefix_cost, few_prefix ? prefix_cost : 0u};
-  bool bad = end > p.N || end < 0 || p.cu_new[0] != 0;
-  const bool one = p.B <= kPlanThreads;  // a single round: the sums are known before they are used
-  unsigned int total[2] = {0, 0}, share[2] = {1, 1};
-  int many = 0;  // blocks that work the many-row line
-  auto share_out = [&] {
-    const float a = kManyTime * total[0], b = kFewTime * total[1];
-    many = total[0] == 0 ? 0 : total[1] == 0 ? p.ctas : max(1, min(p.ctas - 1, __float2int_rn(p.ctas * a / (a + b))));
-    share[0] = max(1u, (total[0] + max(many, 1) - 1) / max(many, 1));
-    const unsigned int teams = max(1, (p.ctas - many) * p.teams);
-    share[1] = max(kFewLeast, (total[1] + teams - 1) / teams);
-  };
-  for (int pass = one ? 1 : 0; pass < 2; ++pass) {  // pass 0 only sums
-    unsigned long long carry = lead[0] | static_cast<unsigned long long>(lead[1]) << 32;  // many-row, few-row << 32
-    for (int b0 = 0; b0 < p.B; b0 += kPlanThreads) {
-      const int b = b0 + tid, count = min(kPlanThreads, p.B - b0);
-      Request r{0, 0, 0};
-      unsigned long long mine = 0;
-      if (b < p.B) {
-        const int c0 = p.cu_new[b], c1 = p.cu_new[b + 1], seq = p.seq_lens[b];
-        bad |= c1 < c0 || seq < 0 || seq > p.max_pages * kPage;
-        r = make_request(p, c0, c1, seq);
-        if (!is_few(p, r)) {
-          unsigned int sum = 0;
-          for (int blk = 0; blk * 2 * p.tp < r.added; ++blk) sum += block_item(p, r, blk, 0).cost();
-          mine = sum * p.Hkv;
-        } else if (r.added > 0) {
-          mine = static_cast<unsigned long long>(few_item(0, visible(p, r, r.added)).cost() * p.Hkv) << 32;
-        }
-      }
-      unsigned long long sum = mine;
-#pragma unroll
-      for (int w = 1; w < 32; w <<= 1) {
-        const unsigned long long t = __shfl_up_sync(0xffffffffu, sum, w);
-        if (lane >= w) sum += t;
-      }
-      if (lane == 31) s_warp[warp] = sum;
-      __syncthreads();
-      unsigned long long before = 0, all = 0;
-#pragma unroll
-      for (int w = 0; w < kPlanThreads / 32; ++w) {
-        const unsigned long long t = s_warp[w];
-        before += w < warp ? t : 0u;
-        all += t;
-      }
-      const unsigned long long cum = carry + before + sum - mine;
-      const unsigned int begin[2] = {static_cast<unsigned int>(carry), static_cast<unsigned int>(carry >> 32)};
-      carry += all;
-      if (pass == 1) {
-        s_cum[0][tid] = static_cast<unsigned int>(cum);
-        s_cum[1][tid] = static_cast<unsigned int>(cum >> 32);
-        s_first[tid] = r.first;
-        s_added[tid] = r.added;
-        s_len[tid] = r.len;
-        if (blockIdx.x == 0 && b < p.B) {
-          p.cum[b] = static_cast<unsigned int>(cum);
-          p.cum[p.B + b] = static_cast<unsigned int>(cum >> 32);
-        }
-        if (one) {
-          total[0] = static_cast<unsigned int>(carry);
-          total[1] = static_cast<unsigned int>(carry >> 32);
-          share_out();
-        }
-      }
-      __syncthreads();
-      if (pass == 0) continue;
-      if (blockIdx.x == 0)  // the request that holds the first own place of every worker
-        for (int w = tid; w < p.ctas * (1 + p.teams); w += kPlanThreads) {
-          const int kind = w >= p.ctas, worker = kind ? w - p.ctas : w;
-          const unsigned long long at = static_cast<unsigned long long>(worker) * share[kind];
-          const unsigned int x = static_cast<unsigned int>(max(at, static_cast<unsigned long long>(lead[kind])));
-          if (at >= total[kind] || x < begin[kind] || x >= static_cast<unsigned int>(kind ? carry >> 32 : carry)) continue;
-          int lo = 0, hi = count;  // the last request beginning at or before x
-          while (hi - lo > 1) {
-            const int mid = (lo + hi) >> 1;
-            if (s_cum[kind][mid] <= x)
-              lo = mid;
-            else
-              hi = mid;
-          }
-          p.start[w] = b0 + lo;
-        }
-      const int n_begin = b0 == 0 ? 0 : s_first[0], n_end = s_first[count - 1] + s_added[count - 1];
-      for (int n = n_begin + blockIdx.x * kPlanThreads + tid; n < n_end; n += gridDim.x * kPlanThreads) {
-        int lo = 0, hi = count;  // the last request whose first token is at or before n
-        while (hi - lo > 1) {
-          const int mid = (lo + hi) >> 1;
-          if (s_first[mid] <= n)
-            lo = mid;
-          else
-            hi = mid;
-        }
-        const Request q{s_first[lo], s_added[lo], s_len[lo]};
-        const int i = n - q.first;
-        int4 t = make_int4(0, 0, 0, 0);  // no own key
-        if (i >= 0 && i < q.added) {
-          if (is_few(p, q)) {
-            const Item it = few_item(s_cum[1][lo], visible(p, q, q.added));
-            t = make_int4(static_cast<int>(it.c0), it.units, it.units, i | kTokFew);
-          } else {
-            const int blk = i / (2 * p.tp);
-            unsigned int c0 = s_cum[0][lo];
-            for (int k = 0; k < blk; ++k) c0 += p.Hkv * block_item(p, q, k, 0).cost();
-            const Item it = block_item(p, q, blk, c0);
-            t = make_int4(static_cast<int>(c0), it.units, tiles_of(visible(p, q, min(q.added, (i / p.tp + 1) * p.tp))),
-                          (i - blk * 2 * p.tp) | static_cast<int>(it.unit) << 16);
-          }
-        }
-        p.tok[n] = t;
-      }
-      __syncthreads();
+__device__ __forceinline__ bool flagged(const PrefixParams& p, int blocks) { return blocks <= kMaxFlags; }
+// The needed block with `rank` needed ones before it.
+__device__ __forceinline__ int needed_block(const PrefixParams& p, const volatile unsigned int* need, int blocks, int rank) {
+  if (!flagged(p, blocks)) return rank;
+  for (int w = 0; w < kMaxFlags / 32; ++w) {
+    unsigned int bits = need[w];
+    const int n = __popc(bits);
+    if (rank < n) {
+      for (; rank; --rank) bits &= bits - 1;
+      return w * 32 + __ffs(bits) - 1;
     }
-    total[0] = static_cast<unsigned int>(carry);
-    total[1] = static_cast<unsigned int>(carry >> 32);
-    share_out();
+    rank -= n;
   }
-  if (blockIdx.x == 0 && tid == 0) {
-    p.hdr[kHdrTotal] = static_cast<int>(total[0]);
-    p.hdr[kHdrTotal + 1] = static_cast<int>(total[1]);
-    p.hdr[kHdrShare] = static_cast<int>(share[0]);
-    p.hdr[kHdrShare + 1] = static_cast<int>(share[1]);
-    p.hdr[kHdrLead] = static_cast<int>(lead[0]);
-    p.hdr[kHdrLead + 1] = static_cast<int>(lead[1]);
-    p.hdr[kHdrMany] = many;
-    p.hdr[kHdrBlocks] = blocks;
-    p.hdr[kHdrTokens] = tokens;
-  }
-  if (bad && blockIdx.x == 0) atomicOr(&g_prefix_status, kStatusBadLength);
+  return 0;  // (never: rank is below the number of needed blocks)
 }
 
-// ---------------------------------------------------------------- attention
+__device__ __forceinline__ Plan make_plan(const PrefixParams& p, Layout& s, volatile unsigned int* need, Begin* begin) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int run = (p.B + THREADS - 1) / THREADS, b_lo = min(p.B, tid * run), b_hi = min(p.B, b_lo + run);
+  Plan l;
+  const int end = p.cu_new[p.B];
+  l.tokens = min(max(end, 0), p.N);
+  const bool few = few_prefix(p, l.tokens);
+  l.blocks = few ? 1 : (l.tokens + 2 * p.tp - 1) / (2 * p.tp);
+  bool bad = end > p.N || end < 0;
+  unsigned long long mine = 0;
+  int first = p.N;
+  for (int b = b_lo; b < b_hi; ++b) {
+    const int c0 = p.cu_new[b], c1 = p.cu_new[b + 1], seq = p.seq_lens[b];
+    bad |= c1 < c0 || seq < 0 || seq > p.max_pages * kPage || (b == 0 && c0 != 0);
+    const Request r = make_request(p, c0, c1, seq);
+    if (b == b_lo) first = r.first;
+    mine += static_cast<unsigned long long>(request_cost(p, r)) << (is_few(p, r) ? 32 : 0);
+    if (r.added > 0 && !is_big(p, r) && flagged(p, l.blocks))
+      for (int k = r.first / (2 * p.tp); k <= (r.first + r.added - 1) / (2 * p.tp) && k < l.blocks; ++k)
+        atomicOr(const_cast<unsigned int*>(need) + k / 32, 1u << (k % 32));
+  }
+  unsigned long long sum = mine;
+#pragma unroll
+  for (int w = 1; w < 32; w <<= 1) {
+    const unsigned long long t = __shfl_up_sync(0xffffffffu, sum, w);
+    if (lane >= w) sum += t;
+  }
+  if (lane == 31) s.warp[warp] = sum;
+  __syncthreads();
+  l.items = l.blocks;
+  if (few)
+    l.items = 1;
+  else if (flagged(p, l.blocks)) {
+    l.items = 0;
+    for (int w = 0; w * 32 < l.blocks; ++w) l.items += __popc(need[w]);
+  }
+  if (l.tokens == 0) l.items = 0;
+  const unsigned int prefix = l.items == 0 ? 0u : static_cast<unsigned int>(p.Hkv) * l.items * prefix_item(p, l.tokens, 0).cost();
+  l.lead[0] = few ? 0u : prefix;
+  l.lead[1] = few ? prefix : 0u;
+  unsigned long long before = l.lead[0] | static_cast<unsigned long long>(l.lead[1]) << 32, all = before;
+#pragma unroll 2
+  for (int w = 0; w < THREADS / 32; ++w) {
+    const unsigned long long t = s.warp[w];
+    before += w < warp ? t : 0u;
+    all += t;
+  }
+  l.total[0] = static_cast<unsigned int>(all);
+  l.total[1] = static_cast<unsigned int>(all >> 32);
+  s.cum[tid] = before + sum - mine;
+  s.first[tid] = first;
+  const float a = kManyTime * l.total[0], b = kFewTime * l.total[1];
+  l.many = l.total[0] == 0 ? 0 : l.total[1] == 0 ? p.ctas : max(1, min(p.ctas - 1, __float2int_rn(p.ctas * a / (a + b))));
+  l.share[0] = max(1u, (l.total[0] + max(l.many, 1) - 1) / max(l.many, 1));
+  const unsigned int teams = max(1, (p.ctas - l.many) * p.teams);
+  l.share[1] = max(kFewLeast, (l.total[1] + teams - 1) / teams);
+  __syncthreads();
+  // the last thread with requests whose key is not above x
+  auto owner = [&](auto key, unsigned int x) {
+    int lo = 0, hi = (p.B + run - 1) / run;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (key(mid) <= x)
+        lo = mid;
+      else
+        hi = mid;
+    }
+    return lo;
+  };
+  auto request = [&](int b) { return make_request(p, p.cu_new[b], p.cu_new[b + 1], p.seq_lens[b]); };
+  const int kind = static_cast<int>(blockIdx.x) >= l.many;
+  if (tid < (kind ? p.teams : 1)) {  // the request that holds this block's worker's first own place
+    const unsigned long long at =
+        static_cast<unsigned long long>(kind ? (blockIdx.x - l.many) * p.teams + tid : blockIdx.x) * l.share[kind];
+    if (at < l.total[kind]) {
+      const unsigned int x = max(static_cast<unsigned int>(at), l.lead[kind]);
+      auto place = [&](int t) { return static_cast<unsigned int>(s.cum[t] >> (32 * kind)); };
+      const int t = owner(place, x);
+      Begin w{t * run, place(t)};
+      for (const int last = min(p.B, (t + 1) * run) - 1; w.b < last; ++w.b) {
+        const Request r = request(w.b);
+        const unsigned int c = is_few(p, r) == static_cast<bool>(kind) ? request_cost(p, r) : 0u;
+        if (w.c0 + c > x) break;
+        w.c0 += c;
+      }
+      begin[tid] = w;
+    }
+  }
+  for (int n = blockIdx.x + gridDim.x * tid; n < l.tokens; n += gridDim.x * THREADS) {
+    const int t = owner([&](int k) { return static_cast<unsigned int>(s.first[k]); }, n);
+    unsigned int c0[2] = {static_cast<unsigned int>(s.cum[t]), static_cast<unsigned int>(s.cum[t] >> 32)};
+    int b = t * run;
+    Request r = request(b);
+    for (const int last = min(p.B, (t + 1) * run) - 1; b < last; ++b) {
+      const Request next = request(b + 1);
+      if (next.first > n) break;
+      c0[is_few(p, r)] += request_cost(p, r);
+      r = next;
+    }
+    const int i = n - r.first;
+    int4 tok = make_int4(0, 0, 0, 0);  // no own key
+    int rank = -1;                     // no item of the prefix
+    if (i >= 0 && i < r.added) {
+      if (is_few(p, r)) {
+        const Item it = few_item(c0[1], visible(p, r, r.added));
+        tok = make_int4(static_cast<int>(it.c0), it.units, it.units, i | kTokFew);
+      } else {
+        const int blk = i / (2 * p.tp);
+        unsigned int c = c0[0];
+        for (int k = 0; k < blk; ++k) c += p.Hkv * block_item(p, r, k, 0).cost();
+        const Item it = block_item(p, r, blk, c);
+        tok = make_int4(static_cast<int>(c), it.units,
+                        (is_big(p, r) ? p.tiles_p : 0) + tiles_of(visible(p, r, min(r.added, (i / p.tp + 1) * p.tp))),
+                        (i - blk * 2 * p.tp) | static_cast<int>(it.unit) << 16);
+      }
+      if (p.tiles_p > 0 && !is_big(p, r)) {
+        rank = few ? 0 : n / (2 * p.tp);
+        if (!few && flagged(p, l.blocks)) {
+          const int blk = rank;
+          rank = __popc(need[blk / 32] & ((1u << (blk % 32)) - 1));
+          for (int w = 0; w < blk / 32; ++w) rank += __popc(need[w]);
+        }
+      }
+    }
+    p.tok[n] = tok;
+    p.rank[n] = rank;
+  }
+  if (blockIdx.x == 0) {
+    if (tid == 0) {
+      p.hdr[kHdrShare] = static_cast<int>(l.share[0]);
+      p.hdr[kHdrShare + 1] = static_cast<int>(l.share[1]);
+      p.hdr[kHdrPrefixItems] = l.items;
+      p.hdr[kHdrTokens] = l.tokens;
+    }
+    if (bad) atomicOr(&g_prefix_status, kStatusBadLength);
+  }
+  fence_proxy_async_smem();  // the tiles will be loaded over what the layout wrote
+  __syncthreads();
+  return l;
+}
+
+// ---------------------------------------------------------------- parts
+// Where a row's part goes: `out` (the row itself, in bf16) or `part`, and the LSE at `lse` (natural for the row
+// itself, base-2 for a part).
+enum { kDstOutput, kDstSlab0, kDstSlab1, kDstOwn, kDstPrefix };
+// First slab row of worker `w` of a kind for its first (0) or last (1) cut item.
+__device__ __forceinline__ size_t many_slab(const PrefixParams& p, int w, int which) {
+  return (static_cast<size_t>(w) * 2 + which) * p.slab_rows;
+}
+__device__ __forceinline__ size_t few_slab(const PrefixParams& p, int w, int which) {
+  return static_cast<size_t>(p.ctas) * 2 * p.slab_rows + (static_cast<size_t>(w) * 2 + which) * p.few_rows;
+}
+struct RowOut {
+  __nv_bfloat16* out;
+  float* part;
+  float* lse;
+};
+// Row `row` of an item at token t0 and K/V head g; `slab`: the slab's first row.
+template <int D>
+__device__ __forceinline__ RowOut row_out(const PrefixParams& p, int dst, size_t slab, int g, int t0, int row) {
+  if (dst == kDstSlab0 || dst == kDstSlab1) return RowOut{nullptr, p.slab_o + (slab + row) * D, p.slab_lse + slab + row};
+  const int t = row / p.group;
+  const size_t orow = static_cast<size_t>(t0 + t) * p.H + g * p.group + (row - t * p.group);
+  if (dst == kDstOutput) return RowOut{p.o + orow * D, nullptr, p.lse + orow};
+  if (dst == kDstOwn) return RowOut{nullptr, p.own_o + orow * D, p.own_lse + orow};
+  return RowOut{nullptr, p.prefix_o + orow * D, p.prefix_lse + orow};
+}
+
+__device__ __forceinline__ float u2f(uint32_t x) { return __uint_as_float(x); }
+__device__ __forceinline__ uint32_t f2u(float x) { return __float_as_uint(x); }
+// 16 lanes x 64 columns of Tensor Memory: of every eight columns lane l gets columns 2 (l % 4) and the next, of rows l / 4
+// (two registers) and l / 4 + 8 (two more).
+__device__ __forceinline__ void tmem_ld_16x256b_x8_wait(uint32_t taddr, uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr) : "memory");
+}
+// The value of lane 0, known to be the same for the whole warp (tensor-core and TMA operands are warp-uniform).
+__device__ __forceinline__ int uni(int x) { return __shfl_sync(0xffffffffu, x, 0); }
+
+// ---------------------------------------------------------------- many rows
 // One lane loads a box of a page pool ((64, 128 rows, d / 64, planes) view: the 64-column halves of the box's rows one
 // behind the other) and adds its bytes to what `bar` expects.
 __device__ __forceinline__ void load_rows_elect(uint32_t dst, const void* tmap, int row, int plane, uint32_t bar, uint32_t bytes) {
@@ -272,24 +362,22 @@ __device__ __forceinline__ void load_rows2_elect(uint32_t dst, uint32_t half, co
 //   one row tile: the slots take its key tiles in turn, so that one's softmax overlaps the other's
 //   products, and slot 0 joins both results at the end.
 // Tensor Memory (512 columns): S_0 [0,128), S_1 [128,256), O_0, O_1 from 256; P_i (bf16 pairs) over S_i.
-constexpr int BM = 128, BN = 128;
-constexpr int PRODUCER_WARP = 8, MMA_WARP = 9, THREADS = 320;
-constexpr int BOX_BYTES = 128 * 128;  // 128 rows x 64 bf16, 128-byte swizzle
-constexpr float LN2 = 0.693147180559945309f;
+constexpr int PRODUCER_WARP = 8, MMA_WARP = 9;
 constexpr int kPieceSlots = 3;
 
 struct __align__(16) Piece {
   int mode;          // 0: no more pieces, 1: one row tile, 2: two row tiles
   int n, n0, n1;     // key tiles of the piece; visited by slot 0 / slot 1
   int j0;            // first key tile
-  int keys;          // keys of the source
+  int ptiles;        // tiles below are the prefix's, the rest own keys from tile 0 on
+  int keys;          // own keys
   int lim0, step;    // the item's token i sees min(keys, lim0 + i * step) of them
   int t0;            // the item's first token
   int rows0, rows1;  // rows of tile 0 / tile 1
   int g;             // K/V head
   int dst;           // where the part goes: kDst*
   int tile_rows;     // rows of a full row tile
-  int pad0, pad1;
+  int pad;
 };
 
 template <int D>
@@ -298,58 +386,33 @@ struct PLayout {
   static constexpr int BOXES = D / 64;
   static constexpr int STAGES = D == 128 ? 5 : 10;
   static constexpr int KV_OFF = 2 * TILE_BYTES;  // after the two query tiles
-  static constexpr int XCH_OFF = KV_OFF + STAGES * TILE_BYTES;  // slot 1's (m, l, lr) of one-tile pieces
+  static constexpr int XCH_OFF = 224 * 1024;  // behind both kinds' rings: slot 1's (m, l, lr) of one-tile pieces
+  static_assert(KV_OFF + STAGES * TILE_BYTES <= XCH_OFF, "the ring reaches into what follows it");
   static constexpr int PIECE_OFF = XCH_OFF + 128 * 12;
   static constexpr int BAR_OFF = PIECE_OFF + kPieceSlots * int(sizeof(Piece));
   // q_full, q_empty, kv_full[S], kv_empty[S], s_full[2], p_full[2], o_full[2], o_empty[2], x_full[4], done,
   // piece_full[], piece_empty[]
   static constexpr int NUM_BARS = 2 + 2 * STAGES + 8 + 4 + 1 + 2 * kPieceSlots;
   static constexpr int MISC_OFF = BAR_OFF + NUM_BARS * 8;  // TMEM base, abort flag
-  static constexpr int SMEM_BYTES = MISC_OFF + 16 + 1024;
-};
-static_assert(PLayout<64>::SMEM_BYTES <= 232448 && PLayout<128>::SMEM_BYTES <= 232448, "shared memory");
+  static constexpr int END = MISC_OFF + 16;
 
-__device__ __forceinline__ float u2f(uint32_t x) { return __uint_as_float(x); }
-__device__ __forceinline__ uint32_t f2u(float x) { return __float_as_uint(x); }
-
-// Where a row's part goes: `out` (the row itself, in bf16) or `part`, and the LSE at `lse` (natural for the
-// row itself, base-2 for a part).  slab: the worker's slab for cut items (slab_o / slab_lse at its first row).
-enum { kDstOutput, kDstSlab0, kDstSlab1, kDstOwn, kDstPrefix };
-struct RowOut {
-  __nv_bfloat16* out;
-  float* part;
-  float* lse;
+  // Initialises barrier `t` (threads 0 .. NUM_BARS - 1, one each).
+  static __device__ __forceinline__ void init(uint32_t sbase, int t) {
+    const int u = t - (2 + 2 * STAGES);  // from s_full on
+    int count = 1;
+    if (u >= 0 && u < 8 && (u / 2 == 1 || u / 2 == 3)) count = 4;                      // p_full, o_empty: a slot's warps
+    if (t >= NUM_BARS - kPieceSlots) count = 9;  // piece_empty: every softmax warp and the MMA warp reads each piece
+    mbar_init(sbase + BAR_OFF + 8 * t, count);
+  }
 };
-template <int D>
-__device__ __forceinline__ RowOut row_out(const PrefixParams& p, int dst, size_t slab_row, int g, int t0, int row) {
-  RowOut w{nullptr, nullptr, nullptr};
-  if (dst == kDstSlab0 || dst == kDstSlab1) {
-    w.part = p.slab_o + (slab_row + row) * D;
-    w.lse = p.slab_lse + slab_row + row;
-    return w;
-  }
-  const int t = row / p.group;
-  const size_t orow = static_cast<size_t>(t0 + t) * p.H + g * p.group + (row - t * p.group);
-  if (dst == kDstOutput) {
-    w.out = p.o + orow * D;
-    w.lse = p.lse + orow;
-  } else {
-    w.part = (dst == kDstOwn ? p.own_o : p.prefix_o) + orow * D;
-    w.lse = (dst == kDstOwn ? p.own_lse : p.prefix_lse) + orow;
-  }
-  return w;
-}
-// First slab row of worker `w` of a kind for its first (0) or last (1) cut item.
-__device__ __forceinline__ size_t many_slab(const PrefixParams& p, int w, int which) {
-  return (static_cast<size_t>(w) * 2 + which) * p.slab_rows;
-}
-__device__ __forceinline__ size_t few_slab(const PrefixParams& p, int w, int which) {
-  return static_cast<size_t>(p.ctas) * 2 * p.slab_rows + (static_cast<size_t>(w) * 2 + which) * p.few_rows;
-}
+// Kept from laying out the work until the end: the needed row blocks and what the block's workers begin with.
+constexpr int SMEM_BYTES = 232448;  // 227 KB opt-in dynamic shared memory per block on sm_103
+constexpr int BEGIN_OFF = SMEM_BYTES - 8 * int(sizeof(Begin)), NEED_OFF = BEGIN_OFF - kMaxFlags / 8;
+static_assert(PLayout<64>::END <= NEED_OFF && PLayout<128>::END <= NEED_OFF && sizeof(Layout) <= PLayout<64>::XCH_OFF, "shared memory");
 
 template <int D>
 __device__ __forceinline__ void many_rows(const CUtensorMap& tmQ, const CUtensorMap& tmK, const CUtensorMap& tmV,
-                                          const PrefixParams& p, uint8_t* smem) {
+                                          const PrefixParams& p, const Plan& l, uint8_t* smem) {
   using L = PLayout<D>;
   const uint32_t sbase = smem_u32(smem);
   const uint32_t kv_smem = sbase + L::KV_OFF;
@@ -364,43 +427,13 @@ __device__ __forceinline__ void many_rows(const CUtensorMap& tmQ, const CUtensor
   volatile float* xch = reinterpret_cast<volatile float*>(smem + L::XCH_OFF);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::MISC_OFF);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::MISC_OFF + 4);
-  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int warp = uni(threadIdx.x / 32), lane = threadIdx.x % 32;
 
-  if (threadIdx.x == 0) {
-    mbar_init(bar_q_full, 1);
-    mbar_init(bar_q_empty, 1);
-    for (int s = 0; s < L::STAGES; ++s) {
-      mbar_init(bar_kv_full + 8 * s, 1);
-      mbar_init(bar_kv_empty + 8 * s, 1);
-    }
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(bar_s_full + 8 * i, 1);
-      mbar_init(bar_p_full + 8 * i, 4);
-      mbar_init(bar_o_full + 8 * i, 1);
-      mbar_init(bar_o_empty + 8 * i, 4);
-    }
-    for (int w = 0; w < 4; ++w) mbar_init(bar_x_full + 8 * w, 1);
-    mbar_init(bar_done, 1);
-    for (int s = 0; s < kPieceSlots; ++s) {
-      mbar_init(bar_piece_full + 8 * s, 1);
-      mbar_init(bar_piece_empty + 8 * s, 9);  // every softmax warp and the MMA warp reads each piece
-    }
-    *abort_flag = 0;
-    fence_mbar_init();
-  }
-  if (warp == MMA_WARP) {
-    tmem_alloc(smem_u32(tmem_slot), 512);
-    tmem_relinquish();
-  }
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   const Waiter W{abort_flag, p.timeout_ns, &g_prefix_status};
 
   if (warp == PRODUCER_WARP) {
-    const unsigned int total = p.hdr[kHdrTotal], share = p.hdr[kHdrShare], prefix_cost = p.hdr[kHdrLead];
-    const int blocks = p.hdr[kHdrBlocks], tokens = p.hdr[kHdrTokens];
+    const unsigned int share = uni(l.share[0]), total = uni(l.total[0]), lead = uni(l.lead[0]);
     const unsigned int x0 = blockIdx.x * share, x1 = min(total, x0 + share);
     int stage = 0, np = 0;
     uint32_t phase = 0, issued = 0, issued_parity = 0;
@@ -408,7 +441,9 @@ __device__ __forceinline__ void many_rows(const CUtensorMap& tmQ, const CUtensor
     // page numbers of 32 tiles of one table row, one per lane
     const int* held_table = nullptr;
     int held_base = -1, held_page = 0;
-    auto kv_load = [&](const CUtensorMap* map, const int* table, int tile, int g) -> bool {
+    auto kv_load = [&](const CUtensorMap* map, const int* own_table, int j, int ptiles, int g) -> bool {
+      const int* table = j < ptiles ? p.prefix_table : own_table;
+      const int tile = j < ptiles ? j : j - ptiles;
       if (table != held_table || (tile & ~31) != held_base) {
         held_table = table;
         held_base = tile & ~31;
@@ -437,32 +472,33 @@ __device__ __forceinline__ void many_rows(const CUtensorMap& tmQ, const CUtensor
         const int* src = reinterpret_cast<const int*>(&q);
         volatile int* dst = reinterpret_cast<volatile int*>(pieces + s);
 #pragma unroll
-        for (int w = 0; w < 14; ++w) dst[w] = src[w];
+        for (int w = 0; w < 15; ++w) dst[w] = src[w];
         mbar_arrive(bar_piece_full + 8 * s);
       }
       __syncwarp();
       ++np;
       return true;
     };
-    // Emits this block's tiles [j0, j1) of an item: tokens [t0, t0 + count) in row tiles of tp tokens.
-    auto emit = [&](bool own, const int* table, int g, int t0, int count, int tiles, int tiles0, int j0, int j1, int keys,
-                    int lim0, int step) -> bool {
-      const int tile_tokens = p.tp;
+    // Emits this block's tiles [j0, j1) of an item: tokens [t0, t0 + count) in row tiles of tp tokens, the first of
+    // which sees tiles0 of its tiles.
+    auto emit = [&](const int* table, int g, int t0, int count, int tiles, int tiles0, int j0, int j1, int ptiles, int keys,
+                    int lim0, int step, int whole) -> bool {
       Piece q;
       q.n = j1 - j0;
-      q.mode = count > tile_tokens ? 2 : 1;
+      q.mode = count > p.tp ? 2 : 1;
       q.n0 = q.mode == 2 ? max(0, min(tiles0, j1) - j0) : (q.n + 1) / 2;
       q.n1 = q.mode == 2 ? q.n : q.n / 2;
       q.j0 = j0;
+      q.ptiles = ptiles;
       q.keys = keys;
       q.lim0 = lim0;
       q.step = step;
       q.t0 = t0;
-      q.tile_rows = tile_tokens * p.group;
-      q.rows0 = min(count, tile_tokens) * p.group;
-      q.rows1 = max(0, count - tile_tokens) * p.group;
+      q.tile_rows = p.tp * p.group;
+      q.rows0 = min(count, p.tp) * p.group;
+      q.rows1 = max(0, count - p.tp) * p.group;
       q.g = g;
-      q.dst = j0 > 0 ? kDstSlab0 : j1 < tiles ? kDstSlab1 : !own ? kDstPrefix : p.tiles_p > 0 ? kDstOwn : kDstOutput;
+      q.dst = j0 > 0 ? kDstSlab0 : j1 < tiles ? kDstSlab1 : whole;
       const int k = np;
       if (!publish(q)) return false;
       if (!wait_all(W, bar_q_empty, (k & 1) ^ 1)) return false;
@@ -471,64 +507,64 @@ __device__ __forceinline__ void many_rows(const CUtensorMap& tmQ, const CUtensor
       for (int i = 0; i < q.mode; ++i)
 #pragma unroll
         for (int b = 0; b < L::BOXES; ++b)
-          tma_load_3d_elect(sbase + i * L::TILE_BYTES + b * BOX_BYTES, &tmQ, b * 64, g * p.group, t0 + i * tile_tokens,
+          tma_load_3d_elect(sbase + i * L::TILE_BYTES + b * BOX_BYTES, &tmQ, b * 64, g * p.group, t0 + i * p.tp,
                             bar_q_full);
       if (q.mode == 1) {  // K_0 K_1 V_0 K_2 V_1 K_3 ...
-        if (!kv_load(&tmK, table, j0, g) || (q.n > 1 && !kv_load(&tmK, table, j0 + 1, g))) return false;
+        if (!kv_load(&tmK, table, j0, ptiles, g) || (q.n > 1 && !kv_load(&tmK, table, j0 + 1, ptiles, g))) return false;
         for (int j = j0; j < j1; ++j)
-          if (!kv_load(&tmV, table, j, g) || (j + 2 < j1 && !kv_load(&tmK, table, j + 2, g))) return false;
+          if (!kv_load(&tmV, table, j, ptiles, g) || (j + 2 < j1 && !kv_load(&tmK, table, j + 2, ptiles, g))) return false;
       } else {
         for (int j = j0; j < j1; ++j)
-          if (!kv_load(&tmK, table, j, g) || !kv_load(&tmV, table, j, g)) return false;
+          if (!kv_load(&tmK, table, j, ptiles, g) || !kv_load(&tmV, table, j, ptiles, g)) return false;
       }
       return true;
     };
 
-    if (x0 < x1 && x0 < prefix_cost) {  // items of the prefix: head by head, block of rows by block
-      const int items = p.Hkv * blocks;
+    if (x0 < x1 && x0 < lead) {  // items of the prefix: head by head, needed block of rows by block
+      const volatile unsigned int* need = reinterpret_cast<const volatile unsigned int*>(smem + NEED_OFF);
+      const int tokens = uni(l.tokens), blocks = uni(l.blocks), per_head = uni(l.items), items = p.Hkv * per_head;
       for (int at = x0 / prefix_item(p, tokens, 0).cost(); ok && at < items; ++at) {
         const Item it = prefix_item(p, tokens, at);
         if (it.c0 >= x1) break;
         const int j0 = it.from(x0), j1 = it.from(x1);
         if (j0 >= j1) continue;
-        const int g = at / blocks, t0 = (at - g * blocks) * 2 * p.tp;
-        ok = emit(false, p.prefix_table, g, t0, min(2 * p.tp, tokens - t0), p.tiles_p, p.tiles_p, j0, j1, p.prefix_len,
-                  p.prefix_len, 0);
+        const int g = at / per_head, t0 = uni(needed_block(p, need, blocks, at - g * per_head)) * 2 * p.tp;
+        ok = emit(nullptr, g, t0, min(2 * p.tp, tokens - t0), p.tiles_p, p.tiles_p, j0, j1, p.tiles_p, 0, 0, 0, kDstPrefix);
       }
     }
-    if (ok && x0 < x1 && x1 > prefix_cost) {  // items of own keys: requests, blocks of tokens, heads
-      int b = p.start[blockIdx.x], base = b - 32;
+    if (ok && x0 < x1 && x1 > lead) {  // items of requests, blocks of tokens, heads
+      const volatile Begin* begin = reinterpret_cast<const volatile Begin*>(smem + BEGIN_OFF);
+      int b = uni(begin->b), base = b - 32;
+      unsigned int c0 = uni(begin->c0);
       int r_cu0 = 0, r_cu1 = 0, r_seq = 0;
-      unsigned int r_cum = 0;
-      for (; ok && b < p.B; ++b) {
+      for (; ok && b < p.B && c0 < x1; ++b) {
         if (b >= base + 32) {  // 32 requests at a time, one per lane
           base = b;
-          const int l = min(b + lane, p.B - 1);
-          r_cu0 = p.cu_new[l];
-          r_cu1 = p.cu_new[l + 1];
-          r_seq = p.seq_lens[l];
-          r_cum = p.cum[l];
+          const int at = min(b + lane, p.B - 1);
+          r_cu0 = p.cu_new[at];
+          r_cu1 = p.cu_new[at + 1];
+          r_seq = p.seq_lens[at];
         }
         const Request r = make_request(p, __shfl_sync(0xffffffffu, r_cu0, b - base), __shfl_sync(0xffffffffu, r_cu1, b - base),
                                        __shfl_sync(0xffffffffu, r_seq, b - base));
-        unsigned int c0 = __shfl_sync(0xffffffffu, r_cum, b - base);
-        if (c0 >= x1) break;
         if (is_few(p, r)) continue;
         const int* table = p.block_table + static_cast<size_t>(b) * p.max_pages;
+        const int ptiles = is_big(p, r) ? p.tiles_p : 0;
         for (int blk = 0; ok && blk * 2 * p.tp < r.added && c0 < x1; ++blk) {
           Item it = block_item(p, r, blk, c0);
           const unsigned int cost = it.cost();
           c0 += p.Hkv * cost;
           if (it.units == 0 || c0 <= x0) continue;
           const int t = blk * 2 * p.tp, count = min(2 * p.tp, r.added - t);
-          const int tiles0 = tiles_of(visible(p, r, min(r.added, t + p.tp)));
+          const int tiles0 = ptiles + tiles_of(visible(p, r, min(r.added, t + p.tp)));
           const int g0 = x0 > it.c0 ? (x0 - it.c0) / cost : 0;
           it.c0 += g0 * cost;
           for (int g = g0; ok && g < p.Hkv && it.c0 < x1; ++g, it.c0 += cost) {
             const int j0 = it.from(x0), j1 = it.from(x1);
             if (j0 < j1)
-              ok = emit(true, table, g, r.first + t, count, it.units, tiles0, j0, j1, r.len,
-                        p.causal ? r.len - r.added + t + 1 : r.len, p.causal);
+              ok = emit(table, g, r.first + t, count, it.units, tiles0, j0, j1, ptiles, r.len,
+                        p.causal ? r.len - r.added + t + 1 : r.len, p.causal,
+                        p.tiles_p == ptiles ? kDstOutput : kDstOwn);
           }
         }
       }
@@ -536,7 +572,7 @@ __device__ __forceinline__ void many_rows(const CUtensorMap& tmQ, const CUtensor
     if (ok) {
       Piece q;
       q.mode = 0;
-      q.n = q.n0 = q.n1 = q.j0 = q.keys = q.lim0 = q.step = q.t0 = q.rows0 = q.rows1 = q.g = q.dst = q.tile_rows = 0;
+      q.n = q.n0 = q.n1 = q.j0 = q.ptiles = q.keys = q.lim0 = q.step = q.t0 = q.rows0 = q.rows1 = q.g = q.dst = q.tile_rows = 0;
       ok = publish(q);
     }
     if (!ok) {  // let every copy already issued land before the block exits
@@ -579,7 +615,7 @@ __device__ __forceinline__ void many_rows(const CUtensorMap& tmQ, const CUtensor
     // in steps of 16 as far as there are keys, and the value rows behind the last key in its last step are
     // set to 0.  Returns the steps.
     auto value_steps = [&](const Piece& q, int tile, int vs) -> int {
-      const int valid = q.keys - tile * BN;
+      const int valid = tile < q.ptiles ? p.prefix_len - tile * BN : q.keys - (tile - q.ptiles) * BN;
       if (valid >= BN) return BN / 16;
       const int steps = (valid + 15) / 16, words = (steps * 16 - valid) * 8;  // 16-byte words per box
       for (int w = lane; w < words * L::BOXES; w += 32) {
@@ -592,11 +628,16 @@ __device__ __forceinline__ void many_rows(const CUtensorMap& tmQ, const CUtensor
     };
     auto issue_pv = [&](int slot, int vs, int steps, bool acc) {  // O_slot (+)= P_slot V, keys in steps of 16
       const uint32_t b0 = dv_lo + ((L::KV_OFF + vs * L::TILE_BYTES) >> 4);
+      if (steps == BN / 16) {
 #pragma unroll
-      for (int kk = 0; kk < BN / 16; ++kk)
-        if (kk < steps)
+        for (int kk = 0; kk < BN / 16; ++kk)
           mma_ts_elect(tmem + 256 + slot * D, tmem + slot * 128 + kk * 8, b0 + ((kk * 2048) >> 4), dv_hi, IDESC_PV,
                        (acc || kk > 0) ? 1u : 0u);
+      } else {
+        for (int kk = 0; kk < steps; ++kk)
+          mma_ts_elect(tmem + 256 + slot * D, tmem + slot * 128 + kk * 8, b0 + ((kk * 2048) >> 4), dv_hi, IDESC_PV,
+                       (acc || kk > 0) ? 1u : 0u);
+      }
     };
     auto ready_pv = [&](int slot, bool first) -> bool {  // P_slot written; O_slot free at a piece's first product
       if (first) {
@@ -612,12 +653,13 @@ __device__ __forceinline__ void many_rows(const CUtensorMap& tmQ, const CUtensor
       const int s = k % kPieceSlots;
       if (!(ok = wait_all(W, bar_piece_full + 8 * s, (k / kPieceSlots) & 1))) break;
       Piece q;
-      q.mode = pieces[s].mode;
-      q.n = pieces[s].n;
-      q.n0 = pieces[s].n0;
-      q.n1 = pieces[s].n1;
-      q.j0 = pieces[s].j0;
-      q.keys = pieces[s].keys;
+      q.mode = uni(pieces[s].mode);
+      q.n = uni(pieces[s].n);
+      q.n0 = uni(pieces[s].n0);
+      q.n1 = uni(pieces[s].n1);
+      q.j0 = uni(pieces[s].j0);
+      q.keys = uni(pieces[s].keys);
+      q.ptiles = uni(pieces[s].ptiles);
       __syncwarp();
       if (lane == 0) mbar_arrive(bar_piece_empty + 8 * s);
       if (q.mode == 0) break;
@@ -698,6 +740,7 @@ __device__ __forceinline__ void many_rows(const CUtensorMap& tmQ, const CUtensor
       if (!(ok = wait_all(W, bar_piece_full + 8 * s, (k / kPieceSlots) & 1))) break;
       const int mode = pieces[s].mode, n = pieces[s].n, n_mine = i ? pieces[s].n1 : pieces[s].n0, j0 = pieces[s].j0;
       const int rows = (mode == 2 && i) ? pieces[s].rows1 : pieces[s].rows0, g = pieces[s].g, dst = pieces[s].dst;
+      const int ptiles = pieces[s].ptiles;
       const int tile_rows = pieces[s].tile_rows, t0 = pieces[s].t0;
       const int row0 = mode == 2 ? i * tile_rows : 0;  // the tile's first row within the item
       int lim = min(pieces[s].keys, pieces[s].lim0 + pieces[s].step * (row0 / p.group + tok));  // keys the row sees
@@ -706,6 +749,7 @@ __device__ __forceinline__ void many_rows(const CUtensorMap& tmQ, const CUtensor
       if (mode == 0) break;
       if (n_mine == 0) continue;
       const bool live = rt < rows, live_warp = wq * 32 < rows;
+      const int lim_p = live ? p.prefix_len : 0;  // of the prefix's keys
       if (!live) lim = 0;
       float m_run = -INFINITY;  // reference max, base-2 units of the scaled score
       float l = 0.f, lr = 0.f;  // sums of the fp32 weights (LSE) and of the bf16 weights the product uses (divides O)
@@ -716,7 +760,8 @@ __device__ __forceinline__ void many_rows(const CUtensorMap& tmQ, const CUtensor
         if (live_warp) {
           uint32_t sr[BN];
           tmem_ld128_wait(t_s, sr);
-          const int left = lim - (j0 + (mode == 1 ? 2 * x + i : x)) * BN;  // keys of this tile the row sees
+          const int tile = j0 + (mode == 1 ? 2 * x + i : x);
+          const int left = tile < ptiles ? lim_p - tile * BN : lim - (tile - ptiles) * BN;  // keys of the tile the row sees
           if (__any_sync(0xffffffffu, left < BN)) {
 #pragma unroll
             for (int c = 0; c < BN; ++c)
@@ -818,31 +863,40 @@ __device__ __forceinline__ void many_rows(const CUtensorMap& tmQ, const CUtensor
         a1 *= inv;
         const RowOut to = row_out<D>(p, dst, many_slab(p, blockIdx.x, dst == kDstSlab1), g, t0, row0 + rt);
         if (live) *to.lse = to.out ? lse2 * LN2 : lse2;
+        // O leaves 16 rows at a time in the layout in which four lanes have eight columns of a row (a whole 32-byte
+        // sector of a part): lane l has columns 2 (l % 4), + 1 of every eight, rows l / 4 and l / 4 + 8
+        const unsigned long long mine = live ? reinterpret_cast<unsigned long long>(to.out ? static_cast<void*>(to.out) : to.part) : 0;
 #pragma unroll
-        for (int c = 0; c < D / 32; ++c) {
-          uint32_t ov[32];
-          tmem_ld32_wait(t_o + c * 32, ov);
-          if (pair) {
-            uint32_t o1[32];
-            tmem_ld32_wait(t_o + D + c * 32, o1);
+        for (int h = 0; h < 2; ++h) {
+          const int r_lo = h * 16 + lane / 4, r_hi = r_lo + 8;
+          const unsigned long long at_lo = __shfl_sync(0xffffffffu, mine, r_lo), at_hi = __shfl_sync(0xffffffffu, mine, r_hi);
+          const float a0_lo = __shfl_sync(0xffffffffu, a0, r_lo), a0_hi = __shfl_sync(0xffffffffu, a0, r_hi);
+          const float a1_lo = __shfl_sync(0xffffffffu, a1, r_lo), a1_hi = __shfl_sync(0xffffffffu, a1, r_hi);
 #pragma unroll
-            for (int e = 0; e < 32; ++e) ov[e] = f2u(u2f(ov[e]) * a0 + u2f(o1[e]) * a1);
-          } else {
+          for (int c = 0; c < D / 64; ++c) {
+            uint32_t ov[32];
+            tmem_ld_16x256b_x8_wait(t_o + (uint32_t(h * 16) << 16) + c * 64, ov);
+            if (pair) {
+              uint32_t o1[32];
+              tmem_ld_16x256b_x8_wait(t_o + D + (uint32_t(h * 16) << 16) + c * 64, o1);
 #pragma unroll
-            for (int e = 0; e < 32; ++e) ov[e] = f2u(u2f(ov[e]) * a0);
-          }
-          if (!live) continue;
-          if (to.out) {
+              for (int e = 0; e < 32; ++e)
+                ov[e] = f2u(u2f(ov[e]) * (e & 2 ? a0_hi : a0_lo) + u2f(o1[e]) * (e & 2 ? a1_hi : a1_lo));
+            } else {
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-              *reinterpret_cast<uint4*>(to.out + c * 32 + e * 8) =
-                  make_uint4(pack_bf16x2(u2f(ov[8 * e]), u2f(ov[8 * e + 1])), pack_bf16x2(u2f(ov[8 * e + 2]), u2f(ov[8 * e + 3])),
-                             pack_bf16x2(u2f(ov[8 * e + 4]), u2f(ov[8 * e + 5])), pack_bf16x2(u2f(ov[8 * e + 6]), u2f(ov[8 * e + 7])));
-          } else {
+              for (int e = 0; e < 32; ++e) ov[e] = f2u(u2f(ov[e]) * (e & 2 ? a0_hi : a0_lo));
+            }
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-              *reinterpret_cast<float4*>(to.part + c * 32 + e * 4) =
-                  make_float4(u2f(ov[4 * e]), u2f(ov[4 * e + 1]), u2f(ov[4 * e + 2]), u2f(ov[4 * e + 3]));
+            for (int e = 0; e < 8; ++e) {
+              const int col = c * 64 + e * 8 + 2 * (lane & 3);
+              if (dst == kDstOutput) {
+                if (at_lo) reinterpret_cast<uint32_t*>(at_lo)[col / 2] = pack_bf16x2(u2f(ov[4 * e]), u2f(ov[4 * e + 1]));
+                if (at_hi) reinterpret_cast<uint32_t*>(at_hi)[col / 2] = pack_bf16x2(u2f(ov[4 * e + 2]), u2f(ov[4 * e + 3]));
+              } else {
+                if (at_lo) reinterpret_cast<float2*>(at_lo)[col / 2] = make_float2(u2f(ov[4 * e]), u2f(ov[4 * e + 1]));
+                if (at_hi) reinterpret_cast<float2*>(at_hi)[col / 2] = make_float2(u2f(ov[4 * e + 2]), u2f(ov[4 * e + 3]));
+              }
+            }
           }
         }
       }
@@ -856,12 +910,6 @@ __device__ __forceinline__ void many_rows(const CUtensorMap& tmQ, const CUtensor
     __syncwarp();
   }
 
-  tc_fence_before();
-  __syncthreads();
-  if (warp == MMA_WARP) {
-    tc_fence_after();
-    tmem_dealloc(tmem, 512);
-  }
 }
 
 // ---------------------------------------------------------------- few rows
@@ -881,11 +929,12 @@ struct FLayout {
   static constexpr int STEP_BYTES = 2 * kStep * D * 2;  // K, then V; 64 columns per box of 16 rows x 128 bytes
   static constexpr int BOX = kStep * 128;
   static constexpr int TEAMS = FEW_WARPS / R;
-  static constexpr int FIT = 224 * 1024 / (TEAMS * STEP_BYTES);
-  static constexpr int STAGES = FIT < 16 ? FIT : 16;
-  static constexpr int BAR_OFF = 224 * 1024;  // full[TEAMS][STAGES], empty[TEAMS][STAGES]
-  static constexpr int MISC_OFF = BAR_OFF + 2 * TEAMS * STAGES * 8;
-  static constexpr int SMEM_BYTES = MISC_OFF + 16 + 1024;
+  static constexpr int FIT = PLayout<D>::XCH_OFF / (TEAMS * STEP_BYTES);
+  static constexpr int STAGES = FIT < 12 ? FIT : 12;
+  static constexpr int BAR_OFF = PLayout<D>::END;  // full[TEAMS][STAGES]; empty[TEAMS][STAGES] where R > 1
+  static constexpr int NUM_BARS = (R > 1 ? 2 : 1) * TEAMS * STAGES;
+  static_assert(STAGES >= 3 && BAR_OFF % 8 == 0 && BAR_OFF + NUM_BARS * 8 <= NEED_OFF && NUM_BARS <= THREADS, "barriers");
+  static_assert(TEAMS * STAGES * STEP_BYTES <= PLayout<D>::XCH_OFF, "the rings reach into what follows them");
 };
 
 // Warp-level products: D (16 x 8) += A (16 x 16) B (16 x 8), bf16 in, fp32 out.
@@ -923,27 +972,26 @@ struct FewPiece {
 
 // The pieces of a stretch [x0, x1) of the few-row line, in order (all lanes of a warp together).
 struct FewWalk {
-  unsigned int x0, x1, lead, cost;
-  int tokens, at, items;  // items of the prefix on this line
+  unsigned int x0, x1, lead, cost, c0;  // c0: first place of request b
+  int tokens, at, items;                // items of the prefix on this line
   int b, base, g;
   bool have;
   Request r;
   Item it;
   int cu0, cu1, seq;  // of request base + lane
-  unsigned int cum;
 
-  __device__ __forceinline__ void start(const PrefixParams& p, unsigned int from, unsigned int to, int first) {
+  __device__ __forceinline__ void start(const PrefixParams& p, const Plan& l, unsigned int from, unsigned int to, int first,
+                                        unsigned int first_place) {
     x0 = from;
     x1 = to;
-    lead = p.hdr[kHdrLead + 1];
-    tokens = p.hdr[kHdrTokens];
+    lead = l.lead[1];
+    tokens = l.tokens;
     items = lead > 0 ? p.Hkv : 0;
     at = x0 < lead ? static_cast<int>(x0 / (lead / p.Hkv)) : items;
-    b = first - 1;
+    b = first;
+    c0 = first_place;
     base = b - 32;
     have = false;
-    g = 0;
-    cost = 0;
   }
   __device__ __forceinline__ bool next(const PrefixParams& p, int lane, FewPiece& q) {
     while (at < items) {
@@ -958,36 +1006,40 @@ struct FewWalk {
     }
     if (x1 <= lead) return false;
     for (;;) {
-      if (have && g < p.Hkv) {
-        if (it.c0 >= x1) return false;
-        const int j0 = it.from(x0), j1 = it.from(x1), head = g++;
-        it.c0 += cost;
-        if (j0 >= j1) continue;
-        q = FewPiece{p.block_table + static_cast<size_t>(b) * p.max_pages, p.max_pages, head, r.first, r.added * p.group,
-                     j0, j1, r.len, p.causal ? r.len - r.added + 1 : r.len, p.causal,
-                     j0 > 0 ? kDstSlab0 : j1 < it.units ? kDstSlab1 : p.tiles_p > 0 ? kDstOwn : kDstOutput};
-        return true;
+      if (have) {
+        if (g < p.Hkv) {
+          if (it.c0 >= x1) return false;
+          const int j0 = it.from(x0), j1 = it.from(x1), head = g++;
+          it.c0 += cost;
+          if (j0 >= j1) continue;
+          q = FewPiece{p.block_table + static_cast<size_t>(b) * p.max_pages, p.max_pages, head, r.first, r.added * p.group,
+                       j0, j1, r.len, p.causal ? r.len - r.added + 1 : r.len, p.causal,
+                       j0 > 0 ? kDstSlab0 : j1 < it.units ? kDstSlab1 : p.tiles_p > 0 ? kDstOwn : kDstOutput};
+          return true;
+        }
+        c0 += p.Hkv * cost;
+        ++b;
+        have = false;
       }
-      have = false;
-      if (++b >= p.B) return false;
-      if (b >= base + 32) {  // 32 requests at a time, one per lane
-        base = b;
-        const int l = min(b + lane, p.B - 1);
-        cu0 = p.cu_new[l];
-        cu1 = p.cu_new[l + 1];
-        seq = p.seq_lens[l];
-        cum = p.cum[p.B + l];
+      for (;; ++b) {
+        if (b >= p.B || c0 >= x1) return false;
+        if (b >= base + 32) {  // 32 requests at a time, one per lane
+          base = b;
+          const int l = min(b + lane, p.B - 1);
+          cu0 = p.cu_new[l];
+          cu1 = p.cu_new[l + 1];
+          seq = p.seq_lens[l];
+        }
+        r = make_request(p, __shfl_sync(0xffffffffu, cu0, b - base), __shfl_sync(0xffffffffu, cu1, b - base),
+                         __shfl_sync(0xffffffffu, seq, b - base));
+        if (r.added == 0 || !is_few(p, r)) continue;
+        it = few_item(c0, visible(p, r, r.added));
+        cost = it.cost();
+        if (c0 + p.Hkv * cost > x0 && cost > 0) break;
+        c0 += p.Hkv * cost;
       }
-      r = make_request(p, __shfl_sync(0xffffffffu, cu0, b - base), __shfl_sync(0xffffffffu, cu1, b - base),
-                       __shfl_sync(0xffffffffu, seq, b - base));
-      const unsigned int c0 = __shfl_sync(0xffffffffu, cum, b - base);
-      if (c0 >= x1) return false;
-      if (r.added == 0 || !is_few(p, r)) continue;
-      it = few_item(c0, visible(p, r, r.added));
-      cost = it.cost();
-      if (cost == 0 || c0 + p.Hkv * cost <= x0) continue;
       g = x0 > c0 ? static_cast<int>((x0 - c0) / cost) : 0;
-      it.c0 += g * cost;
+      it.c0 = c0 + g * cost;
       have = true;
     }
   }
@@ -995,33 +1047,26 @@ struct FewWalk {
 
 template <int D, int NT, int R>
 __device__ __forceinline__ void few_rows(const CUtensorMap& tmK, const CUtensorMap& tmV, const PrefixParams& p,
-                                         uint8_t* smem) {
+                                         const Plan& l, uint8_t* smem) {
   using L = FLayout<D, R>;
   const uint32_t sbase = smem_u32(smem);
-  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int warp = uni(threadIdx.x / 32), lane = threadIdx.x % 32;
   const int team = warp / R, mt = warp % R;
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::MISC_OFF);
-  if (threadIdx.x == 0) {
-    for (int t = 0; t < L::TEAMS * L::STAGES; ++t) {
-      mbar_init(sbase + L::BAR_OFF + 8 * t, 1);
-      mbar_init(sbase + L::BAR_OFF + 8 * (L::TEAMS * L::STAGES + t), R);
-    }
-    *abort_flag = 0;
-    fence_mbar_init();
-  }
-  __syncthreads();
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + PLayout<D>::MISC_OFF + 4);
   if (warp >= FEW_WARPS) return;
   const Waiter W{abort_flag, p.timeout_ns, &g_prefix_status};
   const uint32_t ring = sbase + team * L::STAGES * L::STEP_BYTES;
   const uint32_t bar_full = sbase + L::BAR_OFF + 8 * team * L::STAGES;
   const uint32_t bar_empty = bar_full + 8 * L::TEAMS * L::STAGES;
-  const int worker = (blockIdx.x - p.hdr[kHdrMany]) * L::TEAMS + team;
-  const unsigned int total = p.hdr[kHdrTotal + 1], share = p.hdr[kHdrShare + 1];
-  const unsigned long long begin = static_cast<unsigned long long>(worker) * share;
-  if (begin >= total) return;
-  const unsigned int x0 = static_cast<unsigned int>(begin);
-  const unsigned int x1 = static_cast<unsigned int>(min(begin + share, static_cast<unsigned long long>(total)));
-  const int first = x1 > static_cast<unsigned int>(p.hdr[kHdrLead + 1]) ? p.start[p.ctas + worker] : 0;
+  const int worker = (blockIdx.x - uni(l.many)) * L::TEAMS + team;
+  const unsigned int total = uni(l.total[1]), share = uni(l.share[1]);
+  const unsigned long long from = static_cast<unsigned long long>(worker) * share;
+  if (from >= total) return;
+  const unsigned int x0 = static_cast<unsigned int>(from);
+  const unsigned int x1 = static_cast<unsigned int>(min(from + share, static_cast<unsigned long long>(total)));
+  const volatile Begin* begin = reinterpret_cast<const volatile Begin*>(smem + BEGIN_OFF) + team;
+  const int first = uni(begin->b);
+  const unsigned int first_place = uni(begin->c0);
 
   // the ring's filling side (the team's first warp)
   FewWalk load;
@@ -1031,7 +1076,7 @@ __device__ __forceinline__ void few_rows(const CUtensorMap& tmK, const CUtensorM
   const int* held_table = nullptr;  // page numbers of 32 tiles of one table row, one per lane
   int held_base = -1, held_page = 0;
   if (mt == 0) {
-    load.start(p, x0, x1, first);
+    load.start(p, l, x0, x1, first, first_place);
     lp.j1 = 0;
   }
   auto fill = [&]() -> bool {  // loads the stretch's next step, if there is one
@@ -1081,7 +1126,7 @@ __device__ __forceinline__ void few_rows(const CUtensorMap& tmK, const CUtensorM
   int stage = 0;
   uint32_t full_par = 0;
   FewWalk walk;
-  walk.start(p, x0, x1, first);
+  walk.start(p, l, x0, x1, first, first_place);
   FewPiece q;
   while (ok && walk.next(p, lane, q)) {
     uint32_t qf[D / 16][NT][2];  // Q^T
@@ -1105,13 +1150,13 @@ __device__ __forceinline__ void few_rows(const CUtensorMap& tmK, const CUtensorM
     lim_min = __reduce_min_sync(0xffffffffu, lim_min);
     // per row: the reference (base-2 units of the scaled score); the sum of the fp32 weights (LSE; this thread's keys);
     // the sum of the bf16 weights that the product uses (divides O), kept by a product with ones
-    float o[D / 16][NT][4], m[NT][2], l[NT][2], lr[NT][4];
+    float o[D / 16][NT][4], m[NT][2], lw[NT][2], lr[NT][4];
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         m[t][e] = -INFINITY;
-        l[t][e] = 0.f;
+        lw[t][e] = 0.f;
       }
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
@@ -1172,7 +1217,7 @@ __device__ __forceinline__ void few_rows(const CUtensorMap& tmK, const CUtensorM
             const float top = x[t][e] > m[t][e] + 8.f ? x[t][e] : m[t][e];
             const float f = top == -INFINITY ? 1.f : ex2_approx(m[t][e] - top);
             m[t][e] = top;
-            l[t][e] *= f;
+            lw[t][e] *= f;
             lr[t][e] *= f;
 #pragma unroll
             for (int c = 0; c < D / 16; ++c) {
@@ -1187,8 +1232,8 @@ __device__ __forceinline__ void few_rows(const CUtensorMap& tmK, const CUtensorM
         const float z0 = m[t][0] == -INFINITY ? 0.f : -m[t][0], z1 = m[t][1] == -INFINITY ? 0.f : -m[t][1];
         const float p0 = ex2_approx(fmaf(s[t][0], sl2, z0)), p1 = ex2_approx(fmaf(s[t][1], sl2, z1));
         const float p2 = ex2_approx(fmaf(s[t][2], sl2, z0)), p3 = ex2_approx(fmaf(s[t][3], sl2, z1));
-        l[t][0] += p0 + p2;
-        l[t][1] += p1 + p3;
+        lw[t][0] += p0 + p2;
+        lw[t][1] += p1 + p3;
         pt[t][0] = transpose_8x8(pack_bf16x2(p0, p1));
         pt[t][1] = transpose_8x8(pack_bf16x2(p2, p3));
         mma_16816(lr[t], ones, pt[t][0], pt[t][1]);
@@ -1225,7 +1270,7 @@ __device__ __forceinline__ void few_rows(const CUtensorMap& tmK, const CUtensorM
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
 #pragma unroll
-        for (int w = 4; w <= 16; w <<= 1) l[t][e] += __shfl_xor_sync(0xffffffffu, l[t][e], w);
+        for (int w = 4; w <= 16; w <<= 1) lw[t][e] += __shfl_xor_sync(0xffffffffu, lw[t][e], w);
         const int r = row0 + 8 * t + c0 + e;
         if (r >= q.rows) continue;
         const float inv = lr[t][e] == 0.f ? 0.f : 1.f / lr[t][e];  // no key seen: O = 0 (a NaN sum stays one)
@@ -1242,7 +1287,7 @@ __device__ __forceinline__ void few_rows(const CUtensorMap& tmK, const CUtensorM
               to.part[col] = y;
           }
         if (lane < 4) {
-          const float lse2 = l[t][e] == 0.f ? -INFINITY : m[t][e] + log2f(l[t][e]);
+          const float lse2 = lw[t][e] == 0.f ? -INFINITY : m[t][e] + log2f(lw[t][e]);
           *to.lse = to.out ? lse2 * LN2 : lse2;
         }
       }
@@ -1256,153 +1301,190 @@ template <int D, int NT, int R>
 __global__ void __launch_bounds__(THREADS, 1)
 fa_prefix_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                  const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmK16,
-                 const __grid_constant__ CUtensorMap tmV16, const PrefixParams p) {
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+                 const __grid_constant__ CUtensorMap tmV16, const __grid_constant__ PrefixParams p) {
+  extern __shared__ __align__(1024) uint8_t smem[];
   if (threadIdx.x == 0) {
     tma_prefetch_desc(&tmQ);
     tma_prefetch_desc(&tmK);
     tma_prefetch_desc(&tmV);
     tma_prefetch_desc(&tmK16);
     tma_prefetch_desc(&tmV16);
+    if (smem_u32(smem) % 1024 != 0) atomicOr(&g_prefix_status, kStatusTimeout);  // (the tiles' swizzle needs it)
   }
-  pdl_launch_dependents();
+  volatile unsigned int* need = reinterpret_cast<volatile unsigned int*>(smem + NEED_OFF);
+  if (threadIdx.x < kMaxFlags / 32) need[threadIdx.x] = 0;
+  // both kinds' barriers and the Tensor Memory: which kind the block works is known only after the wait
+  using M = PLayout<D>;
+  using F = FLayout<D, R>;
+  const uint32_t sbase = smem_u32(smem);
+  if (threadIdx.x < M::NUM_BARS) M::init(sbase, threadIdx.x);
+  if (threadIdx.x < F::NUM_BARS) mbar_init(sbase + F::BAR_OFF + 8 * threadIdx.x, threadIdx.x < F::TEAMS * F::STAGES ? 1 : R);
+  if (threadIdx.x == 0) *reinterpret_cast<volatile int*>(smem + M::MISC_OFF + 4) = 0;
+  fence_mbar_init();
+  const int warp = uni(threadIdx.x / 32);
+  if (warp == MMA_WARP) {
+    tmem_alloc(sbase + M::MISC_OFF, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
   pdl_wait();
-  if (static_cast<int>(blockIdx.x) < p.hdr[kHdrMany])
-    many_rows<D>(tmQ, tmK, tmV, p, smem);
+  const Plan l = make_plan(p, *reinterpret_cast<Layout*>(smem), need, reinterpret_cast<Begin*>(smem + BEGIN_OFF));
+  if (static_cast<int>(blockIdx.x) < l.many)
+    many_rows<D>(tmQ, tmK, tmV, p, l, smem);
   else
-    few_rows<D, NT, R>(tmK16, tmV16, p, smem);
+    few_rows<D, NT, R>(tmK16, tmV16, p, l, smem);
+  tc_fence_before();
+  __syncthreads();
+  if (warp == MMA_WARP) {
+    tc_fence_after();
+    tmem_dealloc(*reinterpret_cast<volatile uint32_t*>(smem + M::MISC_OFF), 512);
+  }
 }
 
 // ---------------------------------------------------------------- join
-// W warps join a row, every lane D / 32 columns.  The parts of a row follow from the places of its two items: an
-// item inside one worker's stretch has one part, in the rows of its source; one that is cut has a part in a slab
-// of every worker that worked some of its units.  The lanes look up 32 workers at a time (warp w of W every W-th).
+// W warps join a row, every lane D / 32 columns.  The parts of a row follow from the places of its items: an item
+// inside one worker's stretch has one part, with the rows of its source; one that is cut has a part in a slab of
+// every worker that worked some of its units.  The lanes look up 32 workers at a time (warp w of W every W-th).
+// blockIdx.x: token; the block's warps take every (gridDim.y * 8 / W)-th head.
 template <int D, int W>
-__global__ void __launch_bounds__(256) fa_prefix_join_kernel(const PrefixParams p) {
+__global__ void __launch_bounds__(256) fa_prefix_join_kernel(const __grid_constant__ PrefixParams p) {
   constexpr int C = D / 32;
   __shared__ float s_acc[W > 1 ? 8 : 1][D], s_m[8], s_sum[8];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = warp % W;
-  const long long orow = static_cast<long long>(blockIdx.x) * (8 / W) + warp / W;  // n * H + h
-  pdl_wait();
-  const int tokens = p.hdr[kHdrTokens];
-  if (orow >= static_cast<long long>(tokens) * p.H) return;  // (W > 1: the same row for the whole block)
-  const int n = static_cast<int>(orow / p.H), h = static_cast<int>(orow - static_cast<long long>(n) * p.H);
-  const int g = h / p.group, hh = h - g * p.group;
-  const int4 t = p.tok[n];
-  float m = -INFINITY, sum = 0.f, acc[C];
-#pragma unroll
-  for (int c = 0; c < C; ++c) acc[c] = 0.f;
-  // adds the parts that the lanes have (lse2 = -infinity: none): row `at` of o
-  auto add = [&](float lse2, size_t at, const float* o, int count) {
-    float top = lse2;
-#pragma unroll
-    for (int w = 16; w; w >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, w));
-    top = fmaxf(top, m);
-    const float f = m == -INFINITY ? 0.f : exp2f(m - top), mine = lse2 == -INFINITY ? 0.f : exp2f(lse2 - top);
-    m = top;
-    float all = mine;
-#pragma unroll
-    for (int w = 16; w; w >>= 1) all += __shfl_xor_sync(0xffffffffu, all, w);
-    sum = sum * f + all;
-#pragma unroll
-    for (int c = 0; c < C; ++c) acc[c] *= f;
-#pragma unroll 8
-    for (int k = 0; k < count; ++k) {
-      const float w = __shfl_sync(0xffffffffu, mine, k);
-      const float* src = o + __shfl_sync(0xffffffffu, at, k) * D + lane * C;
-      if (w == 0.f) continue;  // (also lanes without a part)
-      if (C == 4) {
-        const float4 v = *reinterpret_cast<const float4*>(src);
-        acc[0] += w * v.x;
-        acc[1] += w * v.y;
-        acc[2 % C] += w * v.z;
-        acc[3 % C] += w * v.w;
-      } else {
-        const float2 v = *reinterpret_cast<const float2*>(src);
-        acc[0] += w * v.x;
-        acc[1] += w * v.y;
-      }
-    }
-  };
-  // the item's parts: `seen` of its units visible to this row, row `at` of the item, `few`: its line
-  auto join = [&](const Item& it, bool few, int seen, int at, const float* whole, const float* whole_lse) {
-    const unsigned int share = p.hdr[kHdrShare + few];
-    const int first = it.worker(0, share), last = it.worker(it.units - 1, share);
-    if (first == last) {
-      if (sub == 0) add(lane == 0 ? whole_lse[orow] : -INFINITY, orow, whole, 1);
-      return;
-    }
-    for (int w0 = first; w0 <= last; w0 += 32 * W) {
-      const int w = w0 + lane * W + sub;
-      float lse2 = -INFINITY;
-      size_t row = 0;
-      if (w <= last) {
-        const int j0 = it.from(w * share), j1 = it.from((w + 1) * share);
-        if (j0 < j1 && j0 < seen) {
-          row = (few ? few_slab(p, w, j0 == 0) : many_slab(p, w, j0 == 0)) + at;
-          lse2 = p.slab_lse[row];
-        }
-      }
-      add(lse2, row, p.slab_o, min(32, (last - w0 - sub + W) / W));
-    }
-  };
-  if (p.tiles_p > 0) {
-    const bool few = tokens * p.group <= p.few_rows;
-    const int blocks = p.hdr[kHdrBlocks], blk = few ? 0 : n / (2 * p.tp);
-    join(prefix_item(p, tokens, g * blocks + blk), few, few ? INT_MAX : p.tiles_p, (n - blk * 2 * p.tp) * p.group + hh,
-         p.prefix_o, p.prefix_lse);
-  }
-  if (t.z > 0) {
-    const bool few = t.w & kTokFew;
-    Item it{static_cast<unsigned int>(t.x), few ? kFewItemCost : kItemCost, few ? 1u : static_cast<unsigned int>(t.w) >> 16, t.y};
-    it.c0 += g * it.cost();
-    const unsigned int share = p.hdr[kHdrShare + few];
-    if (p.tiles_p == 0 && it.worker(0, share) == it.worker(it.units - 1, share)) return;  // written already
-    join(it, few, t.z, (t.w & (kTokFew - 1)) * p.group + hh, p.own_o, p.own_lse);
-  }
-  if (W > 1) {  // the warps' sums, one after another in the same order
-    s_m[warp] = m;
-    s_sum[warp] = sum;
-#pragma unroll
-    for (int c = 0; c < C; ++c) s_acc[W > 1 ? warp : 0][lane * C + c] = acc[c];
-    __syncthreads();
-    if (warp > 0) return;
-    float top = -INFINITY;
-#pragma unroll
-    for (int w = 0; w < W; ++w) top = fmaxf(top, s_m[w]);
-    sum = 0.f;
+  const int n = blockIdx.x;
+  pdl_launch_dependents();  // (a following call's blocks set themselves up meanwhile)
+  const int4 t = p.tok[n];  // (past the last token: whatever, not used)
+  const int rank = p.rank[n], tokens = p.hdr[kHdrTokens], per_head = p.hdr[kHdrPrefixItems];
+  const unsigned int shares[2] = {static_cast<unsigned int>(p.hdr[kHdrShare]), static_cast<unsigned int>(p.hdr[kHdrShare + 1])};
+  if (n >= tokens) return;
+  const bool few_p = few_prefix(p, tokens), few_o = t.w & kTokFew;
+  Item item_p{0, 0, 0, 0}, item_o{0, 0, 0, 0};
+  if (rank >= 0) item_p = prefix_item(p, tokens, rank);
+  if (t.z > 0)
+    item_o = Item{static_cast<unsigned int>(t.x), few_o ? kFewItemCost : kItemCost,
+                  few_o ? 1u : static_cast<unsigned int>(t.w) >> 16, t.y};
+  const unsigned int cost_p = item_p.cost(), cost_o = item_o.cost();
+  for (int h = blockIdx.y * (8 / W) + warp / W; h < p.H; h += gridDim.y * (8 / W)) {
+    const int g = h / p.group, hh = h - g * p.group;
+    const size_t orow = static_cast<size_t>(n) * p.H + h;
+    Item own = item_o, pre = item_p;
+    own.c0 += g * cost_o;
+    pre.c0 += g * per_head * cost_p;
+    const unsigned int share_o = shares[few_o];
+    if (rank < 0 && t.z > 0 && own.worker(0, share_o) == own.worker(own.units - 1, share_o)) continue;  // written already
+    float m = -INFINITY, sum = 0.f, acc[C];
 #pragma unroll
     for (int c = 0; c < C; ++c) acc[c] = 0.f;
+    // adds the parts that the lanes have (lse2 = -infinity: none)
+    auto add = [&](float lse2, const float* o, int count) {
+      float top = lse2;
 #pragma unroll
-    for (int w = 0; w < W; ++w) {
-      const float f = s_m[w] == -INFINITY ? (s_sum[w] == 0.f ? 0.f : s_sum[w]) : exp2f(s_m[w] - top);
-      sum += f * s_sum[w];
+      for (int w = 16; w; w >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, w));
+      top = fmaxf(top, m);
+      const float f = m == -INFINITY ? 0.f : exp2f(m - top), mine = lse2 == -INFINITY ? 0.f : exp2f(lse2 - top);
+      m = top;
+      float all = mine;
 #pragma unroll
-      for (int c = 0; c < C; ++c) acc[c] += f * s_acc[W > 1 ? w : 0][lane * C + c];
+      for (int w = 16; w; w >>= 1) all += __shfl_xor_sync(0xffffffffu, all, w);
+      sum = sum * f + all;
+#pragma unroll
+      for (int c = 0; c < C; ++c) acc[c] *= f;
+#pragma unroll 8
+      for (int k = 0; k < count; ++k) {
+        const float w = __shfl_sync(0xffffffffu, mine, k);
+        const float* src = reinterpret_cast<const float*>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(o), k)) + lane * C;
+        // (lanes without a part have weight 0 and the address of some other: loaded all the same, so that the loads
+        // of eight parts are under way together, and not added)
+        if (C == 4) {
+          const float4 v = *reinterpret_cast<const float4*>(src);
+          if (w != 0.f) {
+            acc[0] += w * v.x;
+            acc[1] += w * v.y;
+            acc[2 % C] += w * v.z;
+            acc[3 % C] += w * v.w;
+          }
+        } else {
+          const float2 v = *reinterpret_cast<const float2*>(src);
+          if (w != 0.f) {
+            acc[0] += w * v.x;
+            acc[1] += w * v.y;
+          }
+        }
+      }
+    };
+    // the item's parts: `seen` of its units visible to this row, row `at` of the item, `few`: its line
+    auto join = [&](const Item& it, bool few, bool is_own, int seen, int at) {
+      const unsigned int share = shares[few];
+      const int first = it.worker(0, share), last = it.worker(it.units - 1, share);
+      if (first == last) {
+        if (sub == 0)
+          add(lane == 0 ? (is_own ? p.own_lse : p.prefix_lse)[orow] : -INFINITY, (is_own ? p.own_o : p.prefix_o) + orow * D, 1);
+        return;
+      }
+      for (int w0 = first; w0 <= last; w0 += 32 * W) {
+        const int w = w0 + lane * W + sub;
+        float lse2 = -INFINITY;
+        const float* part = p.slab_o;
+        if (w <= last) {
+          const int j0 = it.from(w * share), j1 = it.from((w + 1) * share);
+          if (j0 < j1 && j0 < seen) {
+            const size_t row = (few ? few_slab(p, w, j0 == 0) : many_slab(p, w, j0 == 0)) + at;
+            part += row * D;
+            lse2 = p.slab_lse[row];
+          }
+        }
+        add(lse2, part, max(0, min(32, (last - w0 - sub + W) / W)));
+      }
+    };
+    if (rank >= 0) {
+      const int first = few_p ? 0 : n / (2 * p.tp) * 2 * p.tp;
+      join(pre, few_p, false, INT_MAX, (n - first) * p.group + hh);
     }
-    m = top;
+    if (t.z > 0) join(own, few_o, true, t.z, (t.w & (kTokFew - 1)) * p.group + hh);
+    if (W > 1) {  // the warps' sums, always in the same order
+      s_m[warp] = m;
+      s_sum[warp] = sum;
+#pragma unroll
+      for (int c = 0; c < C; ++c) s_acc[W > 1 ? warp : 0][lane * C + c] = acc[c];
+      __syncthreads();
+      float top = -INFINITY;
+#pragma unroll
+      for (int w = 0; w < W; ++w) top = fmaxf(top, s_m[w]);
+      sum = 0.f;
+#pragma unroll
+      for (int c = 0; c < C; ++c) acc[c] = 0.f;
+#pragma unroll
+      for (int w = 0; w < W; ++w) {
+        const float f = s_m[w] == -INFINITY ? s_sum[w] : exp2f(s_m[w] - top);  // (no part: 0; a NaN sum stays one)
+        sum += f * s_sum[w];
+#pragma unroll
+        for (int c = 0; c < C; ++c) acc[c] += f * s_acc[W > 1 ? w : 0][lane * C + c];
+      }
+      m = top;
+      __syncthreads();
+      if (warp > 0) continue;
+    }
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    __nv_bfloat16* out = p.o + orow * D + lane * C;
+    if (C == 4)
+      *reinterpret_cast<uint2*>(out) =
+          make_uint2(pack_bf16x2(acc[0] * inv, acc[1] * inv), pack_bf16x2(acc[2 % C] * inv, acc[3 % C] * inv));
+    else
+      *reinterpret_cast<uint32_t*>(out) = pack_bf16x2(acc[0] * inv, acc[1] * inv);
+    if (lane == 0) p.lse[orow] = sum == 0.f ? -INFINITY : (m + log2f(sum)) * LN2;
   }
-  const float inv = sum == 0.f ? 0.f : 1.f / sum;
-  __nv_bfloat16* out = p.o + orow * D + lane * C;
-  if (C == 4)
-    *reinterpret_cast<uint2*>(out) =
-        make_uint2(pack_bf16x2(acc[0] * inv, acc[1] * inv), pack_bf16x2(acc[2 % C] * inv, acc[3 % C] * inv));
-  else
-    *reinterpret_cast<uint32_t*>(out) = pack_bf16x2(acc[0] * inv, acc[1] * inv);
-  if (lane == 0) p.lse[orow] = sum == 0.f ? -INFINITY : (m + log2f(sum)) * LN2;
 }
 
 template <int D, int NT, int R>
 static cudaError_t launch(const PrefixMaps& t, const PrefixParams& p, cudaStream_t stream) {
-  constexpr int kSmem = PLayout<D>::SMEM_BYTES > FLayout<D, R>::SMEM_BYTES ? PLayout<D>::SMEM_BYTES : FLayout<D, R>::SMEM_BYTES;
-  static_assert(kSmem <= 232448 && FLayout<D, R>::STAGES >= 3, "shared memory");
   static bool attr_set[64] = {};
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev < 64 && !attr_set[dev]) {
-    e = cudaFuncSetAttribute(fa_prefix_kernel<D, NT, R>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    e = cudaFuncSetAttribute(fa_prefix_kernel<D, NT, R>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
     if (e != cudaSuccess) return e;
     attr_set[dev] = true;
   }
@@ -1413,17 +1495,17 @@ static cudaError_t launch(const PrefixMaps& t, const PrefixParams& p, cudaStream
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  const int plan_blocks = (p.N + 4 * kPlanThreads - 1) / (4 * kPlanThreads);
-  cfg.gridDim = dim3(plan_blocks < 64 ? plan_blocks : 64);
-  cfg.blockDim = dim3(kPlanThreads);
-  if ((e = cudaLaunchKernelEx(&cfg, fa_prefix_plan_kernel, p)) != cudaSuccess) return e;
   cfg.gridDim = dim3(p.ctas);
   cfg.blockDim = dim3(THREADS);
-  cfg.dynamicSmemBytes = kSmem;
+  cfg.dynamicSmemBytes = SMEM_BYTES;
   if ((e = cudaLaunchKernelEx(&cfg, fa_prefix_kernel<D, NT, R>, t.q, t.k, t.v, t.k16, t.v16, p)) != cudaSuccess) return e;
   const long long rows = static_cast<long long>(p.N) * p.H;
   const bool wide = rows < 1024;  // few rows: a block for each
-  cfg.gridDim = dim3(static_cast<unsigned int>(wide ? rows : (rows + 7) / 8));
+  const int heads = (p.H + 7) / 8, spread = (4 * p.ctas + p.N - 1) / p.N;  // else at least four blocks per SM
+  // not launched early: its blocks would gather on the SMs whose attention block ends first (46 -> 63 us for 64
+  // requests behind 16 384 keys)
+  cfg.numAttrs = 0;
+  cfg.gridDim = dim3(p.N, wide ? p.H : heads < spread ? heads : spread);
   cfg.blockDim = dim3(256);
   cfg.dynamicSmemBytes = 0;
   return wide ? cudaLaunchKernelEx(&cfg, fa_prefix_join_kernel<D, 8>, p)
