@@ -920,6 +920,7 @@ fa_status fa_fwd_prefix_paged(const void* q, const void* k_pages, const void* v_
   const long long most = static_cast<long long>(std::min(max_new, N)) * group, rows = most <= 64 ? most : group;
   p.few_rows = rows <= 8 || rows > 64 ? 8 : rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
   p.teams = p.few_rows <= 16 ? 8 : p.few_rows == 32 ? 4 : 2;
+  p.step = d == 64 ? 32 : 16;
   p.tiles_p = static_cast<int>(prefix_pages);
   p.tp = tp;
   const PrefixWorkspace w = prefix_workspace(N, H, Hkv, d);
@@ -938,7 +939,7 @@ fa_status fa_fwd_prefix_paged(const void* q, const void* k_pages, const void* v_
   const int planes = num_pages * Hkv;
   if (!encode_tensor_map(&t.q, q, N, H, d, false, group, 128, tp) ||
       !encode_page_map(&t.k, k_pages, planes, d, fa::kPage) || !encode_page_map(&t.v, v_pages, planes, d, fa::kPage) ||
-      !encode_page_map(&t.k16, k_pages, planes, d, 16) || !encode_page_map(&t.v16, v_pages, planes, d, 16))
+      !encode_page_map(&t.k16, k_pages, planes, d, p.step) || !encode_page_map(&t.v16, v_pages, planes, d, p.step))
     return FA_ERR_CUDA;
   if (fa::launch_fa_fwd_prefix(d, t, p, stream) != cudaSuccess) {
     cudaGetLastError();

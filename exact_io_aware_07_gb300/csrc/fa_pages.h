@@ -55,6 +55,7 @@ struct PrefixParams {
   int ctas;      // blocks of the attention kernel: one per SM, at most kPrefixMaxCtas
   int teams;     // few-row teams per block: 8, 4 or 2
   int few_rows;  // rows of a few-row item at most: 8, 16 (one warp), 32 or 64
+  int step;      // keys per few-row step: 16 (d = 128) or 32
   int tiles_p;   // 128-key tiles of the prefix
   int tp;        // tokens of a 128-row tile
   // workspace
@@ -72,7 +73,7 @@ struct PrefixParams {
 };
 constexpr int kPrefixMaxCtas = 160;
 // q: bf16 (d, H, N) with boxes of 64 columns x group heads x tp tokens; k, v: the page pools as (64, 128 rows, d / 64,
-// num_pages * Hkv) in boxes of whole pages, k16, v16: of 16 rows.
+// num_pages * Hkv) in boxes of whole pages, k16, v16: of `step` rows.
 struct PrefixMaps {
   CUtensorMap q, k, v, k16, v16;
 };

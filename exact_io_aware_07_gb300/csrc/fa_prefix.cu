@@ -21,7 +21,7 @@
 // There are two kinds of them, and every block works one of them:
 //   many rows: up to 256 rows on tcgen05 products, keys in tiles of 128 (bound by the tensor core);
 //   few rows:  the items of few requests (and the prefix, when all rows together are few) on warp-level
-//              products, keys in steps of 16, by teams of one, two or four warps (bound by loading the keys).
+//              products, keys in steps of 16 or 32, by teams of one, two or four warps (bound by loading the keys).
 // The items of a kind stand on a line, a key tile or step and an item taking so many places each, and the
 // kind's workers (blocks, or teams) get equal stretches of it: worker w the tiles whose places begin in
 // [w Q, (w + 1) Q).  So all workers have the same share whatever the lengths, and at most two items of a
@@ -37,15 +37,15 @@ namespace fa {
 static __device__ unsigned int g_prefix_status;  // kStatus* bits
 
 // Places on the lines.  Many rows: an item, and a key tile of an item with up to 128 and more rows; few rows: an
-// item, and one per step.  kManyTime / kFewTime: time of a place of either kind on one SM, for sharing out the SMs.
+// item, and one per step.  kManyTime / kFewTime: microseconds of a place of either kind on one SM, kManyStart: what the
+// many-row kind takes longer to start and end, for sharing out the SMs.
 constexpr unsigned int kItemCost = 8, kTileCost128 = 6, kTileCost256 = 8;
 constexpr unsigned int kFewItemCost = 4, kFewLeast = 4;  // (at least kFewLeast places for a team)
-constexpr float kManyTime = 0.2f, kFewTime = 0.08f;
-constexpr int kStep = 16;       // keys per step of the few-row kind
+constexpr float kManyTime = 0.22f, kFewTime = 0.08f, kManyStart = 6.f;
 constexpr int kBigRows = 128;   // rows from which a request is big
 constexpr int kMaxFlags = 1024; // row blocks of the batch whose need of the prefix is looked at one by one
-// words of p.hdr (two each where the lines have their own: many rows, few rows)
-enum { kHdrShare = 0, kHdrPrefixItems = 2, kHdrTokens };
+// words of p.hdr: both lines' shares, needed row blocks, tokens
+enum { kHdrShare = 0, kHdrItems = 2, kHdrTokens };
 constexpr int kTokFew = 1 << 15;  // in a token's fourth word: its item is on the few-row line
 
 constexpr int THREADS = 320;
@@ -71,8 +71,11 @@ struct Item {
 __device__ __forceinline__ Item many_item(unsigned int c0, int tiles, int rows) {
   return Item{c0, kItemCost, rows <= 128 ? kTileCost128 : kTileCost256, tiles};
 }
-__device__ __forceinline__ Item few_item(unsigned int c0, int keys) {
-  return Item{c0, kFewItemCost, 1u, (keys + kStep - 1) / kStep};
+// Keys per step of the few-row kind: 8 KB of K and V.
+template <int D>
+constexpr int kStep = D == 64 ? 32 : 16;
+__device__ __forceinline__ Item few_item(const PrefixParams& p, unsigned int c0, int keys) {
+  return Item{c0, kFewItemCost, 1u, (keys + p.step - 1) / p.step};
 }
 
 struct Request {
@@ -100,7 +103,7 @@ __device__ __forceinline__ Item block_item(const PrefixParams& p, const Request&
 // A request's places on its line.
 __device__ __forceinline__ unsigned int request_cost(const PrefixParams& p, const Request& r) {
   if (r.added == 0) return 0u;
-  if (is_few(p, r)) return few_item(0, visible(p, r, r.added)).cost() * p.Hkv;
+  if (is_few(p, r)) return few_item(p, 0, visible(p, r, r.added)).cost() * p.Hkv;
   unsigned int sum = 0;
   for (int blk = 0; blk * 2 * p.tp < r.added; ++blk) sum += block_item(p, r, blk, 0).cost();
   return sum * p.Hkv;
@@ -109,7 +112,7 @@ __device__ __forceinline__ unsigned int request_cost(const PrefixParams& p, cons
 // needed block of 2 tp tokens (each counted as a full one unless the batch is smaller).
 __device__ __forceinline__ bool few_prefix(const PrefixParams& p, int tokens) { return tokens * p.group <= p.few_rows; }
 __device__ __forceinline__ Item prefix_item(const PrefixParams& p, int tokens, unsigned int index) {
-  Item it = few_prefix(p, tokens) ? few_item(0, p.prefix_len) : many_item(0, p.tiles_p, min(2 * p.tp, tokens) * p.group);
+  Item it = few_prefix(p, tokens) ? few_item(p, 0, p.prefix_len) : many_item(0, p.tiles_p, min(2 * p.tp, tokens) * p.group);
   it.c0 = index * it.cost();
   return it;
 }
@@ -199,8 +202,10 @@ __device__ __forceinline__ Plan make_plan(const PrefixParams& p, Layout& s, vola
   l.total[1] = static_cast<unsigned int>(all >> 32);
   s.cum[tid] = before + sum - mine;
   s.first[tid] = first;
-  const float a = kManyTime * l.total[0], b = kFewTime * l.total[1];
-  l.many = l.total[0] == 0 ? 0 : l.total[1] == 0 ? p.ctas : max(1, min(p.ctas - 1, __float2int_rn(p.ctas * a / (a + b))));
+  // m blocks for the many-row line with m so that both kinds end together: kManyStart + A / m = B / (G - m)
+  const float a = kManyTime * l.total[0], b = kFewTime * l.total[1], g = p.ctas, d = kManyStart * g - a - b;
+  const float m = (d + sqrtf(d * d + 4.f * kManyStart * a * g)) / (2.f * kManyStart);
+  l.many = l.total[0] == 0 ? 0 : l.total[1] == 0 ? p.ctas : max(1, min(p.ctas - 1, __float2int_ru(m)));
   l.share[0] = max(1u, (l.total[0] + max(l.many, 1) - 1) / max(l.many, 1));
   const unsigned int teams = max(1, (p.ctas - l.many) * p.teams);
   l.share[1] = max(kFewLeast, (l.total[1] + teams - 1) / teams);
@@ -252,7 +257,7 @@ __device__ __forceinline__ Plan make_plan(const PrefixParams& p, Layout& s, vola
     int rank = -1;                     // no item of the prefix
     if (i >= 0 && i < r.added) {
       if (is_few(p, r)) {
-        const Item it = few_item(c0[1], visible(p, r, r.added));
+        const Item it = few_item(p, c0[1], visible(p, r, r.added));
         tok = make_int4(static_cast<int>(it.c0), it.units, it.units, i | kTokFew);
       } else {
         const int blk = i / (2 * p.tp);
@@ -279,7 +284,7 @@ __device__ __forceinline__ Plan make_plan(const PrefixParams& p, Layout& s, vola
     if (tid == 0) {
       p.hdr[kHdrShare] = static_cast<int>(l.share[0]);
       p.hdr[kHdrShare + 1] = static_cast<int>(l.share[1]);
-      p.hdr[kHdrPrefixItems] = l.items;
+      p.hdr[kHdrItems] = l.items;
       p.hdr[kHdrTokens] = l.tokens;
     }
     if (bad) atomicOr(&g_prefix_status, kStatusBadLength);
@@ -913,7 +918,7 @@ __device__ __forceinline__ void many_rows(const CUtensorMap& tmQ, const CUtensor
 }
 
 // ---------------------------------------------------------------- few rows
-// A team of R warps works items of up to 8 NT R rows, warp t of it rows 8 NT t .., keys in steps of 16.  A 128-row
+// A team of R warps works items of up to 8 NT R rows, warp t of it rows 8 NT t .., keys in steps of 16 or 32.  A 128-row
 // tcgen05 tile would spend its softmax on empty rows; here the products are warp-level and transposed, keys (or
 // columns of V) as the 16 rows of mma.sync m16n8k16 and query rows as its 8 columns:
 //   S^T (16 keys x 8 rows) = K Q^T,   O^T (16 columns x 8 rows) += V^T P^T,
@@ -926,8 +931,9 @@ constexpr int FEW_WARPS = 8;
 
 template <int D, int R>
 struct FLayout {
-  static constexpr int STEP_BYTES = 2 * kStep * D * 2;  // K, then V; 64 columns per box of 16 rows x 128 bytes
-  static constexpr int BOX = kStep * 128;
+  static constexpr int STEP = kStep<D>;
+  static constexpr int STEP_BYTES = 2 * STEP * D * 2;  // K, then V; 64 columns per box of STEP rows x 128 bytes
+  static constexpr int BOX = STEP * 128;
   static constexpr int TEAMS = FEW_WARPS / R;
   static constexpr int FIT = PLayout<D>::XCH_OFF / (TEAMS * STEP_BYTES);
   static constexpr int STAGES = FIT < 12 ? FIT : 12;
@@ -1033,7 +1039,7 @@ struct FewWalk {
         r = make_request(p, __shfl_sync(0xffffffffu, cu0, b - base), __shfl_sync(0xffffffffu, cu1, b - base),
                          __shfl_sync(0xffffffffu, seq, b - base));
         if (r.added == 0 || !is_few(p, r)) continue;
-        it = few_item(c0, visible(p, r, r.added));
+        it = few_item(p, c0, visible(p, r, r.added));
         cost = it.cost();
         if (c0 + p.Hkv * cost > x0 && cost > 0) break;
         c0 += p.Hkv * cost;
@@ -1068,32 +1074,47 @@ __device__ __forceinline__ void few_rows(const CUtensorMap& tmK, const CUtensorM
   const int first = uni(begin->b);
   const unsigned int first_place = uni(begin->c0);
 
-  // the ring's filling side (the team's first warp)
+  // The ring's filling side (the team's first warp).  It stands a piece ahead: the next piece's pages (32 tiles', one per
+  // lane) and query rows are asked for when the piece before it begins.
   FewWalk load;
-  FewPiece lp;
-  int lj = 0, issued = 0, lstage = 0;
-  bool more = mt == 0;
-  const int* held_table = nullptr;  // page numbers of 32 tiles of one table row, one per lane
-  int held_base = -1, held_page = 0;
+  FewPiece lp, ahead;
+  int lj = 0, issued = 0, lstage = 0, page = 0, base = 0, ahead_page = 0;
+  bool more = mt == 0, any = false;
+  auto look_ahead = [&] {
+    any = load.next(p, lane, ahead);
+    if (!any) return;
+    const int first_tile = ahead.j0 / (kPage / L::STEP) & ~31;
+    ahead_page = first_tile + lane < ahead.entries ? ahead.table[first_tile + lane] : 0;
+    for (int r = lane; r < ahead.rows; r += 32) {
+      const int tok = r / p.group;
+      const __nv_bfloat16* src = p.q + (static_cast<size_t>(ahead.t0 + tok) * p.H + ahead.g * p.group + (r - tok * p.group)) * D;
+      asm volatile("prefetch.global.L2 [%0];" ::"l"(src));
+      if (D == 128) asm volatile("prefetch.global.L2 [%0];" ::"l"(src + 64));
+    }
+  };
   if (mt == 0) {
     load.start(p, l, x0, x1, first, first_place);
     lp.j1 = 0;
+    look_ahead();
   }
   auto fill = [&]() -> bool {  // loads the stretch's next step, if there is one
     if (lj >= lp.j1) {
-      if (!load.next(p, lane, lp)) {
+      if (!any) {
         more = false;
         return true;
       }
+      lp = ahead;
       lj = lp.j0;
+      page = ahead_page;
+      base = lj / (kPage / L::STEP) & ~31;
+      look_ahead();
     }
-    const int tile = lj / (kPage / kStep);
-    if (lp.table != held_table || (tile & ~31) != held_base) {
-      held_table = lp.table;
-      held_base = tile & ~31;
-      held_page = held_base + lane < lp.entries ? lp.table[held_base + lane] : 0;
+    const int tile = lj / (kPage / L::STEP);
+    if ((tile & ~31) != base) {
+      base = tile & ~31;
+      page = base + lane < lp.entries ? lp.table[base + lane] : 0;
     }
-    int pg = __shfl_sync(0xffffffffu, held_page, tile & 31);
+    int pg = __shfl_sync(0xffffffffu, page, tile & 31);
     if (pg < 0 || pg >= p.num_pages) {  // out of the pool: reads zeros and is reported
       if (lane == 0) atomicOr(&g_prefix_status, kStatusBadPage);
       pg = p.num_pages;
@@ -1101,7 +1122,7 @@ __device__ __forceinline__ void few_rows(const CUtensorMap& tmK, const CUtensorM
     if (R > 1 && issued >= L::STAGES &&
         !wait_all(W, bar_empty + 8 * lstage, (issued / L::STAGES - 1) & 1))
       return false;
-    load_rows2_elect(ring + lstage * L::STEP_BYTES, L::STEP_BYTES / 2, &tmK, &tmV, (lj % (kPage / kStep)) * kStep,
+    load_rows2_elect(ring + lstage * L::STEP_BYTES, L::STEP_BYTES / 2, &tmK, &tmV, (lj % (kPage / L::STEP)) * L::STEP,
                      pg * p.Hkv + lp.g, bar_full + 8 * lstage);
     ++lj;
     ++issued;
@@ -1169,32 +1190,43 @@ __device__ __forceinline__ void few_rows(const CUtensorMap& tmK, const CUtensorM
       if (!(ok = wait_all(W, bar_full + 8 * stage, (full_par >> stage) & 1))) break;
       full_par ^= 1u << stage;
       const uint32_t at = stage * L::STEP_BYTES;
-      const int k0 = j * kStep;
-      float s[NT][4], s2[NT][4];  // two chains of products
+      const int k0 = j * L::STEP;
+      constexpr int U = L::STEP / 16, CHAINS = U == 1 ? 2 : 1;  // sixteens of keys; chains of products for each
+      float s[U][NT][4], s2[NT][4];
 #pragma unroll
       for (int t = 0; t < NT; ++t)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) s[t][e] = s2[t][e] = 0.f;
+        for (int e = 0; e < 4; ++e) {
+          s2[t][e] = 0.f;
 #pragma unroll
-      for (int kk = 0; kk < D / 16; ++kk) {
-        uint32_t a[4];
-        ldmatrix_x4(a, k_at[kk % 4] + at + (kk / 4) * L::BOX);
+          for (int u = 0; u < U; ++u) s[u][t][e] = 0.f;
+        }
 #pragma unroll
-        for (int t = 0; t < NT; ++t) mma_16816(kk & 1 ? s2[t] : s[t], a, qf[kk][t][0], qf[kk][t][1]);
-      }
+      for (int kk = 0; kk < D / 16; ++kk)
 #pragma unroll
-      for (int t = 0; t < NT; ++t)
+        for (int u = 0; u < U; ++u) {
+          uint32_t a[4];
+          ldmatrix_x4(a, k_at[kk % 4] + at + (kk / 4) * L::BOX + u * 2048);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) s[t][e] += s2[t][e];
-      if (k0 + kStep > lim_min) {  // some row does not see all of these keys
-        const int key = k0 + lane / 4;
+          for (int t = 0; t < NT; ++t) mma_16816(CHAINS == 2 && (kk & 1) ? s2[t] : s[u][t], a, qf[kk][t][0], qf[kk][t][1]);
+        }
+      if (CHAINS == 2)
 #pragma unroll
         for (int t = 0; t < NT; ++t)
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            if (key >= lim[t][e]) s[t][e] = -INFINITY;
-            if (key + 8 >= lim[t][e]) s[t][2 + e] = -INFINITY;
-          }
+          for (int e = 0; e < 4; ++e) s[0][t][e] += s2[t][e];
+      if (k0 + L::STEP > lim_min) {  // some row does not see all of these keys
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const int key = k0 + u * 16 + lane / 4;
+#pragma unroll
+          for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              if (key >= lim[t][e]) s[u][t][e] = -INFINITY;
+              if (key + 8 >= lim[t][e]) s[u][t][2 + e] = -INFINITY;
+            }
+        }
       }
       float x[NT][2];
       bool grows = false;
@@ -1202,7 +1234,9 @@ __device__ __forceinline__ void few_rows(const CUtensorMap& tmK, const CUtensorM
       for (int t = 0; t < NT; ++t)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          x[t][e] = fmaxf(s[t][e], s[t][2 + e]);
+          x[t][e] = fmaxf(s[0][t][e], s[0][t][2 + e]);
+#pragma unroll
+          for (int u = 1; u < U; ++u) x[t][e] = fmaxf(x[t][e], fmaxf(s[u][t][e], s[u][t][2 + e]));
 #pragma unroll
           for (int w = 4; w <= 16; w <<= 1) x[t][e] = fmaxf(x[t][e], __shfl_xor_sync(0xffffffffu, x[t][e], w));
           x[t][e] *= sl2;
@@ -1226,37 +1260,43 @@ __device__ __forceinline__ void few_rows(const CUtensorMap& tmK, const CUtensorM
             }
           }
       }
-      uint32_t pt[NT][2];  // P^T
+      uint32_t pt[U][NT][2];  // P^T
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
         const float z0 = m[t][0] == -INFINITY ? 0.f : -m[t][0], z1 = m[t][1] == -INFINITY ? 0.f : -m[t][1];
-        const float p0 = ex2_approx(fmaf(s[t][0], sl2, z0)), p1 = ex2_approx(fmaf(s[t][1], sl2, z1));
-        const float p2 = ex2_approx(fmaf(s[t][2], sl2, z0)), p3 = ex2_approx(fmaf(s[t][3], sl2, z1));
-        lw[t][0] += p0 + p2;
-        lw[t][1] += p1 + p3;
-        pt[t][0] = transpose_8x8(pack_bf16x2(p0, p1));
-        pt[t][1] = transpose_8x8(pack_bf16x2(p2, p3));
-        mma_16816(lr[t], ones, pt[t][0], pt[t][1]);
-      }
-      const int left = q.keys - k0;
-      // value rows behind the source's last key may hold anything: they count as 0 (their weights are 0 too)
-      uint32_t v0 = 0xFFFFFFFFu, v1 = 0xFFFFFFFFu;
-      if (left < kStep) {
-        v0 = (c0 < left ? 0xFFFFu : 0u) | (c0 + 1 < left ? 0xFFFF0000u : 0u);
-        v1 = (c0 + 8 < left ? 0xFFFFu : 0u) | (c0 + 9 < left ? 0xFFFF0000u : 0u);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const float p0 = ex2_approx(fmaf(s[u][t][0], sl2, z0)), p1 = ex2_approx(fmaf(s[u][t][1], sl2, z1));
+          const float p2 = ex2_approx(fmaf(s[u][t][2], sl2, z0)), p3 = ex2_approx(fmaf(s[u][t][3], sl2, z1));
+          lw[t][0] += p0 + p2;
+          lw[t][1] += p1 + p3;
+          pt[u][t][0] = transpose_8x8(pack_bf16x2(p0, p1));
+          pt[u][t][1] = transpose_8x8(pack_bf16x2(p2, p3));
+          mma_16816(lr[t], ones, pt[u][t][0], pt[u][t][1]);
+        }
       }
 #pragma unroll
-      for (int c = 0; c < D / 16; ++c) {
-        uint32_t a[4];
-        ldmatrix_x4_trans(a, v_at[c % 4] + at + (c / 4) * L::BOX);
-        if (left < kStep) {
-          a[0] &= v0;
-          a[1] &= v0;
-          a[2] &= v1;
-          a[3] &= v1;
+      for (int u = 0; u < U; ++u) {
+        const int left = q.keys - k0 - u * 16;
+        // value rows behind the source's last key may hold anything: they count as 0 (their weights are 0 too)
+        uint32_t v0 = 0xFFFFFFFFu, v1 = 0xFFFFFFFFu;
+        if (left < 16) {
+          v0 = (c0 < left ? 0xFFFFu : 0u) | (c0 + 1 < left ? 0xFFFF0000u : 0u);
+          v1 = (c0 + 8 < left ? 0xFFFFu : 0u) | (c0 + 9 < left ? 0xFFFF0000u : 0u);
         }
 #pragma unroll
-        for (int t = 0; t < NT; ++t) mma_16816(o[c][t], a, pt[t][0], pt[t][1]);
+        for (int c = 0; c < D / 16; ++c) {
+          uint32_t a[4];
+          ldmatrix_x4_trans(a, v_at[c % 4] + at + (c / 4) * L::BOX + u * 2048);
+          if (left < 16) {
+            a[0] &= v0;
+            a[1] &= v0;
+            a[2] &= v1;
+            a[3] &= v1;
+          }
+#pragma unroll
+          for (int t = 0; t < NT; ++t) mma_16816(o[c][t], a, pt[u][t][0], pt[u][t][1]);
+        }
       }
       __syncwarp();
       if (R > 1 && lane == 0) mbar_arrive(bar_empty + 8 * stage);
@@ -1344,136 +1384,188 @@ fa_prefix_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
 }
 
 // ---------------------------------------------------------------- join
-// W warps join a row, every lane D / 32 columns.  The parts of a row follow from the places of its items: an item
-// inside one worker's stretch has one part, with the rows of its source; one that is cut has a part in a slab of
-// every worker that worked some of its units.  The lanes look up 32 workers at a time (warp w of W every W-th).
-// blockIdx.x: token; the block's warps take every (gridDim.y * 8 / W)-th head.
+// The parts of a row follow from the places of its items: an item inside one worker's stretch has one part, with the
+// rows of its source; one that is cut has a part in a slab of every worker that worked some of its units.
+struct Parts {
+  Item it;
+  bool few;
+  int first, count, seen, at;  // first worker, workers; units visible to the row; the row's number within the item
+  __device__ __forceinline__ void locate(unsigned int share) {
+    first = it.worker(0, share);
+    count = it.worker(it.units - 1, share) - first + 1;
+  }
+  // Row of the slabs that worker `first + i` wrote the part to; -1 if it had none of the row's units.
+  __device__ __forceinline__ long long slab_row(const PrefixParams& p, unsigned int share, int i) const {
+    const int w = first + i, j0 = it.from(w * share), j1 = it.from((w + 1) * share);
+    if (j0 >= j1 || j0 >= seen) return -1;
+    return static_cast<long long>((few ? few_slab(p, w, j0 == 0) : many_slab(p, w, j0 == 0)) + at);
+  }
+};
+
+// Joins row n * H + h (W warps together, every lane D / 32 columns): t and rank are the token's.  The lanes look up 32
+// parts at a time (warp w of W every W-th), weight them by their LSE and add them eight loads at a time.
 template <int D, int W>
-__global__ void __launch_bounds__(256) fa_prefix_join_kernel(const __grid_constant__ PrefixParams p) {
+__device__ __forceinline__ void join_row(const PrefixParams& p, const Plan& l, size_t orow, int4 t, int rank, int warp, int lane,
+                                         float* smem) {
   constexpr int C = D / 32;
-  __shared__ float s_acc[W > 1 ? 8 : 1][D], s_m[8], s_sum[8];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = warp % W;
-  const int n = blockIdx.x;
-  pdl_launch_dependents();  // (a following call's blocks set themselves up meanwhile)
-  const int4 t = p.tok[n];  // (past the last token: whatever, not used)
-  const int rank = p.rank[n], tokens = p.hdr[kHdrTokens], per_head = p.hdr[kHdrPrefixItems];
-  const unsigned int shares[2] = {static_cast<unsigned int>(p.hdr[kHdrShare]), static_cast<unsigned int>(p.hdr[kHdrShare + 1])};
-  if (n >= tokens) return;
-  const bool few_p = few_prefix(p, tokens), few_o = t.w & kTokFew;
-  Item item_p{0, 0, 0, 0}, item_o{0, 0, 0, 0};
-  if (rank >= 0) item_p = prefix_item(p, tokens, rank);
-  if (t.z > 0)
-    item_o = Item{static_cast<unsigned int>(t.x), few_o ? kFewItemCost : kItemCost,
-                  few_o ? 1u : static_cast<unsigned int>(t.w) >> 16, t.y};
-  const unsigned int cost_p = item_p.cost(), cost_o = item_o.cost();
-  for (int h = blockIdx.y * (8 / W) + warp / W; h < p.H; h += gridDim.y * (8 / W)) {
-    const int g = h / p.group, hh = h - g * p.group;
-    const size_t orow = static_cast<size_t>(n) * p.H + h;
-    Item own = item_o, pre = item_p;
-    own.c0 += g * cost_o;
-    pre.c0 += g * per_head * cost_p;
-    const unsigned int share_o = shares[few_o];
-    if (rank < 0 && t.z > 0 && own.worker(0, share_o) == own.worker(own.units - 1, share_o)) continue;  // written already
-    float m = -INFINITY, sum = 0.f, acc[C];
+  const int n = static_cast<int>(orow / p.H), h = static_cast<int>(orow - static_cast<size_t>(n) * p.H);
+  const int g = h / p.group, hh = h - g * p.group;
+  Parts pre, own;
+  pre.count = own.count = 0;
+  if (rank >= 0) {
+    pre.few = few_prefix(p, l.tokens);
+    pre.it = prefix_item(p, l.tokens, g * l.items + rank);
+    pre.seen = INT_MAX;
+    pre.at = (pre.few ? n : n % (2 * p.tp)) * p.group + hh;
+    pre.locate(pre.few ? l.share[1] : l.share[0]);
+  }
+  if (t.z > 0) {
+    own.few = t.w & kTokFew;
+    own.it = Item{static_cast<unsigned int>(t.x), own.few ? kFewItemCost : kItemCost,
+                  own.few ? 1u : static_cast<unsigned int>(t.w) >> 16, t.y};
+    own.it.c0 += g * own.it.cost();
+    own.seen = t.z;
+    own.at = (t.w & (kTokFew - 1)) * p.group + hh;
+    own.locate(own.few ? l.share[1] : l.share[0]);
+  }
+  float m = -INFINITY, sum = 0.f, acc[C];
+#pragma unroll
+  for (int c = 0; c < C; ++c) acc[c] = 0.f;
+  const int parts = pre.count + own.count;
+  for (int i0 = 0; i0 < parts; i0 += 32 * W) {
+    int i = i0 + lane * W + (W > 1 ? warp : 0);
+    float lse2 = -INFINITY;
+    const float* o = p.slab_o;
+    if (i < parts) {
+      const bool is_own = i >= pre.count;
+      if ((is_own ? own.count : pre.count) == 1) {
+        o = (is_own ? p.own_o : p.prefix_o) + orow * D;
+        lse2 = __ldg((is_own ? p.own_lse : p.prefix_lse) + orow);
+      } else {
+        const long long row = is_own ? own.slab_row(p, own.few ? l.share[1] : l.share[0], i - pre.count)
+                                     : pre.slab_row(p, pre.few ? l.share[1] : l.share[0], i);
+        if (row >= 0) {
+          o = p.slab_o + row * D;
+          lse2 = __ldg(p.slab_lse + row);
+        }
+      }
+    }
+    float top = lse2;
+#pragma unroll
+    for (int w = 16; w; w >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, w));
+    top = fmaxf(top, m);
+    const float f = m == -INFINITY ? 0.f : exp2f(m - top), mine = lse2 == -INFINITY ? 0.f : exp2f(lse2 - top);
+    m = top;
+    float all = mine;
+#pragma unroll
+    for (int w = 16; w; w >>= 1) all += __shfl_xor_sync(0xffffffffu, all, w);
+    sum = sum * f + all;
+#pragma unroll
+    for (int c = 0; c < C; ++c) acc[c] *= f;
+    const int here = min(32, (parts - i0 + W - 1) / W);
+#pragma unroll 8
+    for (int k = 0; k < here; ++k) {
+      const float w = __shfl_sync(0xffffffffu, mine, k);
+      const float* src = reinterpret_cast<const float*>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(o), k)) + lane * C;
+      // (lanes without a part have weight 0 and the address of some other: loaded all the same, so that the loads of
+      // eight parts are under way together, and not added)
+      if (C == 4) {
+        const float4 v = __ldg(reinterpret_cast<const float4*>(src));
+        if (w != 0.f) {
+          acc[0] += w * v.x;
+          acc[1] += w * v.y;
+          acc[2 % C] += w * v.z;
+          acc[3 % C] += w * v.w;
+        }
+      } else {
+        const float2 v = __ldg(reinterpret_cast<const float2*>(src));
+        if (w != 0.f) {
+          acc[0] += w * v.x;
+          acc[1] += w * v.y;
+        }
+      }
+    }
+  }
+  if (W > 1) {  // the warps' sums, always in the same order
+    float(*s_acc)[D] = reinterpret_cast<float(*)[D]>(smem);
+    float* s_m = smem + W * D;
+    float* s_sum = s_m + W;
+    s_m[warp] = m;
+    s_sum[warp] = sum;
+#pragma unroll
+    for (int c = 0; c < C; ++c) s_acc[warp][lane * C + c] = acc[c];
+    __syncthreads();
+    float top = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < W; ++w) top = fmaxf(top, s_m[w]);
+    sum = 0.f;
 #pragma unroll
     for (int c = 0; c < C; ++c) acc[c] = 0.f;
-    // adds the parts that the lanes have (lse2 = -infinity: none)
-    auto add = [&](float lse2, const float* o, int count) {
-      float top = lse2;
 #pragma unroll
-      for (int w = 16; w; w >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, w));
-      top = fmaxf(top, m);
-      const float f = m == -INFINITY ? 0.f : exp2f(m - top), mine = lse2 == -INFINITY ? 0.f : exp2f(lse2 - top);
-      m = top;
-      float all = mine;
+    for (int w = 0; w < W; ++w) {
+      const float f = s_m[w] == -INFINITY ? s_sum[w] : exp2f(s_m[w] - top);  // (no part: 0; a NaN sum stays one)
+      sum += f * s_sum[w];
 #pragma unroll
-      for (int w = 16; w; w >>= 1) all += __shfl_xor_sync(0xffffffffu, all, w);
-      sum = sum * f + all;
-#pragma unroll
-      for (int c = 0; c < C; ++c) acc[c] *= f;
-#pragma unroll 8
-      for (int k = 0; k < count; ++k) {
-        const float w = __shfl_sync(0xffffffffu, mine, k);
-        const float* src = reinterpret_cast<const float*>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(o), k)) + lane * C;
-        // (lanes without a part have weight 0 and the address of some other: loaded all the same, so that the loads
-        // of eight parts are under way together, and not added)
-        if (C == 4) {
-          const float4 v = *reinterpret_cast<const float4*>(src);
-          if (w != 0.f) {
-            acc[0] += w * v.x;
-            acc[1] += w * v.y;
-            acc[2 % C] += w * v.z;
-            acc[3 % C] += w * v.w;
-          }
-        } else {
-          const float2 v = *reinterpret_cast<const float2*>(src);
-          if (w != 0.f) {
-            acc[0] += w * v.x;
-            acc[1] += w * v.y;
-          }
-        }
-      }
-    };
-    // the item's parts: `seen` of its units visible to this row, row `at` of the item, `few`: its line
-    auto join = [&](const Item& it, bool few, bool is_own, int seen, int at) {
-      const unsigned int share = shares[few];
-      const int first = it.worker(0, share), last = it.worker(it.units - 1, share);
-      if (first == last) {
-        if (sub == 0)
-          add(lane == 0 ? (is_own ? p.own_lse : p.prefix_lse)[orow] : -INFINITY, (is_own ? p.own_o : p.prefix_o) + orow * D, 1);
-        return;
-      }
-      for (int w0 = first; w0 <= last; w0 += 32 * W) {
-        const int w = w0 + lane * W + sub;
-        float lse2 = -INFINITY;
-        const float* part = p.slab_o;
-        if (w <= last) {
-          const int j0 = it.from(w * share), j1 = it.from((w + 1) * share);
-          if (j0 < j1 && j0 < seen) {
-            const size_t row = (few ? few_slab(p, w, j0 == 0) : many_slab(p, w, j0 == 0)) + at;
-            part += row * D;
-            lse2 = p.slab_lse[row];
-          }
-        }
-        add(lse2, part, max(0, min(32, (last - w0 - sub + W) / W)));
-      }
-    };
-    if (rank >= 0) {
-      const int first = few_p ? 0 : n / (2 * p.tp) * 2 * p.tp;
-      join(pre, few_p, false, INT_MAX, (n - first) * p.group + hh);
+      for (int c = 0; c < C; ++c) acc[c] += f * s_acc[w][lane * C + c];
     }
-    if (t.z > 0) join(own, few_o, true, t.z, (t.w & (kTokFew - 1)) * p.group + hh);
-    if (W > 1) {  // the warps' sums, always in the same order
-      s_m[warp] = m;
-      s_sum[warp] = sum;
-#pragma unroll
-      for (int c = 0; c < C; ++c) s_acc[W > 1 ? warp : 0][lane * C + c] = acc[c];
-      __syncthreads();
-      float top = -INFINITY;
-#pragma unroll
-      for (int w = 0; w < W; ++w) top = fmaxf(top, s_m[w]);
-      sum = 0.f;
-#pragma unroll
-      for (int c = 0; c < C; ++c) acc[c] = 0.f;
-#pragma unroll
-      for (int w = 0; w < W; ++w) {
-        const float f = s_m[w] == -INFINITY ? s_sum[w] : exp2f(s_m[w] - top);  // (no part: 0; a NaN sum stays one)
-        sum += f * s_sum[w];
-#pragma unroll
-        for (int c = 0; c < C; ++c) acc[c] += f * s_acc[W > 1 ? w : 0][lane * C + c];
-      }
-      m = top;
-      __syncthreads();
-      if (warp > 0) continue;
-    }
-    const float inv = sum == 0.f ? 0.f : 1.f / sum;
-    __nv_bfloat16* out = p.o + orow * D + lane * C;
-    if (C == 4)
-      *reinterpret_cast<uint2*>(out) =
-          make_uint2(pack_bf16x2(acc[0] * inv, acc[1] * inv), pack_bf16x2(acc[2 % C] * inv, acc[3 % C] * inv));
-    else
-      *reinterpret_cast<uint32_t*>(out) = pack_bf16x2(acc[0] * inv, acc[1] * inv);
-    if (lane == 0) p.lse[orow] = sum == 0.f ? -INFINITY : (m + log2f(sum)) * LN2;
+    m = top;
+    if (warp > 0) return;
+  }
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;
+  __nv_bfloat16* out = p.o + orow * D + lane * C;
+  if (C == 4)
+    *reinterpret_cast<uint2*>(out) =
+        make_uint2(pack_bf16x2(acc[0] * inv, acc[1] * inv), pack_bf16x2(acc[2 % C] * inv, acc[3 % C] * inv));
+  else
+    *reinterpret_cast<uint32_t*>(out) = pack_bf16x2(acc[0] * inv, acc[1] * inv);
+  if (lane == 0) p.lse[orow] = sum == 0.f ? -INFINITY : (m + log2f(sum)) * LN2;
+}
+
+// Whether a row of K/V head g has to be joined: it has no, or several parts.  (A row with one item and that inside one
+// worker's stretch is written already.)
+__device__ __forceinline__ bool needs_join(const Plan& l, const int4& t, int rank, int g) {
+  if (rank >= 0 || t.z == 0) return true;
+  const bool few = t.w & kTokFew;
+  Item it{static_cast<unsigned int>(t.x), few ? kFewItemCost : kItemCost, few ? 1u : static_cast<unsigned int>(t.w) >> 16, t.y};
+  it.c0 += g * it.cost();
+  const unsigned int share = few ? l.share[1] : l.share[0];
+  return it.worker(0, share) != it.worker(it.units - 1, share);
+}
+
+// Joins the rows that need it.  W = 8: a row per block (few rows, perhaps of many parts); W = 1: `per_warp` rows per
+// warp, its lanes first looking through them for those to join.
+template <int D, int W>
+__global__ void __launch_bounds__(256) fa_prefix_join_kernel(const __grid_constant__ PrefixParams p, int per_warp) {
+  __shared__ float smem[W > 1 ? W * D + 2 * W : 1];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const long long first = W > 1 ? blockIdx.x : blockIdx.x + static_cast<long long>(gridDim.x) * warp;  // then every stride-th
+  const long long stride = static_cast<long long>(gridDim.x) * 8;
+  pdl_launch_dependents();  // a following call's blocks may set themselves up
+  const long long all = static_cast<long long>(p.N) * p.H, row = first + stride * lane;
+  int4 t = make_int4(0, 0, 0, 0);
+  int rank = -1;
+  if (W > 1 || (lane < per_warp && row < all)) {
+    const int n = static_cast<int>((W > 1 ? first : row) / p.H);
+    t = p.tok[n];  // (past the last token: whatever, not used)
+    rank = p.rank[n];
+  }
+  Plan l;
+  l.share[0] = p.hdr[kHdrShare];
+  l.share[1] = p.hdr[kHdrShare + 1];
+  l.items = p.hdr[kHdrItems];
+  l.tokens = p.hdr[kHdrTokens];
+  const long long rows = static_cast<long long>(l.tokens) * p.H;
+  if (W > 1) {
+    if (first < rows && needs_join(l, t, rank, static_cast<int>(first % p.H) / p.group))
+      join_row<D, W>(p, l, static_cast<size_t>(first), t, rank, warp, lane, smem);
+    return;
+  }
+  const bool need = lane < per_warp && row < rows && needs_join(l, t, rank, static_cast<int>(row % p.H) / p.group);
+  for (unsigned int todo = __ballot_sync(0xffffffffu, need); todo; todo &= todo - 1) {
+    const int k = __ffs(todo) - 1;
+    const int4 tk = make_int4(__shfl_sync(0xffffffffu, t.x, k), __shfl_sync(0xffffffffu, t.y, k),
+                              __shfl_sync(0xffffffffu, t.z, k), __shfl_sync(0xffffffffu, t.w, k));
+    join_row<D, 1>(p, l, static_cast<size_t>(first + stride * k), tk, __shfl_sync(0xffffffffu, rank, k), warp, lane, smem);
   }
 }
 
@@ -1500,16 +1592,17 @@ static cudaError_t launch(const PrefixMaps& t, const PrefixParams& p, cudaStream
   cfg.dynamicSmemBytes = SMEM_BYTES;
   if ((e = cudaLaunchKernelEx(&cfg, fa_prefix_kernel<D, NT, R>, t.q, t.k, t.v, t.k16, t.v16, p)) != cudaSuccess) return e;
   const long long rows = static_cast<long long>(p.N) * p.H;
-  const bool wide = rows < 1024;  // few rows: a block for each
-  const int heads = (p.H + 7) / 8, spread = (4 * p.ctas + p.N - 1) / p.N;  // else at least four blocks per SM
+  const bool wide = rows < 4 * p.ctas;
+  long long per_warp = (rows + 48 * p.ctas - 1) / (48 * p.ctas);  // about as many warps as the SMs hold
+  per_warp = per_warp > 32 ? 32 : per_warp;
   // not launched early: its blocks would gather on the SMs whose attention block ends first (46 -> 63 us for 64
   // requests behind 16 384 keys)
   cfg.numAttrs = 0;
-  cfg.gridDim = dim3(p.N, wide ? p.H : heads < spread ? heads : spread);
+  cfg.gridDim = dim3(static_cast<unsigned int>(wide ? rows : (rows + 8 * per_warp - 1) / (8 * per_warp)));
   cfg.blockDim = dim3(256);
   cfg.dynamicSmemBytes = 0;
-  return wide ? cudaLaunchKernelEx(&cfg, fa_prefix_join_kernel<D, 8>, p)
-              : cudaLaunchKernelEx(&cfg, fa_prefix_join_kernel<D, 1>, p);
+  return wide ? cudaLaunchKernelEx(&cfg, fa_prefix_join_kernel<D, 8>, p, 1)
+              : cudaLaunchKernelEx(&cfg, fa_prefix_join_kernel<D, 1>, p, static_cast<int>(per_warp));
 }
 
 cudaError_t launch_fa_fwd_prefix(int d, const PrefixMaps& t, const PrefixParams& p, cudaStream_t stream) {
@@ -1525,7 +1618,7 @@ cudaError_t launch_fa_fwd_prefix(int d, const PrefixMaps& t, const PrefixParams&
 
 unsigned int prefix_page_cost() { return kTileCost256; }
 unsigned int prefix_item_cost() { return kItemCost; }
-static_assert(kTileCost256 >= kPage / kStep && kItemCost >= kFewItemCost, "prefix_page_cost, prefix_item_cost");
+static_assert(kTileCost256 >= kPage / kStep<128> && kItemCost >= kFewItemCost, "prefix_page_cost, prefix_item_cost");
 
 cudaError_t read_and_clear_prefix_status(cudaStream_t stream, unsigned int* out) {
   cudaError_t e = cudaStreamSynchronize(stream);
