@@ -151,8 +151,8 @@ def fa_fwd_launch_shape(B: int, H: int, T: int, d: int, causal: bool, num_sms: i
 def _stream_handle(stream):
     import torch
 
-    if stream is None:
-        return torch.cuda.current_stream().cuda_stream
+    if stream is None:  # the raw handle: making a Stream object of it takes 2.5 us
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -266,25 +266,22 @@ def fa_fwd_paged(q, k_pages, v_pages, block_table, o, lse, causal: bool, scale: 
         raise FAError(code, "fa_fwd_paged")
 
 
-def _check_ints(**tensors):
-    import torch
-
-    for name, (t, shape) in tensors.items():
-        if t.dtype != torch.int32 or tuple(t.shape) != shape or not t.is_contiguous():
-            raise ValueError(f"{name} must be a contiguous int32 tensor of shape {shape}")
+def _check_int(name, t, shape, int32):
+    if t.dtype is not int32 or t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous int32 tensor of shape {shape}")
 
 
 def _check_pools(k_pages, v_pages):
     """(num_pages, Hkv, d) of two page pools."""
     import torch
 
+    shape = k_pages.shape
     for name, t in (("k_pages", k_pages), ("v_pages", v_pages)):
-        if t.dtype != torch.bfloat16 or t.dim() != 4 or not t.is_contiguous():
+        if t.dtype is not torch.bfloat16 or t.dim() != 4 or not t.is_contiguous():
             raise ValueError(f"{name} must be a contiguous bf16 4-D tensor")
-    num_pages, Hkv, page, d = k_pages.shape
-    if page != PAGE or v_pages.shape != k_pages.shape:
+    if shape[2] != PAGE or v_pages.shape != shape:
         raise ValueError(f"pages must be (num_pages, Hkv, {PAGE}, d)")
-    return num_pages, Hkv, d
+    return shape[0], shape[1], shape[3]
 
 
 def fa_page_plan(ctx_lens, new_lens, free_pages, free_head, block_table, seq_lens, cu_new, slot_map, free_head_out,
@@ -295,18 +292,26 @@ def fa_page_plan(ctx_lens, new_lens, free_pages, free_head, block_table, seq_len
     free_head (1), how many of them are taken.  Updates block_table (B, max_pages) in place; writes seq_lens (B),
     cu_new (B + 1), slot_map (max_tokens; -1 behind the last new token) and free_head_out (1).
     """
+    import torch
+
     if block_table.dim() != 2 or slot_map.dim() != 1 or free_pages.dim() != 1:
         raise ValueError("block_table must be (B, max_pages), slot_map and free_pages one-dimensional")
-    B, max_pages = block_table.shape
-    _check_ints(ctx_lens=(ctx_lens, (B,)), new_lens=(new_lens, (B,)), free_pages=(free_pages, tuple(free_pages.shape)),
-                free_head=(free_head, (1,)), block_table=(block_table, (B, max_pages)), seq_lens=(seq_lens, (B,)),
-                cu_new=(cu_new, (B + 1,)), slot_map=(slot_map, tuple(slot_map.shape)),
-                free_head_out=(free_head_out, (1,)))
+    B, max_pages = table = block_table.shape
+    tokens, free = slot_map.shape, free_pages.shape
+    i32, batch = torch.int32, (B,)
+    _check_int("ctx_lens", ctx_lens, batch, i32)
+    _check_int("new_lens", new_lens, batch, i32)
+    _check_int("free_pages", free_pages, free, i32)
+    _check_int("free_head", free_head, (1,), i32)
+    _check_int("block_table", block_table, table, i32)
+    _check_int("seq_lens", seq_lens, batch, i32)
+    _check_int("cu_new", cu_new, (B + 1,), i32)
+    _check_int("slot_map", slot_map, tokens, i32)
+    _check_int("free_head_out", free_head_out, (1,), i32)
     code = load_library().fa_page_plan(ctx_lens.data_ptr(), new_lens.data_ptr(), free_pages.data_ptr(),
                                        free_head.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(),
                                        cu_new.data_ptr(), slot_map.data_ptr(), free_head_out.data_ptr(), B, max_pages,
-                                       int(num_pages), free_pages.numel(), slot_map.numel(),
-                                       ctypes.c_void_p(_stream_handle(stream)))
+                                       int(num_pages), free[0], tokens[0], _stream_handle(stream))
     if code:
         raise FAError(code, "fa_page_plan")
 
@@ -330,14 +335,18 @@ def fa_kv_append(k_new, v_new, slot_map, k_pages, v_pages, stream=None) -> None:
 
     num_pages, Hkv, d = _check_pools(k_pages, v_pages)
     N = slot_map.shape[0] if slot_map.dim() == 1 else -1
+    _check_int("slot_map", slot_map, (N,), torch.int32)
+    shape, strides = (N, Hkv, d), []
     for name, t in (("k_new", k_new), ("v_new", v_new)):
-        if t.dtype != torch.bfloat16 or tuple(t.shape) != (N, Hkv, d) or t.stride(2) != 1 or \
-                (Hkv > 1 and t.stride(1) != d):
-            raise ValueError(f"{name} must be a bf16 (N, Hkv, d) tensor with contiguous heads, like the pages and slot_map")
-    _check_ints(slot_map=(slot_map, (N,)))
+        if t.dtype is not torch.bfloat16 or t.shape != shape:
+            raise ValueError(f"{name} must be a bf16 (N, Hkv, d) tensor, like the pages and slot_map")
+        token, head, column = t.stride()
+        if column != 1 or (Hkv > 1 and head != d):
+            raise ValueError(f"{name} must have contiguous heads")
+        strides.append(token)
     code = load_library().fa_kv_append(k_new.data_ptr(), v_new.data_ptr(), slot_map.data_ptr(), k_pages.data_ptr(),
-                                       v_pages.data_ptr(), N, Hkv, d, k_new.stride(0), v_new.stride(0), num_pages,
-                                       ctypes.c_void_p(_stream_handle(stream)))
+                                       v_pages.data_ptr(), N, Hkv, d, strides[0], strides[1], num_pages,
+                                       _stream_handle(stream))
     if code:
         raise FAError(code, "fa_kv_append")
 
@@ -359,32 +368,35 @@ def fa_fwd_prefix_paged(q, k_pages, v_pages, prefix_table, prefix_len: int, bloc
     import torch
 
     num_pages, Hkv, d = _check_pools(k_pages, v_pages)
+    rows = q.shape
     for name, t in (("q", q), ("o", o)):
-        if t.dtype != torch.bfloat16 or t.dim() != 3 or t.shape[2] != d or not t.is_contiguous():
+        if t.dtype is not torch.bfloat16 or t.dim() != 3 or t.shape[2] != d or not t.is_contiguous():
             raise ValueError(f"{name} must be a contiguous bf16 (N, H, d) tensor")
-    if o.shape != q.shape:
+    if o.shape != rows:
         raise ValueError("q and o must have the same shape")
-    N, H, _ = q.shape
-    if lse.dtype != torch.float32 or tuple(lse.shape) != (N, H) or not lse.is_contiguous():
+    N, H, _ = rows
+    if lse.dtype is not torch.float32 or lse.shape != (N, H) or not lse.is_contiguous():
         raise ValueError("lse must be a contiguous fp32 (N, H) tensor")
     if block_table.dim() != 2:
         raise ValueError("block_table must be (B, max_pages)")
-    B, max_pages = block_table.shape
-    _check_ints(block_table=(block_table, (B, max_pages)), seq_lens=(seq_lens, (B,)), cu_new=(cu_new, (B + 1,)))
+    B, max_pages = table = block_table.shape
+    i32 = torch.int32
+    _check_int("block_table", block_table, table, i32)
+    _check_int("seq_lens", seq_lens, (B,), i32)
+    _check_int("cu_new", cu_new, (B + 1,), i32)
     if prefix_table is not None:
-        _check_ints(prefix_table=(prefix_table, (prefix_table.numel(),)))
+        _check_int("prefix_table", prefix_table, (prefix_table.numel(),), i32)
     if prefix_len > 0 and (prefix_table is None or prefix_table.numel() * PAGE < prefix_len):
         raise ValueError("prefix_table must hold ceil(prefix_len / 128) pages")
     if workspace is None:
         workspace = torch.empty(max(1, fa_fwd_prefix_paged_workspace_bytes(N, B, H, Hkv, d)), dtype=torch.uint8,
                                 device=q.device)
-    nbytes = workspace.numel() * workspace.element_size()
     code = load_library().fa_fwd_prefix_paged(q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(),
                                               prefix_table.data_ptr() if prefix_len > 0 else None,
                                               block_table.data_ptr(), seq_lens.data_ptr(), cu_new.data_ptr(),
                                               o.data_ptr(), lse.data_ptr(), N, B, H, Hkv, d, int(prefix_len),
                                               int(max_new), int(bool(causal)), float(scale), num_pages, max_pages,
-                                              workspace.data_ptr(), nbytes, ctypes.c_void_p(_stream_handle(stream)))
+                                              workspace.data_ptr(), workspace.nbytes, _stream_handle(stream))
     if code:
         raise FAError(code, "fa_fwd_prefix_paged")
 

@@ -920,6 +920,7 @@ fa_status fa_fwd_prefix_paged(const void* q, const void* k_pages, const void* v_
   const long long most = static_cast<long long>(std::min(max_new, N)) * group, rows = most <= 64 ? most : group;
   p.few_rows = rows <= 8 || rows > 64 ? 8 : rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
   p.teams = p.few_rows <= 16 ? 8 : p.few_rows == 32 ? 4 : 2;
+  p.head_bytes = 2 * d;
   p.step = d == 64 ? 32 : 16;
   p.tiles_p = static_cast<int>(prefix_pages);
   p.tp = tp;

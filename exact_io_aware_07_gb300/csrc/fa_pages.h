@@ -55,6 +55,7 @@ struct PrefixParams {
   int ctas;      // blocks of the attention kernel: one per SM, at most kPrefixMaxCtas
   int teams;     // few-row teams per block: 8, 4 or 2
   int few_rows;  // rows of a few-row item at most: 8, 16 (one warp), 32 or 64
+  int head_bytes;  // of a key's row: 2 d
   int step;      // keys per few-row step: 16 (d = 128) or 32
   int tiles_p;   // 128-key tiles of the prefix
   int tp;        // tokens of a 128-row tile

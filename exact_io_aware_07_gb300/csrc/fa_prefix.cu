@@ -37,11 +37,12 @@ namespace fa {
 static __device__ unsigned int g_prefix_status;  // kStatus* bits
 
 // Places on the lines.  Many rows: an item, and a key tile of an item with up to 128 and more rows; few rows: an
-// item, and one per step.  kManyTime / kFewTime: microseconds of a place of either kind on one SM, kManyStart: what the
-// many-row kind takes longer to start and end, for sharing out the SMs.
+// item, and one per step.  For sharing out the SMs, in microseconds and bytes per microsecond, fitted to the best
+// shares of six batches (64 to 256 requests, prefixes of 1 024 to 32 768 keys): a place of either kind on one SM; what the
+// many-row kind takes longer at its ends; the part of the loading time that its work is to fill; the rate of loading.
 constexpr unsigned int kItemCost = 8, kTileCost128 = 6, kTileCost256 = 8;
 constexpr unsigned int kFewItemCost = 4, kFewLeast = 4;  // (at least kFewLeast places for a team)
-constexpr float kManyTime = 0.22f, kFewTime = 0.08f, kManyStart = 6.f;
+constexpr float kManyTime = 0.22f, kFewTime = 0.12f, kManyStart = 2.6f, kManyShare = 0.4f, kLoadRate = 6.5e6f;
 constexpr int kBigRows = 128;   // rows from which a request is big
 constexpr int kMaxFlags = 1024; // row blocks of the batch whose need of the prefix is looked at one by one
 // words of p.hdr: both lines' shares, needed row blocks, tokens
@@ -202,10 +203,14 @@ __device__ __forceinline__ Plan make_plan(const PrefixParams& p, Layout& s, vola
   l.total[1] = static_cast<unsigned int>(all >> 32);
   s.cum[tid] = before + sum - mine;
   s.first[tid] = first;
-  // m blocks for the many-row line with m so that both kinds end together: kManyStart + A / m = B / (G - m)
+  // Blocks for the many-row line.  m1 of them end it together with the few-row line, kManyStart + A / m1 = B / (G - m1);
+  // where loading all keys takes longer than that, more do no harm to the few rows until their own work takes as long,
+  // and the many-row blocks, which wait for their keys behind the others', are given time for kManyShare of the loading.
   const float a = kManyTime * l.total[0], b = kFewTime * l.total[1], g = p.ctas, d = kManyStart * g - a - b;
-  const float m = (d + sqrtf(d * d + 4.f * kManyStart * a * g)) / (2.f * kManyStart);
-  l.many = l.total[0] == 0 ? 0 : l.total[1] == 0 ? p.ctas : max(1, min(p.ctas - 1, __float2int_ru(m)));
+  float m = (d + sqrtf(d * d + 4.f * kManyStart * a * g)) / (2.f * kManyStart);
+  const float load = (l.total[1] * 8192.f + p.Hkv * p.tiles_p * 2.f * kPage * p.head_bytes) / kLoadRate;
+  m = max(m, min(a / (kManyShare * load), g - b / load));
+  l.many = l.total[0] == 0 ? 0 : l.total[1] == 0 ? p.ctas : max(1, min(p.ctas - 1, __float2int_rn(m)));
   l.share[0] = max(1u, (l.total[0] + max(l.many, 1) - 1) / max(l.many, 1));
   const unsigned int teams = max(1, (p.ctas - l.many) * p.teams);
   l.share[1] = max(kFewLeast, (l.total[1] + teams - 1) / teams);
