@@ -40,7 +40,7 @@ static __device__ unsigned int g_prefix_status;  // kStatus* bits
 // item, and one per step.  For sharing out the SMs, in microseconds and bytes per microsecond, fitted to the best
 // shares of six batches (64 to 256 requests, prefixes of 1 024 to 32 768 keys): a place of either kind on one SM; what the
 // many-row kind takes longer at its ends; the part of the loading time that its work is to fill; the rate of loading.
-constexpr unsigned int kItemCost = 8, kTileCost128 = 6, kTileCost256 = 8;
+constexpr unsigned int kItemCost = 20, kTileCost128 = 6, kTileCost256 = 8;
 constexpr unsigned int kFewItemCost = 4, kFewLeast = 4;  // (at least kFewLeast places for a team)
 constexpr float kManyTime = 0.22f, kFewTime = 0.12f, kManyStart = 2.6f, kManyShare = 0.4f, kLoadRate = 6.5e6f;
 constexpr int kBigRows = 128;   // rows from which a request is big
@@ -1407,12 +1407,32 @@ struct Parts {
   }
 };
 
-// Joins row n * H + h (W warps together, every lane D / 32 columns): t and rank are the token's.  The lanes look up 32
-// parts at a time (warp w of W every W-th), weight them by their LSE and add them eight loads at a time.
-template <int D, int W>
-__device__ __forceinline__ void join_row(const PrefixParams& p, const Plan& l, size_t orow, int4 t, int rank, int warp, int lane,
-                                         float* smem) {
-  constexpr int C = D / 32;
+// A lane's columns of a part.
+template <int C, int G>
+__device__ __forceinline__ void load_columns(const float* src, int sub, float (&v)[C]) {
+  if (C >= 4) {
+#pragma unroll
+    for (int e = 0; e < C / 4; ++e) {
+      const float4 x = __ldg(reinterpret_cast<const float4*>(src + 4 * G * e + 4 * sub));
+      v[4 * e] = x.x;
+      v[(4 * e + 1) % C] = x.y;
+      v[(4 * e + 2) % C] = x.z;
+      v[(4 * e + 3) % C] = x.w;
+    }
+  } else {
+    const float2 x = __ldg(reinterpret_cast<const float2*>(src + 2 * sub));
+    v[0] = x.x;
+    v[1 % C] = x.y;
+  }
+}
+
+// Joins row n * H + h: t and rank are the token's.  G lanes of a warp (`mask`, this one the `sub`-th) or, W > 1, W whole
+// warps together; every lane has D / G columns.  The lanes look up G parts at a time (warp w of W every W-th), weight
+// them by their LSE and add them several loads at a time.
+template <int D, int W, int G>
+__device__ __forceinline__ void join_row(const PrefixParams& p, const Plan& l, size_t orow, int4 t, int rank, int warp, int sub,
+                                         unsigned int mask, float* smem) {
+  constexpr int C = D / G;  // columns 4 G e + 4 sub .. of the e-th four, or (C < 4) C sub ..
   const int n = static_cast<int>(orow / p.H), h = static_cast<int>(orow - static_cast<size_t>(n) * p.H);
   const int g = h / p.group, hh = h - g * p.group;
   Parts pre, own;
@@ -1437,8 +1457,8 @@ __device__ __forceinline__ void join_row(const PrefixParams& p, const Plan& l, s
 #pragma unroll
   for (int c = 0; c < C; ++c) acc[c] = 0.f;
   const int parts = pre.count + own.count;
-  for (int i0 = 0; i0 < parts; i0 += 32 * W) {
-    int i = i0 + lane * W + (W > 1 ? warp : 0);
+  for (int i0 = 0; i0 < parts; i0 += G * W) {
+    const int i = i0 + sub * W + (W > 1 ? warp : 0);
     float lse2 = -INFINITY;
     const float* o = p.slab_o;
     if (i < parts) {
@@ -1457,38 +1477,28 @@ __device__ __forceinline__ void join_row(const PrefixParams& p, const Plan& l, s
     }
     float top = lse2;
 #pragma unroll
-    for (int w = 16; w; w >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, w));
+    for (int w = G / 2; w; w >>= 1) top = fmaxf(top, __shfl_xor_sync(mask, top, w, G));
     top = fmaxf(top, m);
     const float f = m == -INFINITY ? 0.f : exp2f(m - top), mine = lse2 == -INFINITY ? 0.f : exp2f(lse2 - top);
     m = top;
     float all = mine;
 #pragma unroll
-    for (int w = 16; w; w >>= 1) all += __shfl_xor_sync(0xffffffffu, all, w);
+    for (int w = G / 2; w; w >>= 1) all += __shfl_xor_sync(mask, all, w, G);
     sum = sum * f + all;
 #pragma unroll
     for (int c = 0; c < C; ++c) acc[c] *= f;
-    const int here = min(32, (parts - i0 + W - 1) / W);
-#pragma unroll 8
+    const int here = min(G, (parts - i0 + W - 1) / W);
+    // (lanes without a part have weight 0 and the address of some other: loaded all the same, so that the loads of several
+    // parts are under way together, and not added)
+#pragma unroll 8 / (C > 4 ? C / 4 : 1)
     for (int k = 0; k < here; ++k) {
-      const float w = __shfl_sync(0xffffffffu, mine, k);
-      const float* src = reinterpret_cast<const float*>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(o), k)) + lane * C;
-      // (lanes without a part have weight 0 and the address of some other: loaded all the same, so that the loads of
-      // eight parts are under way together, and not added)
-      if (C == 4) {
-        const float4 v = __ldg(reinterpret_cast<const float4*>(src));
-        if (w != 0.f) {
-          acc[0] += w * v.x;
-          acc[1] += w * v.y;
-          acc[2 % C] += w * v.z;
-          acc[3 % C] += w * v.w;
-        }
-      } else {
-        const float2 v = __ldg(reinterpret_cast<const float2*>(src));
-        if (w != 0.f) {
-          acc[0] += w * v.x;
-          acc[1] += w * v.y;
-        }
-      }
+      const float w = __shfl_sync(mask, mine, k, G);
+      const float* src = reinterpret_cast<const float*>(__shfl_sync(mask, reinterpret_cast<unsigned long long>(o), k, G));
+      float v[C];
+      load_columns<C, G>(src, sub, v);
+      if (w != 0.f)
+#pragma unroll
+        for (int c = 0; c < C; ++c) acc[c] += w * v[c];
     }
   }
   if (W > 1) {  // the warps' sums, always in the same order
@@ -1498,7 +1508,7 @@ __device__ __forceinline__ void join_row(const PrefixParams& p, const Plan& l, s
     s_m[warp] = m;
     s_sum[warp] = sum;
 #pragma unroll
-    for (int c = 0; c < C; ++c) s_acc[warp][lane * C + c] = acc[c];
+    for (int c = 0; c < C; ++c) s_acc[warp][sub * C + c] = acc[c];  // (G = 32: C <= 4)
     __syncthreads();
     float top = -INFINITY;
 #pragma unroll
@@ -1511,19 +1521,22 @@ __device__ __forceinline__ void join_row(const PrefixParams& p, const Plan& l, s
       const float f = s_m[w] == -INFINITY ? s_sum[w] : exp2f(s_m[w] - top);  // (no part: 0; a NaN sum stays one)
       sum += f * s_sum[w];
 #pragma unroll
-      for (int c = 0; c < C; ++c) acc[c] += f * s_acc[w][lane * C + c];
+      for (int c = 0; c < C; ++c) acc[c] += f * s_acc[w][sub * C + c];
     }
     m = top;
     if (warp > 0) return;
   }
   const float inv = sum == 0.f ? 0.f : 1.f / sum;
-  __nv_bfloat16* out = p.o + orow * D + lane * C;
-  if (C == 4)
-    *reinterpret_cast<uint2*>(out) =
-        make_uint2(pack_bf16x2(acc[0] * inv, acc[1] * inv), pack_bf16x2(acc[2 % C] * inv, acc[3 % C] * inv));
-  else
-    *reinterpret_cast<uint32_t*>(out) = pack_bf16x2(acc[0] * inv, acc[1] * inv);
-  if (lane == 0) p.lse[orow] = sum == 0.f ? -INFINITY : (m + log2f(sum)) * LN2;
+  __nv_bfloat16* out = p.o + orow * D;
+  if (C >= 4) {
+#pragma unroll
+    for (int e = 0; e < C / 4; ++e)
+      *reinterpret_cast<uint2*>(out + 4 * G * e + 4 * sub) =
+          make_uint2(pack_bf16x2(acc[4 * e] * inv, acc[4 * e + 1] * inv), pack_bf16x2(acc[4 * e + 2] * inv, acc[4 * e + 3] * inv));
+  } else {
+    *reinterpret_cast<uint32_t*>(out + 2 * sub) = pack_bf16x2(acc[0] * inv, acc[1 % C] * inv);
+  }
+  if (sub == 0) p.lse[orow] = sum == 0.f ? -INFINITY : (m + log2f(sum)) * LN2;
 }
 
 // Whether a row of K/V head g has to be joined: it has no, or several parts.  (A row with one item and that inside one
@@ -1537,40 +1550,30 @@ __device__ __forceinline__ bool needs_join(const Plan& l, const int4& t, int ran
   return it.worker(0, share) != it.worker(it.units - 1, share);
 }
 
-// Joins the rows that need it.  W = 8: a row per block (few rows, perhaps of many parts); W = 1: `per_warp` rows per
-// warp, its lanes first looking through them for those to join.
-template <int D, int W>
-__global__ void __launch_bounds__(256) fa_prefix_join_kernel(const __grid_constant__ PrefixParams p, int per_warp) {
+// Joins the rows that need it.  W = 8: a row per block (few rows, perhaps of many parts); else a warp or, of many rows,
+// eight lanes a row (prompt chunks: most rows have two parts, and the time is that of their loads one after another).
+constexpr int kJoinThreads = 128;
+template <int D, int W, int G>
+__global__ void __launch_bounds__(W > 1 ? 32 * W : kJoinThreads) fa_prefix_join_kernel(const __grid_constant__ PrefixParams p) {
   __shared__ float smem[W > 1 ? W * D + 2 * W : 1];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const long long first = W > 1 ? blockIdx.x : blockIdx.x + static_cast<long long>(gridDim.x) * warp;  // then every stride-th
-  const long long stride = static_cast<long long>(gridDim.x) * 8;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = lane % G;
+  const unsigned int mask = G == 32 ? 0xffffffffu : 0xffu << (lane & 24);
   pdl_launch_dependents();  // a following call's blocks may set themselves up
-  const long long all = static_cast<long long>(p.N) * p.H, row = first + stride * lane;
-  int4 t = make_int4(0, 0, 0, 0);
-  int rank = -1;
-  if (W > 1 || (lane < per_warp && row < all)) {
-    const int n = static_cast<int>((W > 1 ? first : row) / p.H);
-    t = p.tok[n];  // (past the last token: whatever, not used)
-    rank = p.rank[n];
-  }
+  const long long all = static_cast<long long>(p.N) * p.H;
+  const long long stride = W > 1 ? gridDim.x : static_cast<long long>(gridDim.x) * (kJoinThreads / G);
+  long long row = W > 1 ? blockIdx.x : static_cast<long long>(blockIdx.x) * (kJoinThreads / G) + threadIdx.x / G;
+  if (row >= all) return;
   Plan l;
   l.share[0] = p.hdr[kHdrShare];
   l.share[1] = p.hdr[kHdrShare + 1];
   l.items = p.hdr[kHdrItems];
   l.tokens = p.hdr[kHdrTokens];
   const long long rows = static_cast<long long>(l.tokens) * p.H;
-  if (W > 1) {
-    if (first < rows && needs_join(l, t, rank, static_cast<int>(first % p.H) / p.group))
-      join_row<D, W>(p, l, static_cast<size_t>(first), t, rank, warp, lane, smem);
-    return;
-  }
-  const bool need = lane < per_warp && row < rows && needs_join(l, t, rank, static_cast<int>(row % p.H) / p.group);
-  for (unsigned int todo = __ballot_sync(0xffffffffu, need); todo; todo &= todo - 1) {
-    const int k = __ffs(todo) - 1;
-    const int4 tk = make_int4(__shfl_sync(0xffffffffu, t.x, k), __shfl_sync(0xffffffffu, t.y, k),
-                              __shfl_sync(0xffffffffu, t.z, k), __shfl_sync(0xffffffffu, t.w, k));
-    join_row<D, 1>(p, l, static_cast<size_t>(first + stride * k), tk, __shfl_sync(0xffffffffu, rank, k), warp, lane, smem);
+  for (; row < all; row += stride) {
+    const int n = static_cast<int>(row / p.H), g = static_cast<int>(row - static_cast<long long>(n) * p.H) / p.group;
+    const int4 t = __ldg(p.tok + n);  // (past the last token: whatever, not used)
+    const int rank = __ldg(p.rank + n);
+    if (row < rows && needs_join(l, t, rank, g)) join_row<D, W, G>(p, l, static_cast<size_t>(row), t, rank, warp, sub, mask, smem);
   }
 }
 
@@ -1598,16 +1601,19 @@ static cudaError_t launch(const PrefixMaps& t, const PrefixParams& p, cudaStream
   if ((e = cudaLaunchKernelEx(&cfg, fa_prefix_kernel<D, NT, R>, t.q, t.k, t.v, t.k16, t.v16, p)) != cudaSuccess) return e;
   const long long rows = static_cast<long long>(p.N) * p.H;
   const bool wide = rows < 4 * p.ctas;
-  long long per_warp = (rows + 48 * p.ctas - 1) / (48 * p.ctas);  // about as many warps as the SMs hold
-  per_warp = per_warp > 32 ? 32 : per_warp;
+  // a warp a row while the SMs hold as many (8 lanes a row: 44 -> 48 us for 64 requests behind 16 384 keys); eight lanes
+  // beyond (160 -> 140 us for a batch of prompt chunks with 77 568 rows), 12 blocks per SM at most
+  const int lanes = rows <= 48ll * p.ctas ? 32 : 8;
+  const long long blocks = (rows * lanes + kJoinThreads - 1) / kJoinThreads;
   // not launched early: its blocks would gather on the SMs whose attention block ends first (46 -> 63 us for 64
   // requests behind 16 384 keys)
   cfg.numAttrs = 0;
-  cfg.gridDim = dim3(static_cast<unsigned int>(wide ? rows : (rows + 8 * per_warp - 1) / (8 * per_warp)));
-  cfg.blockDim = dim3(256);
+  cfg.gridDim = dim3(static_cast<unsigned int>(wide ? rows : blocks < 12 * p.ctas ? blocks : 12 * p.ctas));
+  cfg.blockDim = dim3(wide ? 256 : kJoinThreads);
   cfg.dynamicSmemBytes = 0;
-  return wide ? cudaLaunchKernelEx(&cfg, fa_prefix_join_kernel<D, 8>, p, 1)
-              : cudaLaunchKernelEx(&cfg, fa_prefix_join_kernel<D, 1>, p, static_cast<int>(per_warp));
+  return wide          ? cudaLaunchKernelEx(&cfg, fa_prefix_join_kernel<D, 8, 32>, p)
+         : lanes == 32 ? cudaLaunchKernelEx(&cfg, fa_prefix_join_kernel<D, 1, 32>, p)
+                       : cudaLaunchKernelEx(&cfg, fa_prefix_join_kernel<D, 1, 8>, p);
 }
 
 cudaError_t launch_fa_fwd_prefix(int d, const PrefixMaps& t, const PrefixParams& p, cudaStream_t stream) {
