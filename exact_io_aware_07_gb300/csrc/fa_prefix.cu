@@ -212,6 +212,13 @@ __device__ __forceinline__ Plan make_plan(const PrefixParams& p, Layout& s, vola
   m = max(m, min(a / (kManyShare * load), g - b / load));
   l.many = l.total[0] == 0 ? 0 : l.total[1] == 0 ? p.ctas : max(1, min(p.ctas - 1, __float2int_rn(m)));
   l.share[0] = max(1u, (l.total[0] + max(l.many, 1) - 1) / max(l.many, 1));
+  // Only the prefix on the many-row line: every item in the same whole number of stretches, so that the row blocks of a
+  // head come to a key tile at the same time and all but the first read it from L2.
+  const int items = p.Hkv * l.items, each = items == 0 ? 0 : (2 * l.many + items) / (2 * items);
+  if (l.total[0] > 0 && l.total[0] == l.lead[0] && each > 0 && each * items <= p.ctas - (l.total[1] > 0)) {
+    l.many = each * items;
+    l.share[0] = (l.total[0] / items + each - 1) / each;
+  }
   const unsigned int teams = max(1, (p.ctas - l.many) * p.teams);
   l.share[1] = max(kFewLeast, (l.total[1] + teams - 1) / teams);
   __syncthreads();
@@ -351,18 +358,23 @@ __device__ __forceinline__ void load_rows_elect(uint32_t dst, const void* tmap, 
       " [%0], [%1, {0, %2, 0, %3}], [%4];\n\t}"
       :: "r"(dst), "l"(reinterpret_cast<uint64_t>(tmap)), "r"(row), "r"(plane), "r"(bar), "r"(bytes) : "memory");
 }
-// The same rows of two pools, to dst and dst + half.
+// The same rows of two pools, to dst and dst + half, with an L2 cache policy.
 __device__ __forceinline__ void load_rows2_elect(uint32_t dst, uint32_t half, const void* tmap0, const void* tmap1, int row,
-                                                 int plane, uint32_t bar) {
+                                                 int plane, uint32_t bar, uint64_t policy) {
   asm volatile(
       "{\n\t.reg .pred e;\n\t.reg .b64 st;\n\telect.sync _|e, 0xffffffff;\n\t"
       "@e mbarrier.arrive.expect_tx.shared::cta.b64 st, [%6], %7;\n\t"
-      "@e cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes"
-      " [%0], [%2, {0, %4, 0, %5}], [%6];\n\t"
-      "@e cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes"
-      " [%1], [%3, {0, %4, 0, %5}], [%6];\n\t}"
+      "@e cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint"
+      " [%0], [%2, {0, %4, 0, %5}], [%6], %8;\n\t"
+      "@e cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint"
+      " [%1], [%3, {0, %4, 0, %5}], [%6], %8;\n\t}"
       :: "r"(dst), "r"(dst + half), "l"(reinterpret_cast<uint64_t>(tmap0)), "l"(reinterpret_cast<uint64_t>(tmap1)),
-         "r"(row), "r"(plane), "r"(bar), "r"(2 * half) : "memory");
+         "r"(row), "r"(plane), "r"(bar), "r"(2 * half), "l"(policy) : "memory");
+}
+__device__ __forceinline__ uint64_t l2_policy_evict_normal() {
+  uint64_t pol;
+  asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(pol));
+  return pol;
 }
 
 // Many rows.  Roles: warps 0-3 and 4-7 the softmax of slot 0 and slot 1 (a thread has one of 128 rows),
@@ -1102,6 +1114,8 @@ __device__ __forceinline__ void few_rows(const CUtensorMap& tmK, const CUtensorM
     lp.j1 = 0;
     look_ahead();
   }
+  // own keys are read once: in L2 they go before the prefix, the parts and the kernels' code
+  const uint64_t once = l2_policy_evict_first(), keep = l2_policy_evict_normal();
   auto fill = [&]() -> bool {  // loads the stretch's next step, if there is one
     if (lj >= lp.j1) {
       if (!any) {
@@ -1128,7 +1142,7 @@ __device__ __forceinline__ void few_rows(const CUtensorMap& tmK, const CUtensorM
         !wait_all(W, bar_empty + 8 * lstage, (issued / L::STAGES - 1) & 1))
       return false;
     load_rows2_elect(ring + lstage * L::STEP_BYTES, L::STEP_BYTES / 2, &tmK, &tmV, (lj % (kPage / L::STEP)) * L::STEP,
-                     pg * p.Hkv + lp.g, bar_full + 8 * lstage);
+                     pg * p.Hkv + lp.g, bar_full + 8 * lstage, lp.table == p.prefix_table ? keep : once);
     ++lj;
     ++issued;
     if (++lstage == L::STAGES) lstage = 0;
