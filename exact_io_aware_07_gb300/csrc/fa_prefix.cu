@@ -42,7 +42,7 @@ static __device__ unsigned int g_prefix_status;  // kStatus* bits
 // many-row kind takes longer at its ends; the part of the loading time that its work is to fill; the rate of loading.
 constexpr unsigned int kItemCost = 20, kTileCost128 = 6, kTileCost256 = 8;
 constexpr unsigned int kFewItemCost = 4, kFewLeast = 4;  // (at least kFewLeast places for a team)
-constexpr float kManyTime = 0.22f, kFewTime = 0.12f, kManyStart = 2.6f, kManyShare = 0.4f, kLoadRate = 6.5e6f;
+constexpr float kManyTime = 0.19f, kFewTime = 0.12f, kManyStart = 2.6f, kManyShare = 0.4f, kLoadRate = 6.5e6f;
 constexpr int kBigRows = 128;   // rows from which a request is big
 constexpr int kMaxFlags = 1024; // row blocks of the batch whose need of the prefix is looked at one by one
 // words of p.hdr: both lines' shares, needed row blocks, tokens
@@ -1602,19 +1602,22 @@ static cudaError_t launch(const PrefixMaps& t, const PrefixParams& p, cudaStream
     if (e != cudaSuccess) return e;
     attr_set[dev] = true;
   }
+  const long long rows = static_cast<long long>(p.N) * p.H;
+  const bool wide = rows < 4 * p.ctas;  // few rows: the join takes a block for each
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.stream = stream;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  // Launched early only when there are few rows (14.0 against 14.8 us for one request).  Blocks that start as the
+  // preceding kernel's end land on the SMs in any order, and the last block numbers, which stream the requests' own keys,
+  // gather on neighbouring SMs and starve the others there (87 -> 103 us for 128 requests behind 4 096 keys).
+  cfg.numAttrs = wide ? 1 : 0;
   cfg.gridDim = dim3(p.ctas);
   cfg.blockDim = dim3(THREADS);
   cfg.dynamicSmemBytes = SMEM_BYTES;
   if ((e = cudaLaunchKernelEx(&cfg, fa_prefix_kernel<D, NT, R>, t.q, t.k, t.v, t.k16, t.v16, p)) != cudaSuccess) return e;
-  const long long rows = static_cast<long long>(p.N) * p.H;
-  const bool wide = rows < 4 * p.ctas;
   // a warp a row while the SMs hold as many (8 lanes a row: 44 -> 48 us for 64 requests behind 16 384 keys); eight lanes
   // beyond (160 -> 140 us for a batch of prompt chunks with 77 568 rows), 12 blocks per SM at most
   const int lanes = rows <= 48ll * p.ctas ? 32 : 8;
