@@ -29,6 +29,7 @@ outputs (and workspaces) with PyTorch.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import math
 import os
@@ -156,6 +157,16 @@ def _stream_handle(stream):
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
+
+
+def _on_stream(stream):
+    """Context in which PyTorch allocates and fills tensors on ``stream`` (an int handle or a Stream; None: the current
+    one), so that a kernel there finds them in order and their memory is reused in order."""
+    import torch
+
+    if stream is None:
+        return contextlib.nullcontext()
+    return torch.cuda.stream(torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream)
 
 
 def fa_device_status(stream=None) -> int:
@@ -322,8 +333,9 @@ def page_plan(ctx_lens, new_lens, free_pages, free_head, block_table, max_tokens
     import torch
 
     B = ctx_lens.shape[0]
-    seq, cu, slots, head = (torch.empty(n, dtype=torch.int32, device=ctx_lens.device)
-                            for n in (B, B + 1, max_tokens, 1))
+    with _on_stream(stream):
+        seq, cu, slots, head = (torch.empty(n, dtype=torch.int32, device=ctx_lens.device)
+                                for n in (B, B + 1, max_tokens, 1))
     fa_page_plan(ctx_lens, new_lens, free_pages, free_head, block_table, seq, cu, slots, head, num_pages, stream)
     return seq, cu, slots, head
 
@@ -389,8 +401,11 @@ def fa_fwd_prefix_paged(q, k_pages, v_pages, prefix_table, prefix_len: int, bloc
     if prefix_len > 0 and (prefix_table is None or prefix_table.numel() * PAGE < prefix_len):
         raise ValueError("prefix_table must hold ceil(prefix_len / 128) pages")
     if workspace is None:
-        workspace = torch.empty(max(1, fa_fwd_prefix_paged_workspace_bytes(N, B, H, Hkv, d)), dtype=torch.uint8,
-                                device=q.device)
+        with _on_stream(stream):
+            workspace = torch.empty(max(1, fa_fwd_prefix_paged_workspace_bytes(N, B, H, Hkv, d)), dtype=torch.uint8,
+                                    device=q.device)
+    elif not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
     code = load_library().fa_fwd_prefix_paged(q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(),
                                               prefix_table.data_ptr() if prefix_len > 0 else None,
                                               block_table.data_ptr(), seq_lens.data_ptr(), cu_new.data_ptr(),
@@ -410,8 +425,9 @@ def attention_prefix_paged(q, k_pages, v_pages, prefix_table, prefix_len: int, b
     N, H, d = q.shape
     if scale is None:
         scale = 1.0 / math.sqrt(d)
-    o = torch.zeros_like(q)
-    lse = torch.full((N, H), float("-inf"), dtype=torch.float32, device=q.device)
+    with _on_stream(stream):
+        o = torch.zeros_like(q)
+        lse = torch.full((N, H), float("-inf"), dtype=torch.float32, device=q.device)
     fa_fwd_prefix_paged(q, k_pages, v_pages, prefix_table, prefix_len, block_table, seq_lens, cu_new, max_new, o, lse,
                         causal, scale, None, stream)
     return o, lse

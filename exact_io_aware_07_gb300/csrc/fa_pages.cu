@@ -100,7 +100,9 @@ __global__ void __launch_bounds__(kPlanThreads) fa_page_plan_kernel(const PlanPa
       const int r = last_not_above(s_page, count, f);
       p.block_table[static_cast<size_t>(b0 + r) * p.max_pages + pages_of(s_ctx[r]) + (f - s_page[r])] = fresh_page(f);
     }
-    for (int t = tok0 + me; t < tok1 && t < p.max_tokens; t += stride) {
+    const int stop = min(tok1, p.max_tokens);
+    for (unsigned int at = static_cast<unsigned int>(tok0) + me; at < static_cast<unsigned int>(stop); at += stride) {
+      const int t = static_cast<int>(at);
       const int r = last_not_above(s_tok, count, t);
       const int pos = s_ctx[r] + (t - s_tok[r]), lp = pos >> 7, held = pages_of(s_ctx[r]);
       int pg;

@@ -65,8 +65,8 @@ struct Item {
     const unsigned int j = (x - c0 - lead + unit - 1) / unit;
     return j < static_cast<unsigned int>(units) ? static_cast<int>(j) : units;
   }
-  __device__ __forceinline__ int worker(int unit_index, unsigned int share) const {
-    return static_cast<int>((c0 + lead + unit * unit_index) / share);
+  __device__ __forceinline__ unsigned int worker(int unit_index, unsigned int share) const {
+    return (c0 + lead + unit * unit_index) / share;
   }
 };
 __device__ __forceinline__ Item many_item(unsigned int c0, int tiles, int rows) {
@@ -460,16 +460,17 @@ __device__ __forceinline__ void many_rows(const CUtensorMap& tmQ, const CUtensor
     int stage = 0, np = 0;
     uint32_t phase = 0, issued = 0, issued_parity = 0;
     bool ok = true;
-    // page numbers of 32 tiles of one table row, one per lane
+    // page numbers of 32 tiles of one table row, one per lane (the row of a request may also be the prefix's)
     const int* held_table = nullptr;
-    int held_base = -1, held_page = 0;
+    int held_base = -1, held_limit = 0, held_page = 0;
     auto kv_load = [&](const CUtensorMap* map, const int* own_table, int j, int ptiles, int g) -> bool {
-      const int* table = j < ptiles ? p.prefix_table : own_table;
-      const int tile = j < ptiles ? j : j - ptiles;
-      if (table != held_table || (tile & ~31) != held_base) {
+      const bool of_prefix = j < ptiles;
+      const int* table = of_prefix ? p.prefix_table : own_table;
+      const int tile = of_prefix ? j : j - ptiles, limit = of_prefix ? p.tiles_p : p.max_pages;
+      if (table != held_table || (tile & ~31) != held_base || limit != held_limit) {
         held_table = table;
         held_base = tile & ~31;
-        const int limit = table == p.prefix_table ? p.tiles_p : p.max_pages;
+        held_limit = limit;
         held_page = held_base + lane < limit ? table[held_base + lane] : 0;
       }
       int pg = __shfl_sync(0xffffffffu, held_page, tile & 31);
@@ -1409,9 +1410,13 @@ struct Parts {
   Item it;
   bool few;
   int first, count, seen, at;  // first worker, workers; units visible to the row; the row's number within the item
-  __device__ __forceinline__ void locate(unsigned int share) {
-    first = it.worker(0, share);
-    count = it.worker(it.units - 1, share) - first + 1;
+  __device__ __forceinline__ void locate(const PrefixParams& p, const Plan& l) {
+    const unsigned int share = few ? l.share[1] : l.share[0];
+    // (places past the last worker come only of a cu_new that decreases, which is reported)
+    const unsigned int last = (few ? p.ctas * p.teams : p.ctas) - 1;
+    const unsigned int w0 = min(it.worker(0, share), last), w1 = min(it.worker(it.units - 1, share), last);
+    first = static_cast<int>(w0);
+    count = w1 < w0 ? 1 : static_cast<int>(w1 - w0) + 1;
   }
   // Row of the slabs that worker `first + i` wrote the part to; -1 if it had none of the row's units.
   __device__ __forceinline__ long long slab_row(const PrefixParams& p, unsigned int share, int i) const {
@@ -1456,7 +1461,7 @@ __device__ __forceinline__ void join_row(const PrefixParams& p, const Plan& l, s
     pre.it = prefix_item(p, l.tokens, g * l.items + rank);
     pre.seen = INT_MAX;
     pre.at = (pre.few ? n : n % (2 * p.tp)) * p.group + hh;
-    pre.locate(pre.few ? l.share[1] : l.share[0]);
+    pre.locate(p, l);
   }
   if (t.z > 0) {
     own.few = t.w & kTokFew;
@@ -1465,7 +1470,7 @@ __device__ __forceinline__ void join_row(const PrefixParams& p, const Plan& l, s
     own.it.c0 += g * own.it.cost();
     own.seen = t.z;
     own.at = (t.w & (kTokFew - 1)) * p.group + hh;
-    own.locate(own.few ? l.share[1] : l.share[0]);
+    own.locate(p, l);
   }
   float m = -INFINITY, sum = 0.f, acc[C];
 #pragma unroll
@@ -1612,7 +1617,7 @@ static cudaError_t launch(const PrefixMaps& t, const PrefixParams& p, cudaStream
   cfg.attrs = attr;
   // Launched early only when there are few rows (14.0 against 14.8 us for one request).  Blocks that start as the
   // preceding kernel's end land on the SMs in any order, and the last block numbers, which stream the requests' own keys,
-  // gather on neighbouring SMs and starve the others there (87 -> 103 us for 128 requests behind 4 096 keys).
+  // gather on neighbouring SMs and starve the others there (86 -> 103 us for 128 requests behind 32 768 keys).
   cfg.numAttrs = wide ? 1 : 0;
   cfg.gridDim = dim3(p.ctas);
   cfg.blockDim = dim3(THREADS);

@@ -388,6 +388,155 @@ def test_on_another_stream_and_in_graphs_that_share_a_workspace():
     assert fa.fa_device_status() == 0
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("tokens", [2, 3, 4, 7, 8, 15, 16, 17, 31])
+@pytest.mark.parametrize("prefix", [0, 333])
+def test_rows_per_request(d, tokens, prefix):
+    """4 to 124 rows a request and K/V head: every size of the few-row teams, and requests that fill part of a row tile;
+    beside them requests of fewer rows."""
+    own = [tokens, 1500, tokens + 130, 1 + tokens // 2, 257]
+    b = Batch(d, 8, 2, prefix, own, [tokens, tokens, tokens, 1 + tokens // 2, 1], pad=1, seed=30)
+    b.check(*b.run(), label=f"{4 * tokens} rows P{prefix} d{d}")
+
+
+@pytest.mark.parametrize("d,H,Hkv,tokens", [(64, 2, 2, 1), (128, 4, 1, 1), (128, 8, 1, 2), (64, 32, 1, 1), (128, 16, 1, 4)])
+def test_few_rows_in_all(d, H, Hkv, tokens):
+    """One request, whose rows work the prefix as few rows too: long and short, alone or with own keys."""
+    for prefix, own in ((4000, tokens), (1, 3000), (129, 0), (2049, 515)):
+        b = Batch(d, H, Hkv, prefix, [own], [tokens], seed=31)
+        b.check(*b.run(), label=f"one request P{prefix} own{own}")
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("prefix", [0, 400])
+def test_every_kind_of_request_in_one_batch(d, prefix):
+    """Decoding, drafted, middling and big requests in turn, so that row blocks hold rows of several kinds."""
+    new = [1, 200, 5, 20, 1, 0, 64, 33, 2, 1, 130]
+    own = [900, 200, 77, 520, 1, 300, 700, 33, 129, 256, 1]
+    b = Batch(d, 8, 2, prefix, own, new, pad=3, seed=32)
+    for causal in (True, False):
+        b.check(*b.run(causal), causal, label=f"kinds P{prefix} d{d} causal{int(causal)}")
+
+
+def test_more_row_blocks_than_are_flagged():
+    """2 065 tokens of 128 rows each, two tokens a row block: 1 033 blocks.  Three heads of every token are compared."""
+    new = [1] * 400 + [0] + [1] * 1465 + [200]
+    own = [i % 3 for i in range(len(new) - 1)] + [260]
+    b = Batch(64, 128, 1, 130, own, new, pad=1, seed=33)
+    o, lse = b.run()
+    heads = [0, 77, 127]
+    b.q = np.ascontiguousarray(b.q[:, heads])
+    b.check(o[:, heads], lse[:, heads], label="row blocks")
+
+
+def test_the_prefix_may_be_a_request_of_the_batch():
+    """The prefix's table is the first entries of a request's own row: big, middling and decoding rows read both."""
+    for new in ([150, 1], [20, 1], [1, 1]):
+        b = Batch(64, 8, 2, 0, [700, 40], new, seed=34)
+        b.prefix, b.prefix_table = 200, b.table[0, :2].copy()
+        a = b.device()
+        a["prefix_table"] = a["block_table"][0, :2]
+        b.check(*b.run(prefix_table=a["prefix_table"], block_table=a["block_table"]), label=f"own prefix {new}")
+
+
+@pytest.mark.parametrize("requests", [1, 40])
+def test_calls_one_behind_the_other(requests):
+    """Each call's O is the next call's query, in one workspace: a call starts only when the one before it is through."""
+    import torch
+
+    import exact_io_aware_07_gb300 as fa
+
+    d = 128
+    b = Batch(d, 8, 2, 300, [(37 * i) % 200 + 1 for i in range(requests)], [1] * requests, seed=35)
+    a = b.device()
+    n = a["q"].shape[0]
+    ws = torch.empty(fa.fa_fwd_prefix_paged_workspace_bytes(n, requests, 8, 2, d), dtype=torch.uint8, device="cuda")
+    qs = [a.pop("q")] + [torch.full_like(a["o"], 7.0) for _ in range(6)]
+    lses = [torch.full_like(a["lse"], 7.0) for _ in range(6)]
+    a.pop("o"), a.pop("lse")
+
+    def chain():
+        for i in range(6):
+            fa.fa_fwd_prefix_paged(q=qs[i], o=qs[i + 1], lse=lses[i], causal=True, scale=1.0, workspace=ws, **a)
+
+    chain()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        chain()
+    for replay in (False, True):
+        if replay:
+            for x in qs[1:]:
+                x.fill_(7.0)
+            graph.replay()
+        torch.cuda.synchronize()
+        for i in range(6):
+            b.q = qs[i].view(torch.int16).cpu().numpy().view(np.uint16)
+            b.check(qs[i + 1], lses[i], scale=1.0, label=f"call {i} replay{int(replay)}")
+    assert fa.fa_device_status() == 0
+
+
+def test_two_calls_at_once():
+    """Two streams, each with a workspace of its own."""
+    import torch
+
+    import exact_io_aware_07_gb300 as fa
+
+    pair = [Batch(d, 8, 2, 700, [900, 33, 260, 1] * 6, [1, 3, 40, 1] * 6, seed=36) for d in (64, 128)]
+    args = [x.device() for x in pair]
+    ws = [torch.empty(fa.fa_fwd_prefix_paged_workspace_bytes(a["q"].shape[0], 24, 8, 2, x.d), dtype=torch.uint8,
+                      device="cuda") for x, a in zip(pair, args)]
+    streams = [torch.cuda.Stream() for _ in pair]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for x, a, w, s in zip(pair, args, ws, streams):
+            fa.fa_fwd_prefix_paged(**a, causal=True, scale=x.d ** -0.5, workspace=w, stream=s)
+    torch.cuda.synchronize()
+    assert fa.fa_device_status() == 0
+    for x, a in zip(pair, args):
+        x.check(a["o"], a["lse"], label=f"d{x.d} beside another")
+
+
+def test_wrappers_on_a_given_stream():
+    """The convenience calls allocate, fill and run on the stream they are given, while the current stream is busy."""
+    import torch
+
+    import exact_io_aware_07_gb300 as fa
+
+    b = Batch(128, 8, 2, 500, [300, 40, 129], [1, 2, 1], pad=2, seed=37)
+    a = b.device()
+    a.pop("o"), a.pop("lse")
+    i = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    plan = (i([126, 0]), i([3, 1]), i([5, 4, 9]), i([0]), i([[8, -1], [-1, -1]]))
+    side = torch.cuda.Stream()
+    big = torch.randn(8192, 8192, device="cuda")
+    torch.cuda.synchronize()
+    for stream in (side, side.cuda_stream):
+        for _ in range(4):
+            big @ big  # work on the current stream that the side stream's calls neither wait for nor follow
+        o, lse = fa.attention_prefix_paged(**a, stream=stream)
+        seq, cu, slots, head = fa.page_plan(*plan, 5, 10, stream=stream)
+        junk = [torch.full_like(o, 9.0) for _ in range(4)]  # takes any memory given back too early
+        side.synchronize()
+        assert (o[4:] == 0).all() and torch.isneginf(lse[4:]).all()
+        o[4:], lse[4:] = 7.0, 7.0
+        b.check(o, lse, label="wrapper on a stream")
+        assert seq.tolist() == [129, 1] and cu.tolist() == [0, 3, 4] and head.tolist() == [2]
+        assert slots.tolist() == [8 * 128 + 126, 8 * 128 + 127, 5 * 128, 4 * 128, -1]
+        del junk
+    torch.cuda.synchronize()
+    assert fa.fa_device_status() == 0
+
+
+def test_decreasing_cu_new_is_reported():
+    import exact_io_aware_07_gb300 as fa
+
+    b = Batch(64, 4, 1, 130, [20, 30, 300], [2, 1, 140], seed=38)
+    a = b.device()
+    a["cu_new"][1], a["cu_new"][2] = 3, 1
+    fa.fa_fwd_prefix_paged(**a, causal=True, scale=0.125)
+    assert fa.fa_device_status() == 15 and fa.fa_device_status() == 0
+
+
 # ---------------------------------------------------------------- plan
 
 def _plan_inputs(ctx, new, seed, slack=3, head=2, extra_cols=1):

@@ -117,7 +117,8 @@ def test_binding_refuses_wrong_tensors(lib):
            dict(prefix_table=None), dict(block_table=torch.zeros(3, dtype=torch.int32)),
            dict(block_table=torch.zeros(3, 2, dtype=torch.int32).t()), dict(seq_lens=torch.ones(3, dtype=torch.int32)),
            dict(cu_new=torch.zeros(2, dtype=torch.int32)), dict(lse=torch.zeros(4, 3)),
-           dict(o=torch.zeros(3, 4, 128, dtype=torch.bfloat16))]
+           dict(o=torch.zeros(3, 4, 128, dtype=torch.bfloat16)),
+           dict(workspace=torch.zeros(1, dtype=torch.uint8).expand(2 ** 30))]
     for kw in bad:
         with pytest.raises(ValueError):
             fa.fa_fwd_prefix_paged(**_tensors(**kw))
