@@ -106,6 +106,7 @@ __device__ __forceinline__ unsigned int request_cost(const PrefixParams& p, cons
   if (r.added == 0) return 0u;
   if (is_few(p, r)) return few_item(p, 0, visible(p, r, r.added)).cost() * p.Hkv;
   unsigned int sum = 0;
+#pragma unroll 1
   for (int blk = 0; blk * 2 * p.tp < r.added; ++blk) sum += block_item(p, r, blk, 0).cost();
   return sum * p.Hkv;
 }
@@ -134,16 +135,19 @@ struct Begin {  // what a worker begins with
 struct Plan {
   unsigned int total[2], share[2], lead[2];  // lead: the prefix's places
   int many, tokens, blocks, items;           // blocks that work many rows; new tokens; row blocks; needed ones
+  int few, worker;                           // whether this block works few rows; its number among the blocks of its kind
 };
 
 __device__ __forceinline__ bool flagged(const PrefixParams& p, int blocks) { return blocks <= kMaxFlags; }
 // The needed block with `rank` needed ones before it.
 __device__ __forceinline__ int needed_block(const PrefixParams& p, const volatile unsigned int* need, int blocks, int rank) {
   if (!flagged(p, blocks)) return rank;
+#pragma unroll 1
   for (int w = 0; w < kMaxFlags / 32; ++w) {
     unsigned int bits = need[w];
     const int n = __popc(bits);
     if (rank < n) {
+#pragma unroll 1
       for (; rank; --rank) bits &= bits - 1;
       return w * 32 + __ffs(bits) - 1;
     }
@@ -163,6 +167,7 @@ __device__ __forceinline__ Plan make_plan(const PrefixParams& p, Layout& s, vola
   bool bad = end > p.N || end < 0;
   unsigned long long mine = 0;
   int first = p.N;
+#pragma unroll 1
   for (int b = b_lo; b < b_hi; ++b) {
     const int c0 = p.cu_new[b], c1 = p.cu_new[b + 1], seq = p.seq_lens[b];
     bad |= c1 < c0 || seq < 0 || seq > p.max_pages * kPage || (b == 0 && c0 != 0);
@@ -170,6 +175,7 @@ __device__ __forceinline__ Plan make_plan(const PrefixParams& p, Layout& s, vola
     if (b == b_lo) first = r.first;
     mine += static_cast<unsigned long long>(request_cost(p, r)) << (is_few(p, r) ? 32 : 0);
     if (r.added > 0 && !is_big(p, r) && flagged(p, l.blocks))
+#pragma unroll 1
       for (int k = r.first / (2 * p.tp); k <= (r.first + r.added - 1) / (2 * p.tp) && k < l.blocks; ++k)
         atomicOr(const_cast<unsigned int*>(need) + k / 32, 1u << (k % 32));
   }
@@ -186,6 +192,7 @@ __device__ __forceinline__ Plan make_plan(const PrefixParams& p, Layout& s, vola
     l.items = 1;
   else if (flagged(p, l.blocks)) {
     l.items = 0;
+#pragma unroll 1
     for (int w = 0; w * 32 < l.blocks; ++w) l.items += __popc(need[w]);
   }
   if (l.tokens == 0) l.items = 0;
@@ -225,6 +232,7 @@ __device__ __forceinline__ Plan make_plan(const PrefixParams& p, Layout& s, vola
   // the last thread with requests whose key is not above x
   auto owner = [&](auto key, unsigned int x) {
     int lo = 0, hi = (p.B + run - 1) / run;
+#pragma unroll 1
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
       if (key(mid) <= x)
@@ -235,15 +243,18 @@ __device__ __forceinline__ Plan make_plan(const PrefixParams& p, Layout& s, vola
     return lo;
   };
   auto request = [&](int b) { return make_request(p, p.cu_new[b], p.cu_new[b + 1], p.seq_lens[b]); };
-  const int kind = static_cast<int>(blockIdx.x) >= l.many;
+  l.few = static_cast<int>(blockIdx.x) >= l.many;
+  l.worker = l.few ? blockIdx.x - l.many : blockIdx.x;
+  const int kind = l.few;
   if (tid < (kind ? p.teams : 1)) {  // the request that holds this block's worker's first own place
     const unsigned long long at =
-        static_cast<unsigned long long>(kind ? (blockIdx.x - l.many) * p.teams + tid : blockIdx.x) * l.share[kind];
+        static_cast<unsigned long long>(kind ? l.worker * p.teams + tid : l.worker) * l.share[kind];
     if (at < l.total[kind]) {
       const unsigned int x = max(static_cast<unsigned int>(at), l.lead[kind]);
       auto place = [&](int t) { return static_cast<unsigned int>(s.cum[t] >> (32 * kind)); };
       const int t = owner(place, x);
       Begin w{t * run, place(t)};
+#pragma unroll 1
       for (const int last = min(p.B, (t + 1) * run) - 1; w.b < last; ++w.b) {
         const Request r = request(w.b);
         const unsigned int c = is_few(p, r) == static_cast<bool>(kind) ? request_cost(p, r) : 0u;
@@ -253,11 +264,13 @@ __device__ __forceinline__ Plan make_plan(const PrefixParams& p, Layout& s, vola
       begin[tid] = w;
     }
   }
+#pragma unroll 1
   for (int n = blockIdx.x + gridDim.x * tid; n < l.tokens; n += gridDim.x * THREADS) {
     const int t = owner([&](int k) { return static_cast<unsigned int>(s.first[k]); }, n);
     unsigned int c0[2] = {static_cast<unsigned int>(s.cum[t]), static_cast<unsigned int>(s.cum[t] >> 32)};
     int b = t * run;
     Request r = request(b);
+#pragma unroll 1
     for (const int last = min(p.B, (t + 1) * run) - 1; b < last; ++b) {
       const Request next = request(b + 1);
       if (next.first > n) break;
@@ -274,6 +287,7 @@ __device__ __forceinline__ Plan make_plan(const PrefixParams& p, Layout& s, vola
       } else {
         const int blk = i / (2 * p.tp);
         unsigned int c = c0[0];
+#pragma unroll 1
         for (int k = 0; k < blk; ++k) c += p.Hkv * block_item(p, r, k, 0).cost();
         const Item it = block_item(p, r, blk, c);
         tok = make_int4(static_cast<int>(c), it.units,
@@ -285,6 +299,7 @@ __device__ __forceinline__ Plan make_plan(const PrefixParams& p, Layout& s, vola
         if (!few && flagged(p, l.blocks)) {
           const int blk = rank;
           rank = __popc(need[blk / 32] & ((1u << (blk % 32)) - 1));
+#pragma unroll 1
           for (int w = 0; w < blk / 32; ++w) rank += __popc(need[w]);
         }
       }
@@ -350,13 +365,14 @@ __device__ __forceinline__ int uni(int x) { return __shfl_sync(0xffffffffu, x, 0
 // ---------------------------------------------------------------- many rows
 // One lane loads a box of a page pool ((64, 128 rows, d / 64, planes) view: the 64-column halves of the box's rows one
 // behind the other) and adds its bytes to what `bar` expects.
-__device__ __forceinline__ void load_rows_elect(uint32_t dst, const void* tmap, int row, int plane, uint32_t bar, uint32_t bytes) {
+__device__ __forceinline__ void load_rows_elect(uint32_t dst, const void* tmap, int row, int plane, uint32_t bar, uint32_t bytes,
+                                                uint64_t policy) {
   asm volatile(
       "{\n\t.reg .pred e;\n\t.reg .b64 st;\n\telect.sync _|e, 0xffffffff;\n\t"
       "@e mbarrier.arrive.expect_tx.shared::cta.b64 st, [%4], %5;\n\t"
-      "@e cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {0, %2, 0, %3}], [%4];\n\t}"
-      :: "r"(dst), "l"(reinterpret_cast<uint64_t>(tmap)), "r"(row), "r"(plane), "r"(bar), "r"(bytes) : "memory");
+      "@e cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint"
+      " [%0], [%1, {0, %2, 0, %3}], [%4], %6;\n\t}"
+      :: "r"(dst), "l"(reinterpret_cast<uint64_t>(tmap)), "r"(row), "r"(plane), "r"(bar), "r"(bytes), "l"(policy) : "memory");
 }
 // The same rows of two pools, to dst and dst + half, with an L2 cache policy.
 __device__ __forceinline__ void load_rows2_elect(uint32_t dst, uint32_t half, const void* tmap0, const void* tmap1, int row,
@@ -371,10 +387,42 @@ __device__ __forceinline__ void load_rows2_elect(uint32_t dst, uint32_t half, co
       :: "r"(dst), "r"(dst + half), "l"(reinterpret_cast<uint64_t>(tmap0)), "l"(reinterpret_cast<uint64_t>(tmap1)),
          "r"(row), "r"(plane), "r"(bar), "r"(2 * half), "l"(policy) : "memory");
 }
-__device__ __forceinline__ uint64_t l2_policy_evict_normal() {
-  uint64_t pol;
-  asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(pol));
-  return pol;
+// Four tcgen05.mma, 64 deep: D (+)= A B with both from shared memory, 128-byte rows (a step of 16 is 32 bytes on), or with A
+// from Tensor Memory and B's rows 2 048 bytes a step on.  One election for all four keeps a
+// step's code short.
+__device__ __forceinline__ void mma_ss4_elect(uint32_t d_tmem, uint32_t a_lo, uint32_t a_hi, uint32_t b_lo, uint32_t b_hi,
+                                              uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, q, e;\n\t.reg .b64 da, db;\n\t.reg .b32 a, b;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "setp.ne.b32 p, %6, 0;\n\t"
+      "setp.eq.b32 q, 0, 0;\n\t"
+      "mov.b64 da, {%1, %2};\n\tmov.b64 db, {%3, %4};\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %5, p;\n\t"
+      "add.u32 a, %1, 2;\n\tadd.u32 b, %3, 2;\n\tmov.b64 da, {a, %2};\n\tmov.b64 db, {b, %4};\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %5, q;\n\t"
+      "add.u32 a, %1, 4;\n\tadd.u32 b, %3, 4;\n\tmov.b64 da, {a, %2};\n\tmov.b64 db, {b, %4};\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %5, q;\n\t"
+      "add.u32 a, %1, 6;\n\tadd.u32 b, %3, 6;\n\tmov.b64 da, {a, %2};\n\tmov.b64 db, {b, %4};\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %5, q;\n\t}"
+      :: "r"(d_tmem), "r"(a_lo), "r"(a_hi), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"(accumulate) : "memory");
+}
+__device__ __forceinline__ void mma_ts4_elect(uint32_t d_tmem, uint32_t a_tmem, uint32_t b_lo, uint32_t b_hi, uint32_t idesc,
+                                              uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, q, e;\n\t.reg .b64 db;\n\t.reg .b32 a, b;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "setp.ne.b32 p, %5, 0;\n\t"
+      "setp.eq.b32 q, 0, 0;\n\t"
+      "mov.b64 db, {%2, %3};\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %4, p;\n\t"
+      "add.u32 a, %1, 8;\n\tadd.u32 b, %2, 128;\n\tmov.b64 db, {b, %3};\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a], db, %4, q;\n\t"
+      "add.u32 a, %1, 16;\n\tadd.u32 b, %2, 256;\n\tmov.b64 db, {b, %3};\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a], db, %4, q;\n\t"
+      "add.u32 a, %1, 24;\n\tadd.u32 b, %2, 384;\n\tmov.b64 db, {b, %3};\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a], db, %4, q;\n\t}"
+      :: "r"(d_tmem), "r"(a_tmem), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"(accumulate) : "memory");
 }
 
 // Many rows.  Roles: warps 0-3 and 4-7 the softmax of slot 0 and slot 1 (a thread has one of 128 rows),
@@ -456,7 +504,8 @@ __device__ __forceinline__ void many_rows(const CUtensorMap& tmQ, const CUtensor
 
   if (warp == PRODUCER_WARP) {
     const unsigned int share = uni(l.share[0]), total = uni(l.total[0]), lead = uni(l.lead[0]);
-    const unsigned int x0 = blockIdx.x * share, x1 = min(total, x0 + share);
+    const unsigned int x0 = uni(l.worker) * share, x1 = min(total, x0 + share);
+    const uint64_t once = l2_policy_evict_first();  // (see fa_prefix_kernel)
     int stage = 0, np = 0;
     uint32_t phase = 0, issued = 0, issued_parity = 0;
     bool ok = true;
@@ -479,7 +528,7 @@ __device__ __forceinline__ void many_rows(const CUtensorMap& tmQ, const CUtensor
         pg = p.num_pages;
       }
       if (!wait_all(W, bar_kv_empty + 8 * stage, phase ^ 1)) return false;
-      load_rows_elect(kv_smem + stage * L::TILE_BYTES, map, 0, pg * p.Hkv + g, bar_kv_full + 8 * stage, L::TILE_BYTES);
+      load_rows_elect(kv_smem + stage * L::TILE_BYTES, map, 0, pg * p.Hkv + g, bar_kv_full + 8 * stage, L::TILE_BYTES, once);
       issued |= 1u << stage;
       issued_parity = (issued_parity & ~(1u << stage)) | (phase << stage);
       if (++stage == L::STAGES) {
@@ -527,18 +576,18 @@ __device__ __forceinline__ void many_rows(const CUtensorMap& tmQ, const CUtensor
       if (!wait_all(W, bar_q_empty, (k & 1) ^ 1)) return false;
       const uint32_t box = static_cast<uint32_t>(q.tile_rows) * 128;
       mbar_arrive_expect_tx_elect(bar_q_full, box * L::BOXES * q.mode);
+#pragma unroll 1
       for (int i = 0; i < q.mode; ++i)
 #pragma unroll
         for (int b = 0; b < L::BOXES; ++b)
           tma_load_3d_elect(sbase + i * L::TILE_BYTES + b * BOX_BYTES, &tmQ, b * 64, g * p.group, t0 + i * p.tp,
                             bar_q_full);
-      if (q.mode == 1) {  // K_0 K_1 V_0 K_2 V_1 K_3 ...
-        if (!kv_load(&tmK, table, j0, ptiles, g) || (q.n > 1 && !kv_load(&tmK, table, j0 + 1, ptiles, g))) return false;
-        for (int j = j0; j < j1; ++j)
-          if (!kv_load(&tmV, table, j, ptiles, g) || (j + 2 < j1 && !kv_load(&tmK, table, j + 2, ptiles, g))) return false;
-      } else {
-        for (int j = j0; j < j1; ++j)
-          if (!kv_load(&tmK, table, j, ptiles, g) || !kv_load(&tmV, table, j, ptiles, g)) return false;
+      // two row tiles: K_0 V_0 K_1 V_1 ...; one: K_0 K_1 V_0 K_2 V_1 K_3 ... V_(n-1)
+#pragma unroll 1
+      for (int i = 0; i < 2 * q.n; ++i) {
+        const bool k = q.mode == 2 ? !(i & 1) : i == 0 || ((i & 1) && i < 2 * q.n - 1);
+        const int j = q.mode == 2 ? i >> 1 : k ? (i + 1) >> 1 : i < 2 * q.n - 1 ? (i >> 1) - 1 : q.n - 1;
+        if (!kv_load(k ? &tmK : &tmV, table, j0 + j, ptiles, g)) return false;
       }
       return true;
     };
@@ -546,6 +595,7 @@ __device__ __forceinline__ void many_rows(const CUtensorMap& tmQ, const CUtensor
     if (x0 < x1 && x0 < lead) {  // items of the prefix: head by head, needed block of rows by block
       const volatile unsigned int* need = reinterpret_cast<const volatile unsigned int*>(smem + NEED_OFF);
       const int tokens = uni(l.tokens), blocks = uni(l.blocks), per_head = uni(l.items), items = p.Hkv * per_head;
+#pragma unroll 1
       for (int at = x0 / prefix_item(p, tokens, 0).cost(); ok && at < items; ++at) {
         const Item it = prefix_item(p, tokens, at);
         if (it.c0 >= x1) break;
@@ -560,6 +610,7 @@ __device__ __forceinline__ void many_rows(const CUtensorMap& tmQ, const CUtensor
       int b = uni(begin->b), base = b - 32;
       unsigned int c0 = uni(begin->c0);
       int r_cu0 = 0, r_cu1 = 0, r_seq = 0;
+#pragma unroll 1
       for (; ok && b < p.B && c0 < x1; ++b) {
         if (b >= base + 32) {  // 32 requests at a time, one per lane
           base = b;
@@ -573,6 +624,7 @@ __device__ __forceinline__ void many_rows(const CUtensorMap& tmQ, const CUtensor
         if (is_few(p, r)) continue;
         const int* table = p.block_table + static_cast<size_t>(b) * p.max_pages;
         const int ptiles = is_big(p, r) ? p.tiles_p : 0;
+#pragma unroll 1
         for (int blk = 0; ok && blk * 2 * p.tp < r.added && c0 < x1; ++blk) {
           Item it = block_item(p, r, blk, c0);
           const unsigned int cost = it.cost();
@@ -582,6 +634,7 @@ __device__ __forceinline__ void many_rows(const CUtensorMap& tmQ, const CUtensor
           const int tiles0 = ptiles + tiles_of(visible(p, r, min(r.added, t + p.tp)));
           const int g0 = x0 > it.c0 ? (x0 - it.c0) / cost : 0;
           it.c0 += g0 * cost;
+#pragma unroll 1
           for (int g = g0; ok && g < p.Hkv && it.c0 < x1; ++g, it.c0 += cost) {
             const int j0 = it.from(x0), j1 = it.from(x1);
             if (j0 < j1)
@@ -600,6 +653,7 @@ __device__ __forceinline__ void many_rows(const CUtensorMap& tmQ, const CUtensor
     }
     if (!ok) {  // let every copy already issued land before the block exits
       if (np > 0) drain_all(W, bar_q_full, (np - 1) & 1);
+#pragma unroll 1
       for (int s = 0; s < L::STAGES; ++s)
         if (issued & (1u << s)) drain_all(W, bar_kv_full + 8 * s, (issued_parity >> s) & 1u);
     }
@@ -627,10 +681,8 @@ __device__ __forceinline__ void many_rows(const CUtensorMap& tmQ, const CUtensor
       const uint32_t a0 = dqk_lo + ((qtile * L::TILE_BYTES) >> 4);
       const uint32_t b0 = dqk_lo + ((L::KV_OFF + ks * L::TILE_BYTES) >> 4);
 #pragma unroll
-      for (int kk = 0; kk < D / 16; ++kk) {
-        const uint32_t off = ((kk / 4) * BOX_BYTES + (kk % 4) * 32) >> 4;
-        mma_ss_elect(tmem + slot * 128, a0 + off, dqk_hi, b0 + off, dqk_hi, IDESC_S, kk > 0 ? 1u : 0u);
-      }
+      for (int c = 0; c < D / 64; ++c)
+        mma_ss4_elect(tmem + slot * 128, a0 + c * (BOX_BYTES >> 4), dqk_hi, b0 + c * (BOX_BYTES >> 4), dqk_hi, IDESC_S, c);
       mma_commit_elect(bar_s_full + 8 * slot);
     };
     // The last tile of a source holds fewer than 128 keys, and what its page holds behind them may be
@@ -641,6 +693,7 @@ __device__ __forceinline__ void many_rows(const CUtensorMap& tmQ, const CUtensor
       const int valid = tile < q.ptiles ? p.prefix_len - tile * BN : q.keys - (tile - q.ptiles) * BN;
       if (valid >= BN) return BN / 16;
       const int steps = (valid + 15) / 16, words = (steps * 16 - valid) * 8;  // 16-byte words per box
+#pragma unroll 1
       for (int w = lane; w < words * L::BOXES; w += 32) {
         const int box = w / words, at = w - box * words;
         st_shared_v4(kv_smem + vs * L::TILE_BYTES + box * BOX_BYTES + valid * 128 + at * 16, 0, 0, 0, 0);
@@ -652,11 +705,10 @@ __device__ __forceinline__ void many_rows(const CUtensorMap& tmQ, const CUtensor
     auto issue_pv = [&](int slot, int vs, int steps, bool acc) {  // O_slot (+)= P_slot V, keys in steps of 16
       const uint32_t b0 = dv_lo + ((L::KV_OFF + vs * L::TILE_BYTES) >> 4);
       if (steps == BN / 16) {
-#pragma unroll
-        for (int kk = 0; kk < BN / 16; ++kk)
-          mma_ts_elect(tmem + 256 + slot * D, tmem + slot * 128 + kk * 8, b0 + ((kk * 2048) >> 4), dv_hi, IDESC_PV,
-                       (acc || kk > 0) ? 1u : 0u);
+        mma_ts4_elect(tmem + 256 + slot * D, tmem + slot * 128, b0, dv_hi, IDESC_PV, acc ? 1u : 0u);
+        mma_ts4_elect(tmem + 256 + slot * D, tmem + slot * 128 + 32, b0 + (8192 >> 4), dv_hi, IDESC_PV, 1u);
       } else {
+#pragma unroll 1
         for (int kk = 0; kk < steps; ++kk)
           mma_ts_elect(tmem + 256 + slot * D, tmem + slot * 128 + kk * 8, b0 + ((kk * 2048) >> 4), dv_hi, IDESC_PV,
                        (acc || kk > 0) ? 1u : 0u);
@@ -672,6 +724,7 @@ __device__ __forceinline__ void many_rows(const CUtensorMap& tmQ, const CUtensor
       tc_fence_after();
       return true;
     };
+#pragma unroll 1
     for (int k = 0; ok; ++k) {
       const int s = k % kPieceSlots;
       if (!(ok = wait_all(W, bar_piece_full + 8 * s, (k / kPieceSlots) & 1))) break;
@@ -690,12 +743,14 @@ __device__ __forceinline__ void many_rows(const CUtensorMap& tmQ, const CUtensor
       tc_fence_after();
       int ks = 0, vs = 0;
       if (q.mode == 1) {
+#pragma unroll 1
         for (int x = 0; ok && x < min(q.n, 2); ++x) {
           if (!(ok = take(ks))) break;
           issue_s(x, 0, ks);
           if (x + 1 == q.n) mma_commit_elect(bar_q_empty);
           mma_commit_elect(bar_kv_empty + 8 * ks);
         }
+#pragma unroll 1
         for (int x = 0; ok && x < q.n; ++x) {
           const int slot = x & 1;
           if (!(ok = take(vs))) break;
@@ -717,6 +772,7 @@ __device__ __forceinline__ void many_rows(const CUtensorMap& tmQ, const CUtensor
         issue_s(1, 1, ks);
         if (q.n == 1) mma_commit_elect(bar_q_empty);
         mma_commit_elect(bar_kv_empty + 8 * ks);
+#pragma unroll 1
         for (int j = 0; j < q.n; ++j) {
           bool next = false;
           if (!(ok = take(vs))) break;
@@ -755,9 +811,11 @@ __device__ __forceinline__ void many_rows(const CUtensorMap& tmQ, const CUtensor
     const uint32_t my_s_full = bar_s_full + 8 * i, my_p_full = bar_p_full + 8 * i;
     const uint32_t my_o_full = bar_o_full + 8 * i;
     const int tok = rt / p.group;  // the row's token within its tile
+    const int l_worker = l.worker;  // (l is the sum below)
     const float sl2 = p.scale_log2;
     uint32_t sf_phase = 0, of_phase = 0, x_phase = 0;
     bool ok = true;
+#pragma unroll 1
     for (int k = 0; ok; ++k) {
       const int s = k % kPieceSlots;
       if (!(ok = wait_all(W, bar_piece_full + 8 * s, (k / kPieceSlots) & 1))) break;
@@ -776,6 +834,7 @@ __device__ __forceinline__ void many_rows(const CUtensorMap& tmQ, const CUtensor
       if (!live) lim = 0;
       float m_run = -INFINITY;  // reference max, base-2 units of the scaled score
       float l = 0.f, lr = 0.f;  // sums of the fp32 weights (LSE) and of the bf16 weights the product uses (divides O)
+#pragma unroll 1
       for (int x = 0; x < n_mine; ++x) {
         if (!(ok = wait_all(W, my_s_full, sf_phase))) break;
         sf_phase ^= 1;
@@ -884,18 +943,18 @@ __device__ __forceinline__ void many_rows(const CUtensorMap& tmQ, const CUtensor
         const float lse2 = l == 0.f ? -INFINITY : m_run + log2f(l);
         a0 *= inv;
         a1 *= inv;
-        const RowOut to = row_out<D>(p, dst, many_slab(p, blockIdx.x, dst == kDstSlab1), g, t0, row0 + rt);
+        const RowOut to = row_out<D>(p, dst, many_slab(p, l_worker, dst == kDstSlab1), g, t0, row0 + rt);
         if (live) *to.lse = to.out ? lse2 * LN2 : lse2;
         // O leaves 16 rows at a time in the layout in which four lanes have eight columns of a row (a whole 32-byte
         // sector of a part): lane l has columns 2 (l % 4), + 1 of every eight, rows l / 4 and l / 4 + 8
         const unsigned long long mine = live ? reinterpret_cast<unsigned long long>(to.out ? static_cast<void*>(to.out) : to.part) : 0;
-#pragma unroll
+#pragma unroll 1
         for (int h = 0; h < 2; ++h) {
           const int r_lo = h * 16 + lane / 4, r_hi = r_lo + 8;
           const unsigned long long at_lo = __shfl_sync(0xffffffffu, mine, r_lo), at_hi = __shfl_sync(0xffffffffu, mine, r_hi);
           const float a0_lo = __shfl_sync(0xffffffffu, a0, r_lo), a0_hi = __shfl_sync(0xffffffffu, a0, r_hi);
           const float a1_lo = __shfl_sync(0xffffffffu, a1, r_lo), a1_hi = __shfl_sync(0xffffffffu, a1, r_hi);
-#pragma unroll
+#pragma unroll 1
           for (int c = 0; c < D / 64; ++c) {
             uint32_t ov[32];
             tmem_ld_16x256b_x8_wait(t_o + (uint32_t(h * 16) << 16) + c * 64, ov);
@@ -1018,6 +1077,7 @@ struct FewWalk {
     have = false;
   }
   __device__ __forceinline__ bool next(const PrefixParams& p, int lane, FewPiece& q) {
+#pragma unroll 1
     while (at < items) {
       const Item i = prefix_item(p, tokens, at);
       const int j0 = i.from(x0), j1 = i.from(x1);
@@ -1029,6 +1089,7 @@ struct FewWalk {
       return true;
     }
     if (x1 <= lead) return false;
+#pragma unroll 1
     for (;;) {
       if (have) {
         if (g < p.Hkv) {
@@ -1045,6 +1106,7 @@ struct FewWalk {
         ++b;
         have = false;
       }
+#pragma unroll 1
       for (;; ++b) {
         if (b >= p.B || c0 >= x1) return false;
         if (b >= base + 32) {  // 32 requests at a time, one per lane
@@ -1082,7 +1144,7 @@ __device__ __forceinline__ void few_rows(const CUtensorMap& tmK, const CUtensorM
   const uint32_t ring = sbase + team * L::STAGES * L::STEP_BYTES;
   const uint32_t bar_full = sbase + L::BAR_OFF + 8 * team * L::STAGES;
   const uint32_t bar_empty = bar_full + 8 * L::TEAMS * L::STAGES;
-  const int worker = (blockIdx.x - uni(l.many)) * L::TEAMS + team;
+  const int worker = uni(l.worker) * L::TEAMS + team;
   const unsigned int total = uni(l.total[1]), share = uni(l.share[1]);
   const unsigned long long from = static_cast<unsigned long long>(worker) * share;
   if (from >= total) return;
@@ -1094,15 +1156,15 @@ __device__ __forceinline__ void few_rows(const CUtensorMap& tmK, const CUtensorM
 
   // The ring's filling side (the team's first warp).  It stands a piece ahead: the next piece's pages (32 tiles', one per
   // lane) and query rows are asked for when the piece before it begins.
-  FewWalk load;
-  FewPiece lp, ahead;
+  FewWalk walk, load;
+  FewPiece q, lp, ahead;
   int lj = 0, issued = 0, lstage = 0, page = 0, base = 0, ahead_page = 0;
-  bool more = mt == 0, any = false;
-  auto look_ahead = [&] {
-    any = load.next(p, lane, ahead);
-    if (!any) return;
+  walk.start(p, l, x0, x1, first, first_place);
+  bool have = walk.next(p, lane, q), more = mt == 0, any = have;
+  auto ask = [&] {  // for the piece ahead's pages and query rows
     const int first_tile = ahead.j0 / (kPage / L::STEP) & ~31;
     ahead_page = first_tile + lane < ahead.entries ? ahead.table[first_tile + lane] : 0;
+#pragma unroll 1
     for (int r = lane; r < ahead.rows; r += 32) {
       const int tok = r / p.group;
       const __nv_bfloat16* src = p.q + (static_cast<size_t>(ahead.t0 + tok) * p.H + ahead.g * p.group + (r - tok * p.group)) * D;
@@ -1111,12 +1173,12 @@ __device__ __forceinline__ void few_rows(const CUtensorMap& tmK, const CUtensorM
     }
   };
   if (mt == 0) {
-    load.start(p, l, x0, x1, first, first_place);
+    load = walk;
+    ahead = q;
     lp.j1 = 0;
-    look_ahead();
+    if (any) ask();
   }
-  // own keys are read once: in L2 they go before the prefix, the parts and the kernels' code
-  const uint64_t once = l2_policy_evict_first(), keep = l2_policy_evict_normal();
+  const uint64_t once = l2_policy_evict_first();
   auto fill = [&]() -> bool {  // loads the stretch's next step, if there is one
     if (lj >= lp.j1) {
       if (!any) {
@@ -1127,7 +1189,7 @@ __device__ __forceinline__ void few_rows(const CUtensorMap& tmK, const CUtensorM
       lj = lp.j0;
       page = ahead_page;
       base = lj / (kPage / L::STEP) & ~31;
-      look_ahead();
+      if ((any = load.next(p, lane, ahead))) ask();
     }
     const int tile = lj / (kPage / L::STEP);
     if ((tile & ~31) != base) {
@@ -1143,7 +1205,7 @@ __device__ __forceinline__ void few_rows(const CUtensorMap& tmK, const CUtensorM
         !wait_all(W, bar_empty + 8 * lstage, (issued / L::STAGES - 1) & 1))
       return false;
     load_rows2_elect(ring + lstage * L::STEP_BYTES, L::STEP_BYTES / 2, &tmK, &tmV, (lj % (kPage / L::STEP)) * L::STEP,
-                     pg * p.Hkv + lp.g, bar_full + 8 * lstage, lp.table == p.prefix_table ? keep : once);
+                     pg * p.Hkv + lp.g, bar_full + 8 * lstage, once);
     ++lj;
     ++issued;
     if (++lstage == L::STAGES) lstage = 0;
@@ -1151,6 +1213,7 @@ __device__ __forceinline__ void few_rows(const CUtensorMap& tmK, const CUtensorM
   };
   bool ok = true;
   // one stage behind when other warps read the ring too, so as not to wait for the slowest at every step
+#pragma unroll 1
   for (int t = 0; ok && more && t < L::STAGES - (R > 1); ++t) ok = fill();
 
   const int row0 = mt * 8 * NT, c0 = 2 * (lane & 3);  // this warp's first row; a thread's columns of a product, c0 and c0 + 1
@@ -1166,10 +1229,8 @@ __device__ __forceinline__ void few_rows(const CUtensorMap& tmK, const CUtensorM
   const uint32_t ones[4] = {0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u};
   int stage = 0;
   uint32_t full_par = 0;
-  FewWalk walk;
-  walk.start(p, l, x0, x1, first, first_place);
-  FewPiece q;
-  while (ok && walk.next(p, lane, q)) {
+#pragma unroll 1
+  for (; ok && have; have = walk.next(p, lane, q)) {
     uint32_t qf[D / 16][NT][2];  // Q^T
     int lim[NT][2], lim_min = q.keys;  // keys the thread's rows see (rows past the last one: all, they are not used)
 #pragma unroll
@@ -1206,6 +1267,7 @@ __device__ __forceinline__ void few_rows(const CUtensorMap& tmK, const CUtensorM
         for (int c = 0; c < D / 16; ++c) o[c][t][e] = 0.f;
       }
     }
+#pragma unroll 1
     for (int j = q.j0; j < q.j1; ++j) {
       if (!(ok = wait_all(W, bar_full + 8 * stage, (full_par >> stage) & 1))) break;
       full_par ^= 1u << stage;
@@ -1353,10 +1415,16 @@ __device__ __forceinline__ void few_rows(const CUtensorMap& tmK, const CUtensorM
       }
   }
   if (!ok && mt == 0)  // let every copy already issued land before the block exits
+#pragma unroll 1
     for (int t = 0; t < L::STAGES && t < issued; ++t)
       drain_all(W, bar_full + 8 * t, ((issued - 1 - t) / L::STAGES) & 1);
 }
 
+// All keys are loaded to go first from L2: a key tile is read again, by the other row blocks of its head, within
+// microseconds, while the kernel's code, which every block waits for as it starts, has to live until the next call (55
+// against 61 us for 64 requests behind 16 384 keys, 73 against 84 for 256).  For the same reason loops of run-time length
+// stay rolled, and the many-row code comes first: what is further behind the kernel's start arrives later (80 against
+// 82 us for 128 requests behind 32 768 keys).
 template <int D, int NT, int R>
 __global__ void __launch_bounds__(THREADS, 1)
 fa_prefix_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
@@ -1391,7 +1459,7 @@ fa_prefix_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
   tc_fence_after();
   pdl_wait();
   const Plan l = make_plan(p, *reinterpret_cast<Layout*>(smem), need, reinterpret_cast<Begin*>(smem + BEGIN_OFF));
-  if (static_cast<int>(blockIdx.x) < l.many)
+  if (!l.few)
     many_rows<D>(tmQ, tmK, tmV, p, l, smem);
   else
     few_rows<D, NT, R>(tmK16, tmV16, p, l, smem);
@@ -1476,6 +1544,7 @@ __device__ __forceinline__ void join_row(const PrefixParams& p, const Plan& l, s
 #pragma unroll
   for (int c = 0; c < C; ++c) acc[c] = 0.f;
   const int parts = pre.count + own.count;
+#pragma unroll 1
   for (int i0 = 0; i0 < parts; i0 += G * W) {
     const int i = i0 + sub * W + (W > 1 ? warp : 0);
     float lse2 = -INFINITY;
@@ -1588,6 +1657,7 @@ __global__ void __launch_bounds__(W > 1 ? 32 * W : kJoinThreads) fa_prefix_join_
   l.items = p.hdr[kHdrItems];
   l.tokens = p.hdr[kHdrTokens];
   const long long rows = static_cast<long long>(l.tokens) * p.H;
+#pragma unroll 1
   for (; row < all; row += stride) {
     const int n = static_cast<int>(row / p.H), g = static_cast<int>(row - static_cast<long long>(n) * p.H) / p.group;
     const int4 t = __ldg(p.tok + n);  // (past the last token: whatever, not used)
