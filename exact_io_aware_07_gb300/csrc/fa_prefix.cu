@@ -62,7 +62,8 @@ struct Item {
   // first unit whose place is not before x
   __device__ __forceinline__ int from(unsigned int x) const {
     if (x <= c0 + lead) return 0;
-    const unsigned int j = (x - c0 - lead + unit - 1) / unit;
+    const unsigned int y = x - c0 - lead + unit - 1;  // (units are of three sizes: no division by a variable)
+    const unsigned int j = unit == 1u ? y : unit == kTileCost256 ? y / kTileCost256 : y / kTileCost128;
     return j < static_cast<unsigned int>(units) ? static_cast<int>(j) : units;
   }
   __device__ __forceinline__ unsigned int worker(int unit_index, unsigned int share) const {
@@ -76,7 +77,7 @@ __device__ __forceinline__ Item many_item(unsigned int c0, int tiles, int rows) 
 template <int D>
 constexpr int kStep = D == 64 ? 32 : 16;
 __device__ __forceinline__ Item few_item(const PrefixParams& p, unsigned int c0, int keys) {
-  return Item{c0, kFewItemCost, 1u, (keys + p.step - 1) / p.step};
+  return Item{c0, kFewItemCost, 1u, (keys + p.step - 1) >> (p.step == 32 ? 5 : 4)};
 }
 
 struct Request {
@@ -138,6 +139,11 @@ struct Plan {
   int few, worker;                           // whether this block works few rows; its number among the blocks of its kind
 };
 
+__device__ __forceinline__ float sqrt_approx(float x) {
+  float y;
+  asm("sqrt.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
 __device__ __forceinline__ bool flagged(const PrefixParams& p, int blocks) { return blocks <= kMaxFlags; }
 // The needed block with `rank` needed ones before it.
 __device__ __forceinline__ int needed_block(const PrefixParams& p, const volatile unsigned int* need, int blocks, int rank) {
@@ -200,7 +206,7 @@ __device__ __forceinline__ Plan make_plan(const PrefixParams& p, Layout& s, vola
   l.lead[0] = few ? 0u : prefix;
   l.lead[1] = few ? prefix : 0u;
   unsigned long long before = l.lead[0] | static_cast<unsigned long long>(l.lead[1]) << 32, all = before;
-#pragma unroll 2
+#pragma unroll
   for (int w = 0; w < THREADS / 32; ++w) {
     const unsigned long long t = s.warp[w];
     before += w < warp ? t : 0u;
@@ -214,9 +220,9 @@ __device__ __forceinline__ Plan make_plan(const PrefixParams& p, Layout& s, vola
   // where loading all keys takes longer than that, more do no harm to the few rows until their own work takes as long,
   // and the many-row blocks, which wait for their keys behind the others', are given time for kManyShare of the loading.
   const float a = kManyTime * l.total[0], b = kFewTime * l.total[1], g = p.ctas, d = kManyStart * g - a - b;
-  float m = (d + sqrtf(d * d + 4.f * kManyStart * a * g)) / (2.f * kManyStart);
+  float m = (d + sqrt_approx(d * d + 4.f * kManyStart * a * g)) * (0.5f / kManyStart);
   const float load = (l.total[1] * 8192.f + p.Hkv * p.tiles_p * 2.f * kPage * p.head_bytes) / kLoadRate;
-  m = max(m, min(a / (kManyShare * load), g - b / load));
+  m = max(m, min(__fdividef(a, kManyShare * load), g - __fdividef(b, load)));
   l.many = l.total[0] == 0 ? 0 : l.total[1] == 0 ? p.ctas : max(1, min(p.ctas - 1, __float2int_rn(m)));
   l.share[0] = max(1u, (l.total[0] + max(l.many, 1) - 1) / max(l.many, 1));
   // Only the prefix on the many-row line: every item in the same whole number of stretches, so that the row blocks of a
@@ -265,7 +271,8 @@ __device__ __forceinline__ Plan make_plan(const PrefixParams& p, Layout& s, vola
     }
   }
 #pragma unroll 1
-  for (int n = blockIdx.x + gridDim.x * tid; n < l.tokens; n += gridDim.x * THREADS) {
+  // (the first warp is at `begin` meanwhile)
+  for (int n = blockIdx.x + gridDim.x * (tid - 32); n >= 0 && n < l.tokens; n += gridDim.x * (THREADS - 32)) {
     const int t = owner([&](int k) { return static_cast<unsigned int>(s.first[k]); }, n);
     unsigned int c0[2] = {static_cast<unsigned int>(s.cum[t]), static_cast<unsigned int>(s.cum[t] >> 32)};
     int b = t * run;
@@ -1477,9 +1484,10 @@ fa_prefix_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
 struct Parts {
   Item it;
   bool few;
+  unsigned int share;
   int first, count, seen, at;  // first worker, workers; units visible to the row; the row's number within the item
   __device__ __forceinline__ void locate(const PrefixParams& p, const Plan& l) {
-    const unsigned int share = few ? l.share[1] : l.share[0];
+    share = few ? l.share[1] : l.share[0];
     // (places past the last worker come only of a cu_new that decreases, which is reported)
     const unsigned int last = (few ? p.ctas * p.teams : p.ctas) - 1;
     const unsigned int w0 = min(it.worker(0, share), last), w1 = min(it.worker(it.units - 1, share), last);
@@ -1487,7 +1495,7 @@ struct Parts {
     count = w1 < w0 ? 1 : static_cast<int>(w1 - w0) + 1;
   }
   // Row of the slabs that worker `first + i` wrote the part to; -1 if it had none of the row's units.
-  __device__ __forceinline__ long long slab_row(const PrefixParams& p, unsigned int share, int i) const {
+  __device__ __forceinline__ long long slab_row(const PrefixParams& p, int i) const {
     const int w = first + i, j0 = it.from(w * share), j1 = it.from((w + 1) * share);
     if (j0 >= j1 || j0 >= seen) return -1;
     return static_cast<long long>((few ? few_slab(p, w, j0 == 0) : many_slab(p, w, j0 == 0)) + at);
@@ -1513,24 +1521,18 @@ __device__ __forceinline__ void load_columns(const float* src, int sub, float (&
   }
 }
 
-// Joins row n * H + h: t and rank are the token's.  G lanes of a warp (`mask`, this one the `sub`-th) or, W > 1, W whole
-// warps together; every lane has D / G columns.  The lanes look up G parts at a time (warp w of W every W-th), weight
+// Joins row h of token n if it needs it: if it has no, or several parts (a row with one item and that inside one worker's
+// stretch is written already).  t and rank are the token's.  G lanes of a warp (`mask`, this one the `sub`-th) or, W > 1, W
+// whole warps together; every lane has D / G columns.  The lanes look up G parts at a time (warp w of W every W-th), weight
 // them by their LSE and add them several loads at a time.
 template <int D, int W, int G>
-__device__ __forceinline__ void join_row(const PrefixParams& p, const Plan& l, size_t orow, int4 t, int rank, int warp, int sub,
+__device__ __forceinline__ void join_row(const PrefixParams& p, const Plan& l, int n, int h, int4 t, int rank, int warp, int sub,
                                          unsigned int mask, float* smem) {
   constexpr int C = D / G;  // columns 4 G e + 4 sub .. of the e-th four, or (C < 4) C sub ..
-  const int n = static_cast<int>(orow / p.H), h = static_cast<int>(orow - static_cast<size_t>(n) * p.H);
+  const size_t orow = static_cast<size_t>(n) * p.H + h;
   const int g = h / p.group, hh = h - g * p.group;
   Parts pre, own;
   pre.count = own.count = 0;
-  if (rank >= 0) {
-    pre.few = few_prefix(p, l.tokens);
-    pre.it = prefix_item(p, l.tokens, g * l.items + rank);
-    pre.seen = INT_MAX;
-    pre.at = (pre.few ? n : n % (2 * p.tp)) * p.group + hh;
-    pre.locate(p, l);
-  }
   if (t.z > 0) {
     own.few = t.w & kTokFew;
     own.it = Item{static_cast<unsigned int>(t.x), own.few ? kFewItemCost : kItemCost,
@@ -1539,6 +1541,14 @@ __device__ __forceinline__ void join_row(const PrefixParams& p, const Plan& l, s
     own.seen = t.z;
     own.at = (t.w & (kTokFew - 1)) * p.group + hh;
     own.locate(p, l);
+    if (rank < 0 && own.count == 1) return;
+  }
+  if (rank >= 0) {
+    pre.few = few_prefix(p, l.tokens);
+    pre.it = prefix_item(p, l.tokens, g * l.items + rank);
+    pre.seen = INT_MAX;
+    pre.at = (pre.few ? n : n % (2 * p.tp)) * p.group + hh;
+    pre.locate(p, l);
   }
   float m = -INFINITY, sum = 0.f, acc[C];
 #pragma unroll
@@ -1555,8 +1565,8 @@ __device__ __forceinline__ void join_row(const PrefixParams& p, const Plan& l, s
         o = (is_own ? p.own_o : p.prefix_o) + orow * D;
         lse2 = __ldg((is_own ? p.own_lse : p.prefix_lse) + orow);
       } else {
-        const long long row = is_own ? own.slab_row(p, own.few ? l.share[1] : l.share[0], i - pre.count)
-                                     : pre.slab_row(p, pre.few ? l.share[1] : l.share[0], i);
+        const Parts part = is_own ? own : pre;
+        const long long row = part.slab_row(p, is_own ? i - pre.count : i);
         if (row >= 0) {
           o = p.slab_o + row * D;
           lse2 = __ldg(p.slab_lse + row);
@@ -1578,7 +1588,7 @@ __device__ __forceinline__ void join_row(const PrefixParams& p, const Plan& l, s
     const int here = min(G, (parts - i0 + W - 1) / W);
     // (lanes without a part have weight 0 and the address of some other: loaded all the same, so that the loads of several
     // parts are under way together, and not added)
-#pragma unroll 8 / (C > 4 ? C / 4 : 1)
+#pragma unroll 4 / (C > 4 ? C / 4 : 1)
     for (int k = 0; k < here; ++k) {
       const float w = __shfl_sync(mask, mine, k, G);
       const float* src = reinterpret_cast<const float*>(__shfl_sync(mask, reinterpret_cast<unsigned long long>(o), k, G));
@@ -1627,17 +1637,6 @@ __device__ __forceinline__ void join_row(const PrefixParams& p, const Plan& l, s
   if (sub == 0) p.lse[orow] = sum == 0.f ? -INFINITY : (m + log2f(sum)) * LN2;
 }
 
-// Whether a row of K/V head g has to be joined: it has no, or several parts.  (A row with one item and that inside one
-// worker's stretch is written already.)
-__device__ __forceinline__ bool needs_join(const Plan& l, const int4& t, int rank, int g) {
-  if (rank >= 0 || t.z == 0) return true;
-  const bool few = t.w & kTokFew;
-  Item it{static_cast<unsigned int>(t.x), few ? kFewItemCost : kItemCost, few ? 1u : static_cast<unsigned int>(t.w) >> 16, t.y};
-  it.c0 += g * it.cost();
-  const unsigned int share = few ? l.share[1] : l.share[0];
-  return it.worker(0, share) != it.worker(it.units - 1, share);
-}
-
 // Joins the rows that need it.  W = 8: a row per block (few rows, perhaps of many parts); else a warp or, of many rows,
 // eight lanes a row (prompt chunks: most rows have two parts, and the time is that of their loads one after another).
 constexpr int kJoinThreads = 128;
@@ -1647,22 +1646,21 @@ __global__ void __launch_bounds__(W > 1 ? 32 * W : kJoinThreads) fa_prefix_join_
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = lane % G;
   const unsigned int mask = G == 32 ? 0xffffffffu : 0xffu << (lane & 24);
   pdl_launch_dependents();  // a following call's blocks may set themselves up
-  const long long all = static_cast<long long>(p.N) * p.H;
-  const long long stride = W > 1 ? gridDim.x : static_cast<long long>(gridDim.x) * (kJoinThreads / G);
-  long long row = W > 1 ? blockIdx.x : static_cast<long long>(blockIdx.x) * (kJoinThreads / G) + threadIdx.x / G;
+  const unsigned int all = static_cast<unsigned int>(p.N) * p.H;  // (N H is below 2^31)
+  const unsigned int stride = W > 1 ? gridDim.x : gridDim.x * (kJoinThreads / G);
+  unsigned int row = W > 1 ? blockIdx.x : blockIdx.x * (kJoinThreads / G) + threadIdx.x / G;
   if (row >= all) return;
   Plan l;
   l.share[0] = p.hdr[kHdrShare];
   l.share[1] = p.hdr[kHdrShare + 1];
   l.items = p.hdr[kHdrItems];
   l.tokens = p.hdr[kHdrTokens];
-  const long long rows = static_cast<long long>(l.tokens) * p.H;
 #pragma unroll 1
   for (; row < all; row += stride) {
-    const int n = static_cast<int>(row / p.H), g = static_cast<int>(row - static_cast<long long>(n) * p.H) / p.group;
+    const int n = static_cast<int>(row / p.H), h = static_cast<int>(row) - n * p.H;
     const int4 t = __ldg(p.tok + n);  // (past the last token: whatever, not used)
     const int rank = __ldg(p.rank + n);
-    if (row < rows && needs_join(l, t, rank, g)) join_row<D, W, G>(p, l, static_cast<size_t>(row), t, rank, warp, sub, mask, smem);
+    if (n < l.tokens) join_row<D, W, G>(p, l, n, h, t, rank, warp, sub, mask, smem);
   }
 }
 
