@@ -747,3 +747,15 @@ def test_steps_together(d, H, Hkv):
         new.copy_(i(want))
         graph.replay()
         check(q, want, buf, f"step {s}")
+
+
+@pytest.mark.parametrize("op", ["plan", "append", "prefix", "step"])
+def test_command_line(op, monkeypatch, capsys):
+    import sys
+
+    from exact_io_aware_07_gb300 import __main__ as cli
+
+    monkeypatch.setattr(sys, "argv", ["x", "--op", op, "--B", "3", "--H", "4", "--hkv", "2", "--T", "200", "--d", "64",
+                                      "--prefix", "300", "--new", "2"])
+    assert cli.main() == 0
+    assert "device status 0" in capsys.readouterr().out
