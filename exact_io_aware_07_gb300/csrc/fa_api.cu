@@ -473,8 +473,8 @@ PrefixWorkspace prefix_workspace(int N, int H, int Hkv, int d) {
   const size_t rows = static_cast<size_t>(N) * H;
   const long long item = (static_cast<long long>(N) * (H / Hkv) + 31) / 32 * 32;  // rows an item can have
   w.slab_rows = static_cast<int>(std::min<long long>(256, item));
-  // rows of the slabs of cut items: two per many-row worker (block), two of 128 / 8, / 4 or / 2 rows per team
-  const size_t slabs = static_cast<size_t>(fa::kPrefixMaxCtas) * 2 * (w.slab_rows + 128);
+  // rows of the slabs of cut items: two per many-row worker (block), two of up to 16 rows per few-row worker (warp)
+  const size_t slabs = static_cast<size_t>(fa::kPrefixMaxCtas) * 2 * (w.slab_rows + 16 * fa::kTeams);
   w.tok = take(static_cast<size_t>(N) * 16);
   w.rank = take(static_cast<size_t>(N) * 4);
   w.slab_o = take(slabs * d * 4);
@@ -915,11 +915,10 @@ fa_status fa_fwd_prefix_paged(const void* q, const void* k_pages, const void* v_
   p.scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634074);
   p.timeout_ns = kWaitLimitNs;
   p.ctas = std::min(num_sms, fa::kPrefixMaxCtas);
-  // rows of the few-row items: the fewest that hold a request of max_new tokens; when that is more than 64 rows
-  // (prompt chunks), a decoding request
-  const long long most = static_cast<long long>(std::min(max_new, N)) * group, rows = most <= 64 ? most : group;
-  p.few_rows = rows <= 8 || rows > 64 ? 8 : rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
-  p.teams = p.few_rows <= 16 ? 8 : p.few_rows == 32 ? 4 : 2;
+  // rows of the few-row items at most: 8, or at d = 64 up to 16 where the requests (or, beside prompt chunks, a decoding
+  // request) need them (see few_rows in fa_prefix.cu)
+  const long long most = static_cast<long long>(std::min(max_new, N)) * group, rows = most <= 16 ? most : group;
+  p.few_rows = d == 64 && rows > 8 && rows <= 16 ? 16 : 8;
   p.head_bytes = 2 * d;
   p.step = d == 64 ? 32 : 16;
   p.tiles_p = static_cast<int>(prefix_pages);

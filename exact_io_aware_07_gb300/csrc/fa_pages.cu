@@ -12,6 +12,12 @@ static __device__ unsigned int g_pages_status;  // kStatus* bits
 // scan, and keeps them in shared memory; the blocks share out the tokens and the new pages of
 // those requests, each thread finding its request by bisection.  Blocks need nothing from one
 // another: a kept table entry (read for the tokens that fill up a page) is never written.
+//
+// Bound by latency, not by its bytes (310 KB for 2 000 requests, 0.05 us at the rate of the memory): lengths, scan and
+// barriers, a bisection in shared memory, one dependent load of a page, stores.  2.8 us for 64 decoding requests, 4.5 for
+// 7 prompts of up to 9 000 tokens, 8.9 for 2 000 requests with 62 000 tokens (two scans of 1024 requests one behind the
+// other).  One kernel, every block with the whole scan: a scan over blocks would add a launch or a wait between blocks
+// (2 us) to save at most the second half of the last.
 constexpr int kPlanThreads = 1024;
 
 __device__ __forceinline__ int pages_of(int n) { return (n >> 7) + ((n & 127) != 0); }
@@ -131,6 +137,7 @@ __global__ void __launch_bounds__(kPlanThreads) fa_page_plan_kernel(const PlanPa
 }
 
 cudaError_t launch_page_plan(const PlanParams& p, int num_sms, cudaStream_t stream) {
+  // a block per 4 096 places of the slot map: fewer blocks would queue up stores, more repeat the scan to no use
   const long long want = (static_cast<long long>(p.max_tokens) + 4 * kPlanThreads - 1) / (4 * kPlanThreads);
   const int grid = static_cast<int>(want < 1 ? 1 : want > num_sms ? num_sms : want);
   fa_page_plan_kernel<<<grid, kPlanThreads, 0, stream>>>(p);
@@ -138,7 +145,9 @@ cudaError_t launch_page_plan(const PlanParams& p, int num_sms, cudaStream_t stre
 }
 
 // ---------------------------------------------------------------- append
-// One thread moves 16 bytes of one token's K row and the same 16 bytes of its V row.
+// One thread moves 16 bytes of one token's K row and the same 16 bytes of its V row: a head's 128 or 256 bytes are whole
+// sectors on both sides, whatever the slots.  Bound by HBM, each byte read and written once: 16 384 tokens of 8 heads of 128
+// take 21.9 us, 6.1 TB/s (90 % of the measured copy rate); 64 tokens 1.7 us, which is a launch's latency.
 __global__ void __launch_bounds__(256) fa_kv_append_kernel(const AppendParams p) {
   const int chunks = p.Hkv * p.d / 8, per_head = p.d / 8;
   const long long at = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x;

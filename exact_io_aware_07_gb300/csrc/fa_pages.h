@@ -53,8 +53,7 @@ struct PrefixParams {
   float scale_log2;               // scale * log2(e)
   unsigned long long timeout_ns;  // bound on every in-kernel wait
   int ctas;      // blocks of the attention kernel: one per SM, at most kPrefixMaxCtas
-  int teams;     // few-row teams per block: 8, 4 or 2
-  int few_rows;  // rows of a few-row item at most: 8, 16 (one warp), 32 or 64
+  int few_rows;  // rows of a few-row item at most: 8 or 16
   int head_bytes;  // of a key's row: 2 d
   int step;      // keys per few-row step: 16 (d = 128) or 32
   int tiles_p;   // 128-key tiles of the prefix
@@ -65,7 +64,7 @@ struct PrefixParams {
                       // tile sees, the token's number in the item | kTokFew | places of a unit << 16
   int* rank;          // [N] the token's item of the prefix (K/V head 0); -1: none
   int slab_rows;      // rows of a many-row slab
-  float* slab_o;      // [ctas][2][slab_rows][d], then [ctas * teams][2][few_rows][d]: parts of cut items
+  float* slab_o;      // [ctas][2][slab_rows][d], then [ctas * kTeams][2][few_rows][d]: parts of cut items
   float* slab_lse;    // the same rows, base-2
   float* own_o;       // [N * H][d] parts of whole items of own keys
   float* own_lse;
@@ -73,6 +72,7 @@ struct PrefixParams {
   float* prefix_lse;
 };
 constexpr int kPrefixMaxCtas = 160;
+constexpr int kTeams = 8;  // warps of a block that work few rows
 // q: bf16 (d, H, N) with boxes of 64 columns x group heads x tp tokens; k, v: the page pools as (64, 128 rows, d / 64,
 // num_pages * Hkv) in boxes of whole pages, k16, v16: of `step` rows.
 struct PrefixMaps {

@@ -12,20 +12,25 @@
 // that have several.
 //
 // The work is a list of items: (K/V head, rows, keys), rows being (token, query head) pairs, `group` of them
-// per token.  A request is few (up to 8, 16, 32 or 64 rows: a decoding request, a few drafted tokens), big
-// (from kBigRows rows on: a prompt chunk) or between.  The items are
+// per token.  A request is few (up to 8 rows, or 16 at d = 64: a decoding request, a few drafted tokens), big (from
+// kBigRows rows on: a prompt chunk) or between.  The items are
 //   the prefix for blocks of up to 256 rows of any requests (a key tile is loaded once for all of them),
 //   the own keys of a few or between request,
 //   the prefix and then the own keys of up to 256 rows of a big request (it fills row tiles by itself, so its
-//   rows need no second item and no join).
+//   rows need no second item and no join: 130 us against 148 for a batch of prompt chunks).
 // There are two kinds of them, and every block works one of them:
 //   many rows: up to 256 rows on tcgen05 products, keys in tiles of 128 (bound by the tensor core);
 //   few rows:  the items of few requests (and the prefix, when all rows together are few) on warp-level
-//              products, keys in steps of 16 or 32, by teams of one, two or four warps (bound by loading the keys).
+//              products, keys in steps of 16 or 32, by the block's eight warps one by one (bound by loading the keys).
 // The items of a kind stand on a line, a key tile or step and an item taking so many places each, and the
-// kind's workers (blocks, or teams) get equal stretches of it: worker w the tiles whose places begin in
+// kind's workers (blocks, or warps) get equal stretches of it: worker w the tiles whose places begin in
 // [w Q, (w + 1) Q).  So all workers have the same share whatever the lengths, and at most two items of a
 // worker are cut, its first and its last.  The blocks are shared out between the kinds by their cost.
+//
+// What a call takes (GB300, keys not in L2): one request behind 256 keys 12 us, which is two kernels' latency (the work's
+// layout 3, a piece 5, the boundary between the kernels 1.5, the join 3); 64 requests with up to 1 024 own keys behind 4 096
+// shared ones 39 us (151 MB: 22 us at the measured copy rate); 128 behind 32 768 76 us (69 GFLOP: 36 us at the measured
+// tensor rate, and 40 us of loading); 8 prompt chunks of up to 600 tokens 130 us (125 GFLOP: 65 us).
 #include <limits.h>
 #include <math.h>
 
@@ -41,7 +46,7 @@ static __device__ unsigned int g_prefix_status;  // kStatus* bits
 // shares of six batches (64 to 256 requests, prefixes of 1 024 to 32 768 keys): a place of either kind on one SM; what the
 // many-row kind takes longer at its ends; the part of the loading time that its work is to fill; the rate of loading.
 constexpr unsigned int kItemCost = 20, kTileCost128 = 6, kTileCost256 = 8;
-constexpr unsigned int kFewItemCost = 4, kFewLeast = 4;  // (at least kFewLeast places for a team)
+constexpr unsigned int kFewItemCost = 4, kFewLeast = 4;  // (at least kFewLeast places for a warp)
 constexpr float kManyTime = 0.19f, kFewTime = 0.12f, kManyStart = 2.6f, kManyShare = 0.4f, kLoadRate = 6.5e6f;
 constexpr int kBigRows = 128;   // rows from which a request is big
 constexpr int kMaxFlags = 1024; // row blocks of the batch whose need of the prefix is looked at one by one
@@ -226,13 +231,14 @@ __device__ __forceinline__ Plan make_plan(const PrefixParams& p, Layout& s, vola
   l.many = l.total[0] == 0 ? 0 : l.total[1] == 0 ? p.ctas : max(1, min(p.ctas - 1, __float2int_rn(m)));
   l.share[0] = max(1u, (l.total[0] + max(l.many, 1) - 1) / max(l.many, 1));
   // Only the prefix on the many-row line: every item in the same whole number of stretches, so that the row blocks of a
-  // head come to a key tile at the same time and all but the first read it from L2.
+  // head come to a key tile at the same time and all but the first read it from L2 (76 against 85 us for 128 requests
+  // behind 32 768 keys, 71 against 77 for 256 behind 16 384).
   const int items = p.Hkv * l.items, each = items == 0 ? 0 : (2 * l.many + items) / (2 * items);
   if (l.total[0] > 0 && l.total[0] == l.lead[0] && each > 0 && each * items <= p.ctas - (l.total[1] > 0)) {
     l.many = each * items;
     l.share[0] = (l.total[0] / items + each - 1) / each;
   }
-  const unsigned int teams = max(1, (p.ctas - l.many) * p.teams);
+  const unsigned int teams = max(1, (p.ctas - l.many) * kTeams);
   l.share[1] = max(kFewLeast, (l.total[1] + teams - 1) / teams);
   __syncthreads();
   // the last thread with requests whose key is not above x
@@ -252,9 +258,9 @@ __device__ __forceinline__ Plan make_plan(const PrefixParams& p, Layout& s, vola
   l.few = static_cast<int>(blockIdx.x) >= l.many;
   l.worker = l.few ? blockIdx.x - l.many : blockIdx.x;
   const int kind = l.few;
-  if (tid < (kind ? p.teams : 1)) {  // the request that holds this block's worker's first own place
+  if (tid < (kind ? kTeams : 1)) {  // the request that holds this block's worker's first own place
     const unsigned long long at =
-        static_cast<unsigned long long>(kind ? l.worker * p.teams + tid : l.worker) * l.share[kind];
+        static_cast<unsigned long long>(kind ? l.worker * kTeams + tid : l.worker) * l.share[kind];
     if (at < l.total[kind]) {
       const unsigned int x = max(static_cast<unsigned int>(at), l.lead[kind]);
       auto place = [&](int t) { return static_cast<unsigned int>(s.cum[t] >> (32 * kind)); };
@@ -1002,29 +1008,30 @@ __device__ __forceinline__ void many_rows(const CUtensorMap& tmQ, const CUtensor
 }
 
 // ---------------------------------------------------------------- few rows
-// A team of R warps works items of up to 8 NT R rows, warp t of it rows 8 NT t .., keys in steps of 16 or 32.  A 128-row
-// tcgen05 tile would spend its softmax on empty rows; here the products are warp-level and transposed, keys (or
-// columns of V) as the 16 rows of mma.sync m16n8k16 and query rows as its 8 columns:
+// A warp works items of up to 8 NT rows, keys in steps of 16 or 32 (8 KB of K and V).  A 128-row tcgen05 tile would spend
+// its softmax on empty rows; here the products are warp-level and transposed, keys (or columns of V) as the 16 rows of
+// mma.sync m16n8k16 and query rows as its 8 columns:
 //   S^T (16 keys x 8 rows) = K Q^T,   O^T (16 columns x 8 rows) += V^T P^T,
 // so that eight rows cost one product per 16 x 16 of K and V and half the accumulators that rows as M would.  P^T
 // becomes the second product's operand by an 8 x 8 transpose in registers (movmatrix); the softmax state stays in
-// registers too, and a warp meets no other but at its team's ring of K/V steps, which the team's first warp fills by
-// TMA.  The 8 / R teams of a block are independent, so one's item start (request, table and query loads) and end hide
-// behind the others' keys in flight.
-constexpr int FEW_WARPS = 8;
-
-template <int D, int R>
+// registers too, and a warp meets no other: each fills its own ring of K/V steps by TMA, and one's item start (request,
+// table and query loads) and end hide behind the others' keys in flight.
+//
+// Bound by loading the keys with 8 rows: 32 requests with 1 000 to 32 768 keys (2.2 GB) take 340 us, 6.5 TB/s, 96 % of the
+// measured copy rate.  With 16 rows the warp-level products and exponentials take twice as long and are the bound at d = 128, and the
+// tcgen05 kind is better from some 100 keys on (64 requests of 16 rows: 54 against 81 us with 1 024 keys, 31 against 35 with
+// 200, 24 against 18 with 20).  At d = 64 a step has half the work per key: 12 rows take 60 us against 76 with 1 000 keys and 16
+// against 31 with 40, but 24 rows, as two warps, 91 against 77.  So the few are up to 8 rows at d = 128, up to 16 at d = 64.
+template <int D>
 struct FLayout {
   static constexpr int STEP = kStep<D>;
   static constexpr int STEP_BYTES = 2 * STEP * D * 2;  // K, then V; 64 columns per box of STEP rows x 128 bytes
   static constexpr int BOX = STEP * 128;
-  static constexpr int TEAMS = FEW_WARPS / R;
-  static constexpr int FIT = PLayout<D>::XCH_OFF / (TEAMS * STEP_BYTES);
-  static constexpr int STAGES = FIT < 12 ? FIT : 12;
-  static constexpr int BAR_OFF = PLayout<D>::END;  // full[TEAMS][STAGES]; empty[TEAMS][STAGES] where R > 1
-  static constexpr int NUM_BARS = (R > 1 ? 2 : 1) * TEAMS * STAGES;
+  static constexpr int STAGES = PLayout<D>::XCH_OFF / (kTeams * STEP_BYTES);
+  static constexpr int BAR_OFF = PLayout<D>::END;  // full[kTeams][STAGES]
+  static constexpr int NUM_BARS = kTeams * STAGES;
   static_assert(STAGES >= 3 && BAR_OFF % 8 == 0 && BAR_OFF + NUM_BARS * 8 <= NEED_OFF && NUM_BARS <= THREADS, "barriers");
-  static_assert(TEAMS * STAGES * STEP_BYTES <= PLayout<D>::XCH_OFF, "the rings reach into what follows them");
+  static_assert(kTeams * STAGES * STEP_BYTES <= PLayout<D>::XCH_OFF, "the rings reach into what follows them");
 };
 
 // Warp-level products: D (16 x 8) += A (16 x 16) B (16 x 8), bf16 in, fp32 out.
@@ -1138,26 +1145,24 @@ struct FewWalk {
   }
 };
 
-template <int D, int NT, int R>
+template <int D, int NT>
 __device__ __forceinline__ void few_rows(const CUtensorMap& tmK, const CUtensorMap& tmV, const PrefixParams& p,
                                          const Plan& l, uint8_t* smem) {
-  using L = FLayout<D, R>;
+  using L = FLayout<D>;
   const uint32_t sbase = smem_u32(smem);
   const int warp = uni(threadIdx.x / 32), lane = threadIdx.x % 32;
-  const int team = warp / R, mt = warp % R;
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + PLayout<D>::MISC_OFF + 4);
-  if (warp >= FEW_WARPS) return;
+  if (warp >= kTeams) return;
   const Waiter W{abort_flag, p.timeout_ns, &g_prefix_status};
-  const uint32_t ring = sbase + team * L::STAGES * L::STEP_BYTES;
-  const uint32_t bar_full = sbase + L::BAR_OFF + 8 * team * L::STAGES;
-  const uint32_t bar_empty = bar_full + 8 * L::TEAMS * L::STAGES;
-  const int worker = uni(l.worker) * L::TEAMS + team;
+  const uint32_t ring = sbase + warp * L::STAGES * L::STEP_BYTES;
+  const uint32_t bar_full = sbase + L::BAR_OFF + 8 * warp * L::STAGES;
+  const int worker = uni(l.worker) * kTeams + warp;
   const unsigned int total = uni(l.total[1]), share = uni(l.share[1]);
   const unsigned long long from = static_cast<unsigned long long>(worker) * share;
   if (from >= total) return;
   const unsigned int x0 = static_cast<unsigned int>(from);
   const unsigned int x1 = static_cast<unsigned int>(min(from + share, static_cast<unsigned long long>(total)));
-  const volatile Begin* begin = reinterpret_cast<const volatile Begin*>(smem + BEGIN_OFF) + team;
+  const volatile Begin* begin = reinterpret_cast<const volatile Begin*>(smem + BEGIN_OFF) + warp;
   const int first = uni(begin->b);
   const unsigned int first_place = uni(begin->c0);
 
@@ -1167,7 +1172,7 @@ __device__ __forceinline__ void few_rows(const CUtensorMap& tmK, const CUtensorM
   FewPiece q, lp, ahead;
   int lj = 0, issued = 0, lstage = 0, page = 0, base = 0, ahead_page = 0;
   walk.start(p, l, x0, x1, first, first_place);
-  bool have = walk.next(p, lane, q), more = mt == 0, any = have;
+  bool have = walk.next(p, lane, q), more = true, any = have;
   auto ask = [&] {  // for the piece ahead's pages and query rows
     const int first_tile = ahead.j0 / (kPage / L::STEP) & ~31;
     ahead_page = first_tile + lane < ahead.entries ? ahead.table[first_tile + lane] : 0;
@@ -1179,18 +1184,16 @@ __device__ __forceinline__ void few_rows(const CUtensorMap& tmK, const CUtensorM
       if (D == 128) asm volatile("prefetch.global.L2 [%0];" ::"l"(src + 64));
     }
   };
-  if (mt == 0) {
-    load = walk;
-    ahead = q;
-    lp.j1 = 0;
-    if (any) ask();
-  }
+  load = walk;
+  ahead = q;
+  lp.j1 = 0;
+  if (any) ask();
   const uint64_t once = l2_policy_evict_first();
-  auto fill = [&]() -> bool {  // loads the stretch's next step, if there is one
+  auto fill = [&] {  // loads the stretch's next step, if there is one
     if (lj >= lp.j1) {
       if (!any) {
         more = false;
-        return true;
+        return;
       }
       lp = ahead;
       lj = lp.j0;
@@ -1208,22 +1211,17 @@ __device__ __forceinline__ void few_rows(const CUtensorMap& tmK, const CUtensorM
       if (lane == 0) atomicOr(&g_prefix_status, kStatusBadPage);
       pg = p.num_pages;
     }
-    if (R > 1 && issued >= L::STAGES &&
-        !wait_all(W, bar_empty + 8 * lstage, (issued / L::STAGES - 1) & 1))
-      return false;
     load_rows2_elect(ring + lstage * L::STEP_BYTES, L::STEP_BYTES / 2, &tmK, &tmV, (lj % (kPage / L::STEP)) * L::STEP,
                      pg * p.Hkv + lp.g, bar_full + 8 * lstage, once);
     ++lj;
     ++issued;
     if (++lstage == L::STAGES) lstage = 0;
-    return true;
   };
-  bool ok = true;
-  // one stage behind when other warps read the ring too, so as not to wait for the slowest at every step
 #pragma unroll 1
-  for (int t = 0; ok && more && t < L::STAGES - (R > 1); ++t) ok = fill();
+  for (int t = 0; more && t < L::STAGES; ++t) fill();
+  bool ok = true;
 
-  const int row0 = mt * 8 * NT, c0 = 2 * (lane & 3);  // this warp's first row; a thread's columns of a product, c0 and c0 + 1
+  const int c0 = 2 * (lane & 3);  // a thread's columns of a product are c0 and c0 + 1
   const float sl2 = p.scale_log2;
   // shared-memory words of a 16 x 16 block of K (rows as they are) and of V (transposed), within a step
   const int k_row = lane & 15, v_row = ((lane >> 4) << 3) + (lane & 7);
@@ -1242,7 +1240,7 @@ __device__ __forceinline__ void few_rows(const CUtensorMap& tmK, const CUtensorM
     int lim[NT][2], lim_min = q.keys;  // keys the thread's rows see (rows past the last one: all, they are not used)
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
-      const int r = row0 + 8 * t + lane / 4, tok = r / p.group;
+      const int r = 8 * t + lane / 4, tok = r / p.group;
       const __nv_bfloat16* src = p.q + (static_cast<size_t>(q.t0 + tok) * p.H + q.g * p.group + (r - tok * p.group)) * D + c0;
 #pragma unroll
       for (int kk = 0; kk < D / 16; ++kk) {
@@ -1251,7 +1249,7 @@ __device__ __forceinline__ void few_rows(const CUtensorMap& tmK, const CUtensorM
       }
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        const int row = row0 + 8 * t + c0 + e;
+        const int row = 8 * t + c0 + e;
         lim[t][e] = row < q.rows ? min(q.keys, q.lim0 + q.step * (row / p.group)) : q.keys;
         lim_min = min(lim_min, lim[t][e]);
       }
@@ -1388,9 +1386,8 @@ __device__ __forceinline__ void few_rows(const CUtensorMap& tmK, const CUtensorM
         }
       }
       __syncwarp();
-      if (R > 1 && lane == 0) mbar_arrive(bar_empty + 8 * stage);
       if (++stage == L::STAGES) stage = 0;
-      if (more && !(ok = fill())) break;
+      if (more) fill();
     }
     if (!ok) break;
     const size_t slab = few_slab(p, worker, q.dst == kDstSlab1);
@@ -1400,7 +1397,7 @@ __device__ __forceinline__ void few_rows(const CUtensorMap& tmK, const CUtensorM
       for (int e = 0; e < 2; ++e) {
 #pragma unroll
         for (int w = 4; w <= 16; w <<= 1) lw[t][e] += __shfl_xor_sync(0xffffffffu, lw[t][e], w);
-        const int r = row0 + 8 * t + c0 + e;
+        const int r = 8 * t + c0 + e;
         if (r >= q.rows) continue;
         const float inv = lr[t][e] == 0.f ? 0.f : 1.f / lr[t][e];  // no key seen: O = 0 (a NaN sum stays one)
         const RowOut to = row_out<D>(p, q.dst, slab, q.g, q.t0, r);
@@ -1421,7 +1418,7 @@ __device__ __forceinline__ void few_rows(const CUtensorMap& tmK, const CUtensorM
         }
       }
   }
-  if (!ok && mt == 0)  // let every copy already issued land before the block exits
+  if (!ok)  // let every copy already issued land before the block exits
 #pragma unroll 1
     for (int t = 0; t < L::STAGES && t < issued; ++t)
       drain_all(W, bar_full + 8 * t, ((issued - 1 - t) / L::STAGES) & 1);
@@ -1432,7 +1429,7 @@ __device__ __forceinline__ void few_rows(const CUtensorMap& tmK, const CUtensorM
 // against 61 us for 64 requests behind 16 384 keys, 73 against 84 for 256).  For the same reason loops of run-time length
 // stay rolled, and the many-row code comes first: what is further behind the kernel's start arrives later (80 against
 // 82 us for 128 requests behind 32 768 keys).
-template <int D, int NT, int R>
+template <int D, int NT>
 __global__ void __launch_bounds__(THREADS, 1)
 fa_prefix_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                  const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmK16,
@@ -1450,10 +1447,10 @@ fa_prefix_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
   if (threadIdx.x < kMaxFlags / 32) need[threadIdx.x] = 0;
   // both kinds' barriers and the Tensor Memory: which kind the block works is known only after the wait
   using M = PLayout<D>;
-  using F = FLayout<D, R>;
+  using F = FLayout<D>;
   const uint32_t sbase = smem_u32(smem);
   if (threadIdx.x < M::NUM_BARS) M::init(sbase, threadIdx.x);
-  if (threadIdx.x < F::NUM_BARS) mbar_init(sbase + F::BAR_OFF + 8 * threadIdx.x, threadIdx.x < F::TEAMS * F::STAGES ? 1 : R);
+  if (threadIdx.x < F::NUM_BARS) mbar_init(sbase + F::BAR_OFF + 8 * threadIdx.x, 1);
   if (threadIdx.x == 0) *reinterpret_cast<volatile int*>(smem + M::MISC_OFF + 4) = 0;
   fence_mbar_init();
   const int warp = uni(threadIdx.x / 32);
@@ -1469,7 +1466,7 @@ fa_prefix_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
   if (!l.few)
     many_rows<D>(tmQ, tmK, tmV, p, l, smem);
   else
-    few_rows<D, NT, R>(tmK16, tmV16, p, l, smem);
+    few_rows<D, NT>(tmK16, tmV16, p, l, smem);
   tc_fence_before();
   __syncthreads();
   if (warp == MMA_WARP) {
@@ -1489,7 +1486,7 @@ struct Parts {
   __device__ __forceinline__ void locate(const PrefixParams& p, const Plan& l) {
     share = few ? l.share[1] : l.share[0];
     // (places past the last worker come only of a cu_new that decreases, which is reported)
-    const unsigned int last = (few ? p.ctas * p.teams : p.ctas) - 1;
+    const unsigned int last = (few ? p.ctas * kTeams : p.ctas) - 1;
     const unsigned int w0 = min(it.worker(0, share), last), w1 = min(it.worker(it.units - 1, share), last);
     first = static_cast<int>(w0);
     count = w1 < w0 ? 1 : static_cast<int>(w1 - w0) + 1;
@@ -1664,35 +1661,36 @@ __global__ void __launch_bounds__(W > 1 ? 32 * W : kJoinThreads) fa_prefix_join_
   }
 }
 
-template <int D, int NT, int R>
+template <int D, int NT>
 static cudaError_t launch(const PrefixMaps& t, const PrefixParams& p, cudaStream_t stream) {
   static bool attr_set[64] = {};
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev < 64 && !attr_set[dev]) {
-    e = cudaFuncSetAttribute(fa_prefix_kernel<D, NT, R>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
+    e = cudaFuncSetAttribute(fa_prefix_kernel<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
     if (e != cudaSuccess) return e;
     attr_set[dev] = true;
   }
   const long long rows = static_cast<long long>(p.N) * p.H;
-  const bool wide = rows < 4 * p.ctas;  // few rows: the join takes a block for each
+  // few rows, perhaps of many parts: the join takes a block for each (35 against 57 us for one request with 30 000 keys)
+  const bool wide = rows < 4 * p.ctas;
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.stream = stream;
   cfg.attrs = attr;
-  // Launched early only when there are few rows (14.0 against 14.8 us for one request).  Blocks that start as the
+  // Launched early only when there are few rows (12.5 against 13.5 us for one request).  Blocks that start as the
   // preceding kernel's end land on the SMs in any order, and the last block numbers, which stream the requests' own keys,
-  // gather on neighbouring SMs and starve the others there (86 -> 103 us for 128 requests behind 32 768 keys).
+  // gather on neighbouring SMs and starve the others there (76 -> 88 us for 128 requests behind 32 768 keys).
   cfg.numAttrs = wide ? 1 : 0;
   cfg.gridDim = dim3(p.ctas);
   cfg.blockDim = dim3(THREADS);
   cfg.dynamicSmemBytes = SMEM_BYTES;
-  if ((e = cudaLaunchKernelEx(&cfg, fa_prefix_kernel<D, NT, R>, t.q, t.k, t.v, t.k16, t.v16, p)) != cudaSuccess) return e;
-  // a warp a row while the SMs hold as many (8 lanes a row: 44 -> 48 us for 64 requests behind 16 384 keys); eight lanes
-  // beyond (160 -> 140 us for a batch of prompt chunks with 77 568 rows), 12 blocks per SM at most
+  if ((e = cudaLaunchKernelEx(&cfg, fa_prefix_kernel<D, NT>, t.q, t.k, t.v, t.k16, t.v16, p)) != cudaSuccess) return e;
+  // a warp a row while the SMs hold as many (42.2 us for 64 requests behind 4 096 keys, 43.6 with eight lanes a row); eight
+  // lanes beyond (130 against 149 us for prompt chunks with 77 568 rows), 12 blocks per SM at most
   const int lanes = rows <= 48ll * p.ctas ? 32 : 8;
   const long long blocks = (rows * lanes + kJoinThreads - 1) / kJoinThreads;
   // not launched early: its blocks would gather on the SMs whose attention block ends first (46 -> 63 us for 64
@@ -1707,14 +1705,8 @@ static cudaError_t launch(const PrefixMaps& t, const PrefixParams& p, cudaStream
 }
 
 cudaError_t launch_fa_fwd_prefix(int d, const PrefixMaps& t, const PrefixParams& p, cudaStream_t stream) {
-#define FA_LAUNCH(D)                                                                                    \
-  return p.few_rows == 8    ? launch<D, 1, 1>(t, p, stream)                                             \
-         : p.few_rows == 16 ? launch<D, 2, 1>(t, p, stream)                                             \
-         : p.few_rows == 32 ? launch<D, 2, 2>(t, p, stream)                                             \
-                            : launch<D, 2, 4>(t, p, stream)
-  if (d == 64) FA_LAUNCH(64);
-  FA_LAUNCH(128);
-#undef FA_LAUNCH
+  if (d == 128) return launch<128, 1>(t, p, stream);
+  return p.few_rows == 8 ? launch<64, 1>(t, p, stream) : launch<64, 2>(t, p, stream);
 }
 
 unsigned int prefix_page_cost() { return kTileCost256; }
