@@ -460,7 +460,7 @@ struct __align__(16) Piece {
   int g;             // K/V head
   int dst;           // where the part goes: kDst*
   int tile_rows;     // rows of a full row tile
-  int pad;
+  int turn;          // the slot that begins a piece of one row tile
 };
 
 template <int D>
@@ -519,7 +519,7 @@ __device__ __forceinline__ void many_rows(const CUtensorMap& tmQ, const CUtensor
     const unsigned int share = uni(l.share[0]), total = uni(l.total[0]), lead = uni(l.lead[0]);
     const unsigned int x0 = uni(l.worker) * share, x1 = min(total, x0 + share);
     const uint64_t once = l2_policy_evict_first();  // (see fa_prefix_kernel)
-    int stage = 0, np = 0;
+    int stage = 0, np = 0, turn = 0;
     uint32_t phase = 0, issued = 0, issued_parity = 0;
     bool ok = true;
     // page numbers of 32 tiles of one table row, one per lane (the row of a request may also be the prefix's)
@@ -557,7 +557,7 @@ __device__ __forceinline__ void many_rows(const CUtensorMap& tmQ, const CUtensor
         const int* src = reinterpret_cast<const int*>(&q);
         volatile int* dst = reinterpret_cast<volatile int*>(pieces + s);
 #pragma unroll
-        for (int w = 0; w < 15; ++w) dst[w] = src[w];
+        for (int w = 0; w < 16; ++w) dst[w] = src[w];
         mbar_arrive(bar_piece_full + 8 * s);
       }
       __syncwarp();
@@ -571,8 +571,12 @@ __device__ __forceinline__ void many_rows(const CUtensorMap& tmQ, const CUtensor
       Piece q;
       q.n = j1 - j0;
       q.mode = count > p.tp ? 2 : 1;
-      q.n0 = q.mode == 2 ? max(0, min(tiles0, j1) - j0) : (q.n + 1) / 2;
-      q.n1 = q.mode == 2 ? q.n : q.n / 2;
+      // pieces of a single tile take the slots in turn: one's end overlaps the next one's scores and softmax (62 against
+      // 73 us for 300 requests of 32 rows with 100 keys)
+      q.turn = q.n == 1 && q.mode == 1 ? turn : 0;
+      if (q.n == 1 && q.mode == 1) turn ^= 1;
+      q.n0 = q.mode == 2 ? max(0, min(tiles0, j1) - j0) : (q.n + 1 - q.turn) / 2;
+      q.n1 = q.mode == 2 ? q.n : (q.n + q.turn) / 2;
       q.j0 = j0;
       q.ptiles = ptiles;
       q.keys = keys;
@@ -661,7 +665,7 @@ __device__ __forceinline__ void many_rows(const CUtensorMap& tmQ, const CUtensor
     if (ok) {
       Piece q;
       q.mode = 0;
-      q.n = q.n0 = q.n1 = q.j0 = q.ptiles = q.keys = q.lim0 = q.step = q.t0 = q.rows0 = q.rows1 = q.g = q.dst = q.tile_rows = 0;
+      q.n = q.n0 = q.n1 = q.j0 = q.ptiles = q.keys = q.lim0 = q.step = q.t0 = q.rows0 = q.rows1 = q.g = q.dst = q.tile_rows = q.turn = 0;
       ok = publish(q);
     }
     if (!ok) {  // let every copy already issued land before the block exits
@@ -749,6 +753,7 @@ __device__ __forceinline__ void many_rows(const CUtensorMap& tmQ, const CUtensor
       q.j0 = uni(pieces[s].j0);
       q.keys = uni(pieces[s].keys);
       q.ptiles = uni(pieces[s].ptiles);
+      q.turn = uni(pieces[s].turn);
       __syncwarp();
       if (lane == 0) mbar_arrive(bar_piece_empty + 8 * s);
       if (q.mode == 0) break;
@@ -759,13 +764,13 @@ __device__ __forceinline__ void many_rows(const CUtensorMap& tmQ, const CUtensor
 #pragma unroll 1
         for (int x = 0; ok && x < min(q.n, 2); ++x) {
           if (!(ok = take(ks))) break;
-          issue_s(x, 0, ks);
+          issue_s(x ^ q.turn, 0, ks);
           if (x + 1 == q.n) mma_commit_elect(bar_q_empty);
           mma_commit_elect(bar_kv_empty + 8 * ks);
         }
 #pragma unroll 1
         for (int x = 0; ok && x < q.n; ++x) {
-          const int slot = x & 1;
+          const int slot = (x & 1) ^ q.turn;
           if (!(ok = take(vs))) break;
           const int steps = value_steps(q, q.j0 + x, vs);
           if (!(ok = ready_pv(slot, x < 2))) break;
@@ -855,7 +860,7 @@ __device__ __forceinline__ void many_rows(const CUtensorMap& tmQ, const CUtensor
         if (live_warp) {
           uint32_t sr[BN];
           tmem_ld128_wait(t_s, sr);
-          const int tile = j0 + (mode == 1 ? 2 * x + i : x);
+          const int tile = j0 + (mode == 1 && n > 1 ? 2 * x + i : x);
           const int left = tile < ptiles ? lim_p - tile * BN : lim - (tile - ptiles) * BN;  // keys of the tile the row sees
           if (__any_sync(0xffffffffu, left < BN)) {
 #pragma unroll
