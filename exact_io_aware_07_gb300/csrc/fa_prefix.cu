@@ -5,7 +5,9 @@
 // row are cut into parts that run on different SMs, each giving (O_p, LSE_p); a row's parts join as
 //   LSE = ln sum_p e^LSE_p,   O = sum_p e^(LSE_p - LSE) O_p,
 // which is the softmax over all keys, so that the prefix can be worked once for the rows of the whole
-// batch and the own keys request by request.
+// batch and the own keys request by request.  Scores, maxima, sums and parts are fp32.  The weights e^(s_j - m) are
+// rounded to bf16 for the product with V, the operand type of the tensor core; the sum that divides O is that of the
+// rounded weights, so that the roundings move O by at most 2^-8 of its values' spread, not of their size.  O is rounded once more.
 //
 // Two kernels on the stream: fa_prefix_kernel, one block per SM, lays out the work from the device lengths
 // (every block for itself) and works its share of the keys; fa_prefix_join_kernel joins the parts of the rows
