@@ -527,6 +527,44 @@ def test_wrappers_on_a_given_stream():
     assert fa.fa_device_status() == 0
 
 
+@pytest.mark.parametrize("d,H,Hkv,prefix,own,new", [
+    (64, 4, 4, 300, [700, 5, 129], [1, 2, 1]),      # few rows only
+    (64, 12, 1, 300, [700, 40], [1, 1]),            # few rows of two tiles of eight
+    (128, 8, 2, 500, [900, 64, 300], [150, 20, 1]),  # every kind
+    (128, 6, 2, 0, [2000, 1], [1, 1]),              # rows cut into many parts
+])
+def test_nothing_else_is_written(d, H, Hkv, prefix, own, new):
+    """Outputs and a workspace of exactly the asked size inside larger buffers: what surrounds them and every input stay."""
+    import torch
+
+    import exact_io_aware_07_gb300 as fa
+
+    b = Batch(d, H, Hkv, prefix, own, new, pad=2, seed=39)
+    a = b.device()
+    before = {k: v.clone() for k, v in a.items() if torch.is_tensor(v) and k not in ("o", "lse")}
+    n = a["q"].shape[0]
+    size = fa.fa_fwd_prefix_paged_workspace_bytes(n, len(own), H, Hkv, d)
+    room = 4096
+
+    def inside(numel, dtype, fill):
+        buf = torch.full((numel + 2 * room,), fill, dtype=dtype, device="cuda")
+        return buf, buf[room:room + numel]
+
+    ws_buf, ws = inside(size, torch.uint8, 0xA5)
+    o_buf, o = inside(n * H * d, torch.bfloat16, 7.0)
+    lse_buf, lse = inside(n * H, torch.float32, 7.0)
+    a.update(o=o.view(n, H, d), lse=lse.view(n, H))
+    for _ in range(2):
+        fa.fa_fwd_prefix_paged(**a, causal=True, scale=d ** -0.5, workspace=ws)
+    torch.cuda.synchronize()
+    assert fa.fa_device_status() == 0
+    b.check(a["o"], a["lse"], label="inside larger buffers")
+    for buf, fill in ((ws_buf, 0xA5), (o_buf, 7.0), (lse_buf, 7.0)):
+        assert (buf[:room] == fill).all() and (buf[-room:] == fill).all()
+    for k, v in before.items():
+        assert torch.equal(v.view(torch.uint8), a[k].view(torch.uint8)), k
+
+
 def test_decreasing_cu_new_is_reported():
     import exact_io_aware_07_gb300 as fa
 
