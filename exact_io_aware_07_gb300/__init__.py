@@ -153,7 +153,7 @@ def _stream_handle(stream):
     import torch
 
     if stream is None:  # the raw handle: making a Stream object of it takes 2.5 us
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -286,11 +286,12 @@ def _check_pools(k_pages, v_pages):
     """(num_pages, Hkv, d) of two page pools."""
     import torch
 
-    shape = k_pages.shape
-    for name, t in (("k_pages", k_pages), ("v_pages", v_pages)):
-        if t.dtype is not torch.bfloat16 or t.dim() != 4 or not t.is_contiguous():
-            raise ValueError(f"{name} must be a contiguous bf16 4-D tensor")
-    if shape[2] != PAGE or v_pages.shape != shape:
+    shape, bf16 = k_pages.shape, torch.bfloat16
+    if not (k_pages.dtype is bf16 and v_pages.dtype is bf16 and len(shape) == 4 and shape[2] == PAGE
+            and v_pages.shape == shape and k_pages.is_contiguous() and v_pages.is_contiguous()):
+        for name, t in (("k_pages", k_pages), ("v_pages", v_pages)):
+            if t.dtype is not bf16 or t.dim() != 4 or not t.is_contiguous():
+                raise ValueError(f"{name} must be a contiguous bf16 4-D tensor")
         raise ValueError(f"pages must be (num_pages, Hkv, {PAGE}, d)")
     return shape[0], shape[1], shape[3]
 
@@ -309,16 +310,21 @@ def fa_page_plan(ctx_lens, new_lens, free_pages, free_head, block_table, seq_len
         raise ValueError("block_table must be (B, max_pages), slot_map and free_pages one-dimensional")
     B, max_pages = table = block_table.shape
     tokens, free = slot_map.shape, free_pages.shape
-    i32, batch = torch.int32, (B,)
-    _check_int("ctx_lens", ctx_lens, batch, i32)
-    _check_int("new_lens", new_lens, batch, i32)
-    _check_int("free_pages", free_pages, free, i32)
-    _check_int("free_head", free_head, (1,), i32)
-    _check_int("block_table", block_table, table, i32)
-    _check_int("seq_lens", seq_lens, batch, i32)
-    _check_int("cu_new", cu_new, (B + 1,), i32)
-    _check_int("slot_map", slot_map, tokens, i32)
-    _check_int("free_head_out", free_head_out, (1,), i32)
+    i32, batch, one = torch.int32, (B,), (1,)
+    # (written out: nine calls would take a fourth of a small plan's time)
+    if not (ctx_lens.dtype is i32 and new_lens.dtype is i32 and free_pages.dtype is i32 and free_head.dtype is i32
+            and block_table.dtype is i32 and seq_lens.dtype is i32 and cu_new.dtype is i32 and slot_map.dtype is i32
+            and free_head_out.dtype is i32 and ctx_lens.shape == batch and new_lens.shape == batch
+            and free_head.shape == one and seq_lens.shape == batch and cu_new.shape == (B + 1,)
+            and free_head_out.shape == one and ctx_lens.is_contiguous() and new_lens.is_contiguous()
+            and free_pages.is_contiguous() and block_table.is_contiguous() and seq_lens.is_contiguous()
+            and cu_new.is_contiguous() and slot_map.is_contiguous()):
+        for name, t, shape in (("ctx_lens", ctx_lens, batch), ("new_lens", new_lens, batch),
+                               ("free_pages", free_pages, free), ("free_head", free_head, one),
+                               ("block_table", block_table, table), ("seq_lens", seq_lens, batch),
+                               ("cu_new", cu_new, (B + 1,)), ("slot_map", slot_map, tokens),
+                               ("free_head_out", free_head_out, one)):
+            _check_int(name, t, shape, i32)
     code = load_library().fa_page_plan(ctx_lens.data_ptr(), new_lens.data_ptr(), free_pages.data_ptr(),
                                        free_head.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(),
                                        cu_new.data_ptr(), slot_map.data_ptr(), free_head_out.data_ptr(), B, max_pages,
@@ -380,22 +386,25 @@ def fa_fwd_prefix_paged(q, k_pages, v_pages, prefix_table, prefix_len: int, bloc
     import torch
 
     num_pages, Hkv, d = _check_pools(k_pages, v_pages)
-    rows = q.shape
-    for name, t in (("q", q), ("o", o)):
-        if t.dtype is not torch.bfloat16 or t.dim() != 3 or t.shape[2] != d or not t.is_contiguous():
-            raise ValueError(f"{name} must be a contiguous bf16 (N, H, d) tensor")
-    if o.shape != rows:
+    rows, table, i32, bf16 = q.shape, block_table.shape, torch.int32, torch.bfloat16
+    if not (q.dtype is bf16 and o.dtype is bf16 and len(rows) == 3 and rows[2] == d and o.shape == rows
+            and q.is_contiguous() and o.is_contiguous()):
+        for name, t in (("q", q), ("o", o)):
+            if t.dtype is not bf16 or t.dim() != 3 or t.shape[2] != d or not t.is_contiguous():
+                raise ValueError(f"{name} must be a contiguous bf16 (N, H, d) tensor")
         raise ValueError("q and o must have the same shape")
     N, H, _ = rows
-    if lse.dtype is not torch.float32 or lse.shape != (N, H) or not lse.is_contiguous():
+    if lse.dtype is not torch.float32 or lse.shape != rows[:2] or not lse.is_contiguous():
         raise ValueError("lse must be a contiguous fp32 (N, H) tensor")
-    if block_table.dim() != 2:
+    if len(table) != 2:
         raise ValueError("block_table must be (B, max_pages)")
-    B, max_pages = table = block_table.shape
-    i32 = torch.int32
-    _check_int("block_table", block_table, table, i32)
-    _check_int("seq_lens", seq_lens, (B,), i32)
-    _check_int("cu_new", cu_new, (B + 1,), i32)
+    B, max_pages = table
+    if not (block_table.dtype is i32 and seq_lens.dtype is i32 and cu_new.dtype is i32 and seq_lens.shape == (B,)
+            and cu_new.shape == (B + 1,) and block_table.is_contiguous() and seq_lens.is_contiguous()
+            and cu_new.is_contiguous()):
+        _check_int("block_table", block_table, table, i32)
+        _check_int("seq_lens", seq_lens, (B,), i32)
+        _check_int("cu_new", cu_new, (B + 1,), i32)
     if prefix_table is not None:
         _check_int("prefix_table", prefix_table, (prefix_table.numel(),), i32)
     if prefix_len > 0 and (prefix_table is None or prefix_table.numel() * PAGE < prefix_len):

@@ -94,7 +94,8 @@ fa_status current_device(int* dev_out, int* num_sms) {
 
 // `p` must be device memory of device `dev`, and [p, p + bytes) must lie in one
 // allocation.  One driver query per pointer (memory type, ordinal, range).
-fa_status check_device_range(const void* p, size_t bytes, int dev) {
+fa_status check_device_range(const void* p, size_t bytes, int dev, CUdeviceptr* base_out = nullptr,
+                             size_t* size_out = nullptr) {
   const DriverFns& fns = driver_fns();
   if (!fns.pointer_attrs) return FA_ERR_CUDA;
   const CUdeviceptr dp = reinterpret_cast<CUdeviceptr>(p);
@@ -109,6 +110,10 @@ fa_status check_device_range(const void* p, size_t bytes, int dev) {
   if (fns.pointer_attrs(4, attrs, data, dp) != CUDA_SUCCESS) return FA_ERR_BAD_POINTER;
   if (mem_type != CU_MEMORYTYPE_DEVICE || ordinal != dev || size == 0) return FA_ERR_BAD_POINTER;
   if (dp < base || dp - base > size || bytes > size - (dp - base)) return FA_ERR_BAD_POINTER;
+  if (base_out) {
+    *base_out = base;
+    *size_out = size;
+  }
   return FA_OK;
 }
 
@@ -122,13 +127,29 @@ struct Range {
   size_t n;
 };
 
-// Every range is device memory of device `dev`, and no output overlaps an input or another output.
+// Every range is device memory of device `dev`, and no output overlaps an input or another output.  A range inside an
+// allocation that this call has asked about already (small tensors mostly share one) takes no further query.
 fa_status check_ranges(const Range* ins, int num_ins, const Range* outs, int num_outs, int dev) {
+  struct {
+    CUdeviceptr base;
+    size_t size;
+  } known[16];
+  int num_known = 0;
+  auto check = [&](const Range& r) {
+    const CUdeviceptr p = reinterpret_cast<CUdeviceptr>(r.p);
+    for (int k = 0; k < num_known; ++k)
+      if (p >= known[k].base && p - known[k].base <= known[k].size && r.n <= known[k].size - (p - known[k].base)) return FA_OK;
+    CUdeviceptr base = 0;
+    size_t size = 0;
+    const fa_status st = check_device_range(r.p, r.n, dev, &base, &size);
+    if (st == FA_OK && num_known < 16) known[num_known++] = {base, size};
+    return st;
+  };
   fa_status st;
   for (int i = 0; i < num_ins; ++i)
-    if ((st = check_device_range(ins[i].p, ins[i].n, dev)) != FA_OK) return st;
+    if ((st = check(ins[i])) != FA_OK) return st;
   for (int a = 0; a < num_outs; ++a) {
-    if ((st = check_device_range(outs[a].p, outs[a].n, dev)) != FA_OK) return st;
+    if ((st = check(outs[a])) != FA_OK) return st;
     for (int i = 0; i < num_ins; ++i)
       if (overlaps(outs[a].p, outs[a].n, ins[i].p, ins[i].n)) return FA_ERR_ALIAS;
     for (int b = 0; b < a; ++b)
