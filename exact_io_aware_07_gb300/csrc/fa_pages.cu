@@ -14,8 +14,8 @@ static __device__ unsigned int g_pages_status;  // kStatus* bits
 // another: a kept table entry (read for the tokens that fill up a page) is never written.
 //
 // Bound by latency, not by its bytes (310 KB for 2 000 requests, 0.05 us at the rate of the memory): lengths, scan and
-// barriers, a bisection in shared memory, one dependent load of a page, stores.  2.8 us for 64 decoding requests, 4.5 for
-// 7 prompts of up to 9 000 tokens, 8.9 for 2 000 requests with 62 000 tokens (two scans of 1024 requests one behind the
+// barriers, a bisection in shared memory, one dependent load of a page, stores.  2.7 us for 64 decoding requests, 3.1 for
+// 7 prompts of up to 9 000 tokens, 7.0 for 2 000 requests with 62 000 tokens (two scans of 1024 requests one behind the
 // other).  One kernel, every block with the whole scan: a scan over blocks would add a launch or a wait between blocks
 // (2 us) to save at most the second half of the last.
 constexpr int kPlanThreads = 1024;
@@ -55,18 +55,22 @@ __global__ void __launch_bounds__(kPlanThreads) fa_page_plan_kernel(const PlanPa
     return -1;
   };
   unsigned long long carry = 0;  // tokens (low half) and new pages (high half) of the requests so far
+  int next_c = tid < p.B ? p.ctx_lens[tid] : 0, next_n = tid < p.B ? p.new_lens[tid] : 0;
   for (int b0 = 0; b0 < p.B; b0 += kPlanThreads) {
     const int b = b0 + tid, count = min(kPlanThreads, p.B - b0);
-    int c = 0, n = 0;
+    int c = next_c, n = next_n;
+    if (p.B - b > kPlanThreads) {  // the next requests' lengths load while these are scanned
+      next_c = p.ctx_lens[b + kPlanThreads];
+      next_n = p.new_lens[b + kPlanThreads];
+    }
     if (b < p.B) {
-      c = p.ctx_lens[b];
-      n = p.new_lens[b];
       if (c < 0 || n < 0 || static_cast<long long>(c) + n > static_cast<long long>(p.max_pages) * kPage) {
         bad |= kStatusBadLength;
         c = min(max(c, 0), p.max_pages * kPage);
         n = 0;
       }
     }
+    if (b >= p.B) c = n = 0;
     const unsigned long long mine =
         static_cast<unsigned int>(n) | static_cast<unsigned long long>(pages_of(c + n) - pages_of(c)) << 32;
     unsigned long long sum = mine;
@@ -137,8 +141,8 @@ __global__ void __launch_bounds__(kPlanThreads) fa_page_plan_kernel(const PlanPa
 }
 
 cudaError_t launch_page_plan(const PlanParams& p, int num_sms, cudaStream_t stream) {
-  // a block per 4 096 places of the slot map: fewer blocks would queue up stores, more repeat the scan to no use
-  const long long want = (static_cast<long long>(p.max_tokens) + 4 * kPlanThreads - 1) / (4 * kPlanThreads);
+  // a thread per place of the slot map (8.9 -> 7.0 us for 62 000 tokens against four places one behind the other)
+  const long long want = (static_cast<long long>(p.max_tokens) + kPlanThreads - 1) / kPlanThreads;
   const int grid = static_cast<int>(want < 1 ? 1 : want > num_sms ? num_sms : want);
   fa_page_plan_kernel<<<grid, kPlanThreads, 0, stream>>>(p);
   return cudaGetLastError();
