@@ -495,7 +495,7 @@ PrefixWorkspace prefix_workspace(int N, int H, int Hkv, int d) {
   const long long item = (static_cast<long long>(N) * (H / Hkv) + 31) / 32 * 32;  // rows an item can have
   w.slab_rows = static_cast<int>(std::min<long long>(256, item));
   // rows of the slabs of cut items: two per many-row worker (block), two of up to 16 rows per few-row worker (warp)
-  const size_t slabs = static_cast<size_t>(fa::kPrefixMaxCtas) * 2 * (w.slab_rows + 16 * fa::kTeams);
+  const size_t slabs = static_cast<size_t>(fa::kPrefixMaxCtas) * 2 * (w.slab_rows + 16 * fa::kFewWarps);
   w.tok = take(static_cast<size_t>(N) * 16);
   w.rank = take(static_cast<size_t>(N) * 4);
   w.slab_o = take(slabs * d * 4);

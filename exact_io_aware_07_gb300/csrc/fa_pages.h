@@ -64,7 +64,7 @@ struct PrefixParams {
                       // tile sees, the token's number in the item | kTokFew | places of a unit << 16
   int* rank;          // [N] the token's item of the prefix (K/V head 0); -1: none
   int slab_rows;      // rows of a many-row slab
-  float* slab_o;      // [ctas][2][slab_rows][d], then [ctas * kTeams][2][few_rows][d]: parts of cut items
+  float* slab_o;      // [ctas][2][slab_rows][d], then [ctas * kFewWarps][2][few_rows][d]: parts of cut items
   float* slab_lse;    // the same rows, base-2
   float* own_o;       // [N * H][d] parts of whole items of own keys
   float* own_lse;
@@ -72,7 +72,7 @@ struct PrefixParams {
   float* prefix_lse;
 };
 constexpr int kPrefixMaxCtas = 160;
-constexpr int kTeams = 8;  // warps of a block that work few rows
+constexpr int kFewWarps = 8;  // warps of a block that work few rows
 // q: bf16 (d, H, N) with boxes of 64 columns x group heads x tp tokens; k, v: the page pools as (64, 128 rows, d / 64,
 // num_pages * Hkv) in boxes of whole pages, k16, v16: of `step` rows.
 struct PrefixMaps {

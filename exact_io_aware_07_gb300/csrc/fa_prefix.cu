@@ -240,8 +240,8 @@ __device__ __forceinline__ Plan make_plan(const PrefixParams& p, Layout& s, vola
     l.many = each * items;
     l.share[0] = (l.total[0] / items + each - 1) / each;
   }
-  const unsigned int teams = max(1, (p.ctas - l.many) * kTeams);
-  l.share[1] = max(kFewLeast, (l.total[1] + teams - 1) / teams);
+  const unsigned int warps = max(1, (p.ctas - l.many) * kFewWarps);
+  l.share[1] = max(kFewLeast, (l.total[1] + warps - 1) / warps);
   __syncthreads();
   // the last thread with requests whose key is not above x
   auto owner = [&](auto key, unsigned int x) {
@@ -260,9 +260,9 @@ __device__ __forceinline__ Plan make_plan(const PrefixParams& p, Layout& s, vola
   l.few = static_cast<int>(blockIdx.x) >= l.many;
   l.worker = l.few ? blockIdx.x - l.many : blockIdx.x;
   const int kind = l.few;
-  if (tid < (kind ? kTeams : 1)) {  // the request that holds this block's worker's first own place
+  if (tid < (kind ? kFewWarps : 1)) {  // the request that holds this block's worker's first own place
     const unsigned long long at =
-        static_cast<unsigned long long>(kind ? l.worker * kTeams + tid : l.worker) * l.share[kind];
+        static_cast<unsigned long long>(kind ? l.worker * kFewWarps + tid : l.worker) * l.share[kind];
     if (at < l.total[kind]) {
       const unsigned int x = max(static_cast<unsigned int>(at), l.lead[kind]);
       auto place = [&](int t) { return static_cast<unsigned int>(s.cum[t] >> (32 * kind)); };
@@ -1034,11 +1034,11 @@ struct FLayout {
   static constexpr int STEP = kStep<D>;
   static constexpr int STEP_BYTES = 2 * STEP * D * 2;  // K, then V; 64 columns per box of STEP rows x 128 bytes
   static constexpr int BOX = STEP * 128;
-  static constexpr int STAGES = PLayout<D>::XCH_OFF / (kTeams * STEP_BYTES);
-  static constexpr int BAR_OFF = PLayout<D>::END;  // full[kTeams][STAGES]
-  static constexpr int NUM_BARS = kTeams * STAGES;
+  static constexpr int STAGES = PLayout<D>::XCH_OFF / (kFewWarps * STEP_BYTES);
+  static constexpr int BAR_OFF = PLayout<D>::END;  // full[kFewWarps][STAGES]
+  static constexpr int NUM_BARS = kFewWarps * STAGES;
   static_assert(STAGES >= 3 && BAR_OFF % 8 == 0 && BAR_OFF + NUM_BARS * 8 <= NEED_OFF && NUM_BARS <= THREADS, "barriers");
-  static_assert(kTeams * STAGES * STEP_BYTES <= PLayout<D>::XCH_OFF, "the rings reach into what follows them");
+  static_assert(kFewWarps * STAGES * STEP_BYTES <= PLayout<D>::XCH_OFF, "the rings reach into what follows them");
 };
 
 // Warp-level products: D (16 x 8) += A (16 x 16) B (16 x 8), bf16 in, fp32 out.
@@ -1159,11 +1159,11 @@ __device__ __forceinline__ void few_rows(const CUtensorMap& tmK, const CUtensorM
   const uint32_t sbase = smem_u32(smem);
   const int warp = uni(threadIdx.x / 32), lane = threadIdx.x % 32;
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + PLayout<D>::MISC_OFF + 4);
-  if (warp >= kTeams) return;
+  if (warp >= kFewWarps) return;
   const Waiter W{abort_flag, p.timeout_ns, &g_prefix_status};
   const uint32_t ring = sbase + warp * L::STAGES * L::STEP_BYTES;
   const uint32_t bar_full = sbase + L::BAR_OFF + 8 * warp * L::STAGES;
-  const int worker = uni(l.worker) * kTeams + warp;
+  const int worker = uni(l.worker) * kFewWarps + warp;
   const unsigned int total = uni(l.total[1]), share = uni(l.share[1]);
   const unsigned long long from = static_cast<unsigned long long>(worker) * share;
   if (from >= total) return;
@@ -1173,7 +1173,7 @@ __device__ __forceinline__ void few_rows(const CUtensorMap& tmK, const CUtensorM
   const int first = uni(begin->b);
   const unsigned int first_place = uni(begin->c0);
 
-  // The ring's filling side (the team's first warp).  It stands a piece ahead: the next piece's pages (32 tiles', one per
+  // The ring's filling side stands a piece ahead: the next piece's pages (32 tiles', one per
   // lane) and query rows are asked for when the piece before it begins.
   FewWalk walk, load;
   FewPiece q, lp, ahead;
@@ -1493,7 +1493,7 @@ struct Parts {
   __device__ __forceinline__ void locate(const PrefixParams& p, const Plan& l) {
     share = few ? l.share[1] : l.share[0];
     // (places past the last worker come only of a cu_new that decreases, which is reported)
-    const unsigned int last = (few ? p.ctas * kTeams : p.ctas) - 1;
+    const unsigned int last = (few ? p.ctas * kFewWarps : p.ctas) - 1;
     const unsigned int w0 = min(it.worker(0, share), last), w1 = min(it.worker(it.units - 1, share), last);
     first = static_cast<int>(w0);
     count = w1 < w0 ? 1 : static_cast<int>(w1 - w0) + 1;

@@ -392,7 +392,7 @@ def test_on_another_stream_and_in_graphs_that_share_a_workspace():
 @pytest.mark.parametrize("tokens", [2, 3, 4, 7, 8, 15, 16, 17, 31])
 @pytest.mark.parametrize("prefix", [0, 333])
 def test_rows_per_request(d, tokens, prefix):
-    """4 to 124 rows a request and K/V head: every size of the few-row teams, and requests that fill part of a row tile;
+    """4 to 124 rows a request and K/V head: requests on warp-level products, and those that fill part of a row tile;
     beside them requests of fewer rows."""
     own = [tokens, 1500, tokens + 130, 1 + tokens // 2, 257]
     b = Batch(d, 8, 2, prefix, own, [tokens, tokens, tokens, 1 + tokens // 2, 1], pad=1, seed=30)
