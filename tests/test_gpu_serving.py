@@ -475,6 +475,49 @@ def test_calls_one_behind_the_other(requests):
     assert fa.fa_device_status() == 0
 
 
+def test_batches_of_all_sizes_in_turn_share_a_workspace():
+    """One request, a decoding batch and prompt chunks one behind the other on a stream and in a graph, all in one
+    workspace: each gives the bits that it gives alone."""
+    import torch
+
+    import exact_io_aware_07_gb300 as fa
+
+    shapes = [(128, 8, 2, 300, [40], [1]), (64, 16, 16, 100, [200, 3, 70], [6, 1, 2]),
+              (128, 8, 2, 1000, [(53 * i) % 400 + 1 for i in range(90)], [1] * 90), (128, 8, 2, 260, [600, 64], [400, 30])]
+    batches = [Batch(*x, pad=1, seed=40) for x in shapes]
+    args = [b.device() for b in batches]
+    size = max(fa.fa_fwd_prefix_paged_workspace_bytes(a["q"].shape[0], len(b.own), b.H, b.Hkv, b.d)
+               for a, b in zip(args, batches))
+    ws = torch.empty(size, dtype=torch.uint8, device="cuda")
+    alone = []
+    for b, a in zip(batches, args):
+        fa.fa_fwd_prefix_paged(**a, causal=True, scale=b.d ** -0.5)
+        torch.cuda.synchronize()
+        b.check(a["o"], a["lse"], label="alone")
+        alone.append((a["o"].clone(), a["lse"].clone()))
+    order = [0, 2, 0, 1, 3, 0, 0, 2, 1, 1, 3, 2, 0]
+
+    def turns():
+        outs = []
+        for i in order:
+            a = dict(args[i], o=torch.full_like(args[i]["o"], 7.0), lse=torch.full_like(args[i]["lse"], 7.0))
+            fa.fa_fwd_prefix_paged(**a, causal=True, scale=batches[i].d ** -0.5, workspace=ws)
+            outs.append((a["o"], a["lse"]))
+        return outs
+
+    graph = torch.cuda.CUDAGraph()
+    first = turns()
+    with torch.cuda.graph(graph):
+        second = turns()
+    for _ in range(3):
+        graph.replay()
+    torch.cuda.synchronize()
+    assert fa.fa_device_status() == 0
+    for outs in (first, second):
+        for i, (o, lse) in zip(order, outs):
+            assert torch.equal(o, alone[i][0]) and torch.equal(lse, alone[i][1]), i
+
+
 def test_two_calls_at_once():
     """Two streams, each with a workspace of its own."""
     import torch
