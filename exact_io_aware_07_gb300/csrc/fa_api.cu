@@ -850,7 +850,7 @@ fa_status fa_kv_append(const void* k_new, const void* v_new, const int* slot_map
   for (long long s : {k_stride, v_stride})
     if (N > 1) {
       if (s % 8 != 0) return FA_ERR_MISALIGNED;
-      if (s < width || s > (1ll << 40)) return FA_ERR_BAD_SHAPE;
+      if (s < width || s > (1ll << 40) / N) return FA_ERR_BAD_SHAPE;  // (the extents below stay far from 64 bits)
     }
   if (N == 1) k_stride = v_stride = width;
   int dev = 0, num_sms = 0;

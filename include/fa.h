@@ -355,7 +355,8 @@ fa_status fa_page_plan(const int* ctx_lens, const int* new_lens, const int* free
  *   N, Hkv       : tokens and K/V heads, >= 1; d: 64 or 128.
  * One kernel.  Errors: as fa_fwd_paged for the shared arguments; FA_ERR_MISALIGNED also
  * for a stride that is not a multiple of 8; FA_ERR_BAD_SHAPE also for a stride that is
- * too small; FA_ERR_ALIAS when a pool overlaps an input or the other pool.
+ * too small or with which N rows would reach over 2^40 elements; FA_ERR_ALIAS when a
+ * pool overlaps an input or the other pool.
  */
 fa_status fa_kv_append(const void* k_new, const void* v_new, const int* slot_map, void* k_pages, void* v_pages,
                        int N, int Hkv, int d, long long k_stride, long long v_stride, int num_pages,

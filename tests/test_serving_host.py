@@ -174,3 +174,19 @@ def test_oracle_attention_is_attention_on_the_joined_keys(causal):
 def test_oracle_empty_row():
     o, lse, spread, _ = paged.row(np.ones(4), np.zeros((0, 4)), np.zeros((0, 4)), 1.0)
     assert not o.any() and lse == -np.inf and not spread.any()
+
+
+@pytest.mark.parametrize("N,d,stride", [
+    (2 ** 24 + 1, 64, 2 ** 40),      # (N - 1) * stride is 2^64: nothing in 64 bits
+    (2 ** 24 + 1, 128, 2 ** 39),     # as many bytes
+    (2 ** 25 + 1, 64, 2 ** 39),
+    (2 ** 30 + 1, 64, 2 ** 34),
+    (2 ** 20 + 1, 64, 2 ** 40),      # 2^60 elements: no such memory
+])
+@pytest.mark.parametrize("which", ["ks", "vs"])
+def test_kv_append_refuses_rows_past_any_memory(lib, N, d, stride, which):
+    """Rows so far apart that the extent of the new keys or values does not fit 64 bits must not pass for a short one."""
+    far = A * 2 ** 20  # the pool and the slots are clear of the other arguments
+    kw = dict(slots=far, kp=2 * far, vp=3 * far, N=N, Hkv=1, d=d, ks=d, vs=d)
+    assert _append(lib, **{**kw, which: stride}) == 3
+    assert _append(lib, **kw) in (6, 10)  # rows side by side: up to the device
