@@ -477,6 +477,12 @@ fa_status launch_splitkv(Prepared& pr, int d, int num_splits, float* ws, cudaStr
   return FA_OK;
 }
 
+// Sizes of a batch that fa_fwd_prefix_paged takes: rows countable in 31 bits, a token's rows of a K/V head in a row tile.
+bool prefix_shape(int N, int B, int H, int Hkv) {
+  return N >= 1 && B >= 1 && H >= 1 && Hkv >= 1 && H % Hkv == 0 && H / Hkv <= 128 &&
+         static_cast<long long>(N) * H <= INT_MAX;
+}
+
 // Workspace of fa_fwd_prefix_paged: byte offsets of its parts (each a multiple of 256).
 struct PrefixWorkspace {
   size_t tok, rank, slab_o, slab_lse, own_o, own_lse, prefix_o, prefix_lse, bytes;
@@ -872,7 +878,7 @@ fa_status fa_kv_append(const void* k_new, const void* v_new, const int* slot_map
 }
 
 size_t fa_fwd_prefix_paged_workspace_bytes(int N, int B, int H, int Hkv, int d) {
-  if (N < 1 || B < 1 || H < 1 || Hkv < 1 || H % Hkv != 0 || (d != 64 && d != 128)) return 0;
+  if (!prefix_shape(N, B, H, Hkv) || (d != 64 && d != 128)) return 0;
   return prefix_workspace(N, H, Hkv, d).bytes;
 }
 
@@ -883,11 +889,10 @@ fa_status fa_fwd_prefix_paged(const void* q, const void* k_pages, const void* v_
                               cudaStream_t stream) {
   if (!q || !k_pages || !v_pages || !block_table || !seq_lens || !cu_new || !o || !lse) return FA_ERR_NULL_PTR;
   if (prefix_len > 0 && !prefix_table) return FA_ERR_NULL_PTR;
-  if (N < 1 || B < 1 || H < 1 || Hkv < 1 || H % Hkv != 0 || H / Hkv > 128 || prefix_len < 0 || max_new < 1 ||
-      num_pages < 1 || max_pages < 1)
+  if (!prefix_shape(N, B, H, Hkv) || prefix_len < 0 || max_new < 1 || num_pages < 1 || max_pages < 1)
     return FA_ERR_BAD_SHAPE;
-  if (static_cast<long long>(N) * H > INT_MAX || static_cast<long long>(num_pages) * Hkv >= INT_MAX ||
-      num_pages > INT_MAX / fa::kPage || max_pages > INT_MAX / fa::kPage || prefix_len > (1 << 30))
+  if (static_cast<long long>(num_pages) * Hkv >= INT_MAX || num_pages > INT_MAX / fa::kPage ||
+      max_pages > INT_MAX / fa::kPage || prefix_len > (1 << 30))
     return FA_ERR_BAD_SHAPE;
   if (d != 64 && d != 128) return FA_ERR_UNSUPPORTED_HEAD_DIM;
   // tokens of a 128-row tile; the most places the work can take on the lines that the SMs share

@@ -190,3 +190,16 @@ def test_kv_append_refuses_rows_past_any_memory(lib, N, d, stride, which):
     kw = dict(slots=far, kp=2 * far, vp=3 * far, N=N, Hkv=1, d=d, ks=d, vs=d)
     assert _append(lib, **{**kw, which: stride}) == 3
     assert _append(lib, **kw) in (6, 10)  # rows side by side: up to the device
+
+
+@pytest.mark.parametrize("sizes", [
+    (1, 1, 258, 2, 64),                    # 129 query heads of one K/V head
+    (1 << 24, 1, 256, 128, 64),            # 2^32 rows
+    (2 ** 31 - 1, 1, 2, 2, 128),
+    (2 ** 31 - 1, 1, 2 ** 31 - 1, 2 ** 31 - 1, 128),  # a size that does not fit 64 bits
+])
+def test_prefix_attention_workspace_size_is_0_out_of_range(lib, sizes):
+    """Sizes that the call refuses whatever its other arguments have no workspace."""
+    N, B, H, Hkv, d = sizes
+    assert _attend(lib, N=N, B=B, H=H, Hkv=Hkv, d=d) == 3
+    assert fa.fa_fwd_prefix_paged_workspace_bytes(*sizes) == 0
