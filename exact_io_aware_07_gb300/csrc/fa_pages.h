@@ -41,6 +41,7 @@ cudaError_t read_and_clear_pages_status(cudaStream_t stream, unsigned int* out);
 
 struct PrefixParams {
   const __nv_bfloat16* q;
+  const __nv_bfloat16* v;  // the page pool
   const int* prefix_table;
   const int* block_table;
   const int* seq_lens;

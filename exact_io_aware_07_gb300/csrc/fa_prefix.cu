@@ -374,6 +374,117 @@ __device__ __forceinline__ void tmem_ld_16x256b_x8_wait(uint32_t taddr, uint32_t
       : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
       : "r"(taddr) : "memory");
 }
+// ---------------------------------------------------------------- values that are not finite
+// The weight of an own key that causality hides from a row is 0, but 0 times an infinity or NaN is not, and a product's tile
+// (or step) on the diagonal has keys that only some of its rows see.  So there such values are set to 0 before the product
+// (`finite`), and afterwards added to the rows that see them: a row's sum has them with a weight above 0, so that it is
+// that infinity or NaN, whatever the weight and the divisor.  Values of other tiles are seen by all rows of a product.
+// The look at the diagonal's values takes 0.3 us of 131 for prompt chunks and 0.4 of 57 for drafted tokens; the code beside it
+// costs calls without a diagonal up to 1.3 us (77.1 for 128 requests behind 32 768 keys).  With such values in every request
+// the same chunks take 250 us, drafts 100.  (A NaN sought in the finished rows by the join, which then works those rows again,
+// cost every call 4 us: the join waits for its code.)
+__device__ __forceinline__ uint32_t finite(uint32_t x) {  // of two bf16, those that are
+  const uint32_t t = x & 0x7F807F80u;
+  return ((t & 0x7F80u) == 0x7F80u ? 0u : x & 0xFFFFu) | ((t >> 16) == 0x7F80u ? 0u : x & 0xFFFF0000u);
+}
+// sum += x * 0: of two bf16 each stays a zero until it is NaN.
+__device__ __forceinline__ void add_bf16x2_zeros(uint32_t x, uint32_t& sum) {
+  asm("fma.rn.bf16x2 %0, %1, %2, %0;" : "+r"(sum) : "r"(x), "r"(0u));
+}
+// Sets the values of `bytes` of shared memory that are not finite to 0 and notes whether there were any.
+__device__ __forceinline__ void zero_not_finite(uint32_t at, int bytes, volatile int* zeroed) {
+  const int lane_at = (threadIdx.x & 31) * 16;
+  uint32_t off[4] = {0, 0, 0, 0};  // 0, or NaN with a value that is not finite
+#pragma unroll 4
+  for (int w = lane_at; w < bytes; w += 512) {
+    const float4 x = ld_shared_v4f(at + w);
+    add_bf16x2_zeros(__float_as_uint(x.x), off[0]);
+    add_bf16x2_zeros(__float_as_uint(x.y), off[1]);
+    add_bf16x2_zeros(__float_as_uint(x.z), off[2]);
+    add_bf16x2_zeros(__float_as_uint(x.w), off[3]);
+  }
+  if (__builtin_expect(!__any_sync(0xffffffffu, ((off[0] | off[1] | off[2] | off[3]) & 0x7FFF7FFFu) != 0), 1)) return;
+#pragma unroll 1
+  for (int w = lane_at; w < bytes; w += 512) {
+    const float4 x = ld_shared_v4f(at + w);
+    st_shared_v4(at + w, finite(__float_as_uint(x.x)), finite(__float_as_uint(x.y)), finite(__float_as_uint(x.z)),
+                 finite(__float_as_uint(x.w)));
+  }
+  *zeroed = 1;
+  __threadfence_block();     // before anything tells of the product
+  fence_proxy_async_smem();  // before the tensor core reads and the next copy writes here
+  __syncwarp();
+}
+// Lane r's row is at `to` (nowhere: none) and sees the own keys below `lim`: adds to it what was set to 0 of the keys from
+// k0 to k1 of the request with token t0, the first of the item.  (What is added twice, or beside itself, changes nothing.)
+template <int D>
+__device__ __noinline__ void add_not_finite(const PrefixParams& p, int g, int t0, int k0, int k1, const RowOut& to, int lim) {
+  const int lane = threadIdx.x & 31;
+  __syncwarp();  // the rows are written
+  if (k1 <= 0) return;
+  int b = 0;
+#pragma unroll 1
+  for (int hi = p.B; hi - b > 1;) {
+    const int mid = (b + hi) >> 1;
+    if (p.cu_new[mid] <= t0)
+      b = mid;
+    else
+      hi = mid;
+  }
+  const Request r = make_request(p, p.cu_new[b], p.cu_new[b + 1], p.seq_lens[b]);
+  k0 = max(k0, max(0, r.len - r.added + t0 - r.first + 1) / kPage * kPage);  // from the first tile on the diagonal
+  k1 = min(k1, r.len);
+  const bool out = to.out != nullptr;
+  const unsigned long long row = reinterpret_cast<unsigned long long>(out ? static_cast<void*>(to.out) : to.part);
+  float sum[D / 32];  // of columns lane, lane + 32 ..: what the keys so far add
+#pragma unroll
+  for (int c = 0; c < D / 32; ++c) sum[c] = 0.f;
+  int next = 0;  // the rows see more keys from one to the next: those before `next` are done
+  auto add_below = [&](int k) {  // to the rows that see no key from k on
+#pragma unroll 1
+    for (; next < 32 && __shfl_sync(0xffffffffu, lim, next) <= k; ++next) {
+      const unsigned long long at = __shfl_sync(0xffffffffu, row, next);
+      const bool bf16 = __shfl_sync(0xffffffffu, out, next);
+#pragma unroll
+      for (int c = 0; c < D / 32; ++c) {
+        if (!at || sum[c] == 0.f) continue;
+        if (bf16) {
+          __nv_bfloat16* o = reinterpret_cast<__nv_bfloat16*>(at) + lane + 32 * c;
+          *o = __float2bfloat16_rn(__bfloat162float(*o) + sum[c]);
+        } else {
+          reinterpret_cast<float*>(at)[lane + 32 * c] += sum[c];
+        }
+      }
+    }
+  };
+#pragma unroll 1
+  for (; k0 < k1; k0 += 32) {  // a key per lane first: which have such values
+    const uint32_t* mine = nullptr;
+    bool any = false;
+    if (k0 + lane < k1) {
+      const int page = p.block_table[static_cast<size_t>(b) * p.max_pages + (k0 + lane) / kPage];
+      if (page >= 0 && page < p.num_pages) {  // (another reads as zeros)
+        mine = reinterpret_cast<const uint32_t*>(p.v + ((static_cast<size_t>(page) * p.Hkv + g) * kPage + (k0 + lane) % kPage) * D);
+#pragma unroll 4
+        for (int c = 0; c < D / 2; ++c) any |= finite(mine[c]) != mine[c];
+      }
+    }
+#pragma unroll 1
+    for (unsigned int keys = __ballot_sync(0xffffffffu, any); keys; keys &= keys - 1) {
+      const int k = __ffs(keys) - 1;
+      const uint32_t* v = reinterpret_cast<const uint32_t*>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(mine), k));
+      add_below(k0 + k);
+#pragma unroll
+      for (int c = 0; c < D / 32; ++c) {
+        const uint32_t x = v[(lane + 32 * c) / 2];
+        const float y = __uint_as_float(lane & 1 ? x & 0xFFFF0000u : x << 16);
+        if (!isfinite(y)) sum[c] += y;
+      }
+    }
+  }
+  add_below(INT_MAX);
+}
+
 // The value of lane 0, known to be the same for the whole warp (tensor-core and TMA operands are warp-uniform).
 __device__ __forceinline__ int uni(int x) { return __shfl_sync(0xffffffffu, x, 0); }
 
@@ -478,7 +589,7 @@ struct PLayout {
   // q_full, q_empty, kv_full[S], kv_empty[S], s_full[2], p_full[2], o_full[2], o_empty[2], x_full[4], done,
   // piece_full[], piece_empty[]
   static constexpr int NUM_BARS = 2 + 2 * STAGES + 8 + 4 + 1 + 2 * kPieceSlots;
-  static constexpr int MISC_OFF = BAR_OFF + NUM_BARS * 8;  // TMEM base, abort flag
+  static constexpr int MISC_OFF = BAR_OFF + NUM_BARS * 8;  // TMEM base, abort flag, whether values were set to 0
   static constexpr int END = MISC_OFF + 16;
 
   // Initialises barrier `t` (threads 0 .. NUM_BARS - 1, one each).
@@ -512,6 +623,7 @@ __device__ __forceinline__ void many_rows(const CUtensorMap& tmQ, const CUtensor
   volatile float* xch = reinterpret_cast<volatile float*>(smem + L::XCH_OFF);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::MISC_OFF);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::MISC_OFF + 4);
+  volatile int* zeroed = reinterpret_cast<volatile int*>(smem + L::MISC_OFF + 8);
   const int warp = uni(threadIdx.x / 32), lane = threadIdx.x % 32;
 
   const uint32_t tmem = *tmem_slot;
@@ -707,15 +819,24 @@ __device__ __forceinline__ void many_rows(const CUtensorMap& tmQ, const CUtensor
     // The last tile of a source holds fewer than 128 keys, and what its page holds behind them may be
     // anything.  Their weights are 0, but 0 times an infinity or NaN is not: the product runs over the keys
     // in steps of 16 as far as there are keys, and the value rows behind the last key in its last step are
-    // set to 0.  Returns the steps.
+    // set to 0.  So are the values that are not finite of a tile on the diagonal (see `finite`; the softmax of the tile
+    // takes longer than this look at it).  Returns the steps.
     auto value_steps = [&](const Piece& q, int tile, int vs) -> int {
-      const int valid = tile < q.ptiles ? p.prefix_len - tile * BN : q.keys - (tile - q.ptiles) * BN;
-      if (valid >= BN) return BN / 16;
-      const int steps = (valid + 15) / 16, words = (steps * 16 - valid) * 8;  // 16-byte words per box
+      const int own = (tile - q.ptiles) * BN, valid = tile < q.ptiles ? p.prefix_len - tile * BN : q.keys - own;
+      const bool diagonal = tile >= q.ptiles && min(q.keys, own + BN) > q.lim0;
+      const int steps = valid >= BN ? BN / 16 : (valid + 15) / 16;
+      if (valid >= BN && !diagonal) return steps;
+      const uint32_t rows = kv_smem + vs * L::TILE_BYTES;
+      const int words = max(0, steps * 16 - valid) * 8;  // 16-byte words per box
 #pragma unroll 1
       for (int w = lane; w < words * L::BOXES; w += 32) {
         const int box = w / words, at = w - box * words;
-        st_shared_v4(kv_smem + vs * L::TILE_BYTES + box * BOX_BYTES + valid * 128 + at * 16, 0, 0, 0, 0);
+        st_shared_v4(rows + box * BOX_BYTES + valid * 128 + at * 16, 0, 0, 0, 0);
+      }
+      if (diagonal) {
+        __syncwarp();
+#pragma unroll 1
+        for (int box = 0; box < L::BOXES; ++box) zero_not_finite(rows + box * BOX_BYTES, steps * 2048, zeroed);
       }
       fence_proxy_async_smem();
       __syncwarp();
@@ -755,6 +876,7 @@ __device__ __forceinline__ void many_rows(const CUtensorMap& tmQ, const CUtensor
       q.j0 = uni(pieces[s].j0);
       q.keys = uni(pieces[s].keys);
       q.ptiles = uni(pieces[s].ptiles);
+      q.lim0 = uni(pieces[s].lim0);
       q.turn = uni(pieces[s].turn);
       __syncwarp();
       if (lane == 0) mbar_arrive(bar_piece_empty + 8 * s);
@@ -1008,6 +1130,10 @@ __device__ __forceinline__ void many_rows(const CUtensorMap& tmQ, const CUtensor
         mbar_arrive(bar_o_empty + 8 * i);
         if (pair) mbar_arrive(bar_o_empty + 8);
       }
+      if (__builtin_expect(__any_sync(0xffffffffu, *zeroed), 0)) {  // (for this piece or one before it)
+        const RowOut to = row_out<D>(p, dst, many_slab(p, l_worker, dst == kDstSlab1), g, t0, row0 + rt);
+        add_not_finite<D>(p, g, t0, (j0 - ptiles) * BN, (j0 + n - ptiles) * BN, live ? to : RowOut{}, lim);
+      }
     }
     __syncwarp();
   }
@@ -1159,6 +1285,7 @@ __device__ __forceinline__ void few_rows(const CUtensorMap& tmK, const CUtensorM
   const uint32_t sbase = smem_u32(smem);
   const int warp = uni(threadIdx.x / 32), lane = threadIdx.x % 32;
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + PLayout<D>::MISC_OFF + 4);
+  volatile int* zeroed = reinterpret_cast<volatile int*>(smem + PLayout<D>::MISC_OFF + 8);
   if (warp >= kFewWarps) return;
   const Waiter W{abort_flag, p.timeout_ns, &g_prefix_status};
   const uint32_t ring = sbase + warp * L::STAGES * L::STEP_BYTES;
@@ -1310,6 +1437,10 @@ __device__ __forceinline__ void few_rows(const CUtensorMap& tmK, const CUtensorM
 #pragma unroll
           for (int e = 0; e < 4; ++e) s[0][t][e] += s2[t][e];
       if (k0 + L::STEP > lim_min) {  // some row does not see all of these keys
+        if (lim_min < q.keys)  // (the rows behind the last key are no values)
+#pragma unroll 1
+          for (int box = 0; box < D / 64; ++box)
+            zero_not_finite(ring + L::STEP_BYTES / 2 + at + box * L::BOX, min(L::STEP, q.keys - k0) * 128, zeroed);
 #pragma unroll
         for (int u = 0; u < U; ++u) {
           const int key = k0 + u * 16 + lane / 4;
@@ -1424,6 +1555,9 @@ __device__ __forceinline__ void few_rows(const CUtensorMap& tmK, const CUtensorM
           *to.lse = to.out ? lse2 * LN2 : lse2;
         }
       }
+    if (__builtin_expect(lim_min < q.keys && __any_sync(0xffffffffu, *zeroed), 0))  // (by one of the block's warps)
+      add_not_finite<D>(p, q.g, q.t0, q.j0 * L::STEP, q.j1 * L::STEP,
+                        lane < q.rows ? row_out<D>(p, q.dst, slab, q.g, q.t0, lane) : RowOut{}, q.lim0 + lane / p.group);
   }
   if (!ok)  // let every copy already issued land before the block exits
 #pragma unroll 1
@@ -1458,7 +1592,7 @@ fa_prefix_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
   const uint32_t sbase = smem_u32(smem);
   if (threadIdx.x < M::NUM_BARS) M::init(sbase, threadIdx.x);
   if (threadIdx.x < F::NUM_BARS) mbar_init(sbase + F::BAR_OFF + 8 * threadIdx.x, 1);
-  if (threadIdx.x == 0) *reinterpret_cast<volatile int*>(smem + M::MISC_OFF + 4) = 0;
+  if (threadIdx.x < 2) reinterpret_cast<volatile int*>(smem + M::MISC_OFF + 4)[threadIdx.x] = 0;
   fence_mbar_init();
   const int warp = uni(threadIdx.x / 32);
   if (warp == MMA_WARP) {

@@ -390,9 +390,8 @@ fa_status fa_kv_append(const void* k_new, const void* v_new, const int* slot_map
  * Device errors (fa_device_status): FA_ERR_BAD_PAGE for a page outside the pool (it reads
  * as zeros), FA_ERR_BAD_LENGTH for a length outside the table or the batch (cut to fit).
  * Where cu_new decreases (reported as FA_ERR_BAD_LENGTH) the rows concerned hold no meaning.
- * The result does not depend on scheduling: equal calls give equal bits.  An infinity or NaN
- * in the value of a request's new token may reach that request's earlier new tokens too,
- * which give it the weight 0; it reaches no other request.  Two kernels.
+ * The result does not depend on scheduling: equal calls give equal bits.  An infinity or NaN in
+ * a key or value reaches only the rows that see it.  Two kernels.
  * Errors: as fa_fwd_paged for the shared arguments; FA_ERR_WORKSPACE; FA_ERR_BAD_SHAPE also
  * for N, B, max_pages or max_new < 1, prefix_len < 0, H / Hkv > 128, and sizes whose key
  * tiles cannot be counted in 31 bits.

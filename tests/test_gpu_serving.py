@@ -840,3 +840,90 @@ def test_command_line(op, monkeypatch, capsys):
                                       "--prefix", "300", "--new", "2"])
     assert cli.main() == 0
     assert "device status 0" in capsys.readouterr().out
+
+
+# ---------------------------------------------------------------- values that are not finite
+
+@pytest.mark.parametrize("prefix", [0, 200])
+@pytest.mark.parametrize("d,H,Hkv,own,new", [
+    (64, 8, 2, [40, 30, 150, 3000], [1, 2, 20, 2]),
+    (64, 16, 16, [200, 64, 700], [8, 5, 1]),              # few-row items of 8 and 16 rows
+    (128, 8, 2, [400, 33, 300, 5000], [150, 2, 20, 2]),   # big, few and middling requests, one cut into many parts
+    (128, 4, 4, [2000], [7]),                             # one request
+    (64, 8, 2, [1200, 9], [1100, 2]),                     # over 7 296 rows
+    (128, 8, 2, [1000, 40], [1000, 1]),
+])
+def test_values_that_are_not_finite_reach_only_the_rows_that_see_them(d, H, Hkv, own, new, prefix):
+    """New tokens whose values have a NaN and infinities in some columns: the rows before them, whose weights there are 0,
+    keep every column; the rows from them on keep the other columns.  A NaN in the prefix beside them reaches all rows'
+    column.  The clean call before and after gives the same bits."""
+    import torch
+
+    import exact_io_aware_07_gb300 as fa
+
+    b = Batch(d, H, Hkv, prefix, own, new, pad=1, seed=41)
+    ref = b.reference()
+    a = b.device()
+    n, group = a["q"].shape[0], H // Hkv
+    ws = torch.full((fa.fa_fwd_prefix_paged_workspace_bytes(n, len(own), H, Hkv, d),), 0xFF, dtype=torch.uint8, device="cuda")
+
+    def run():
+        a["o"].fill_(7.0), a["lse"].fill_(7.0)
+        fa.fa_fwd_prefix_paged(**a, causal=True, scale=d ** -0.5, workspace=ws)
+        torch.cuda.synchronize()
+        assert fa.fa_device_status() == 0
+        return a["o"].clone(), a["lse"].clone()
+
+    o0, lse0 = run()
+    compare(o0, lse0, ref, int(b.cu[-1]), d, "clean")
+    marks = {}  # (row, head, column) -> what it has to be
+    v = b.v.copy()
+    for r, (s, t) in enumerate(zip(own, new)):
+        for i in sorted({1, t // 2, t - 1}) if t > 1 else []:
+            key = s - t + i
+            for g in {0, Hkv - 1}:
+                at = v[b.table[r, key // 128], g, key % 128]
+                for col, x in ((3 + i % 7, NAN_BITS), (20, INF_BITS), (d - 1, INF_BITS | 0x8000)):
+                    at[col] = x
+                    for row in range(int(b.cu[r]) + i, int(b.cu[r + 1])):
+                        for h in range(g * group, (g + 1) * group):
+                            marks[row, h, col] = x
+    if prefix:
+        v[b.prefix_table[0], Hkv - 1, 7, 40] = NAN_BITS
+        for row in range(int(b.cu[-1])):
+            for h in range((Hkv - 1) * group, H):
+                marks[row, h, 40] = NAN_BITS
+    a["v_pages"] = to_device(None, v)
+    o, lse = run()
+    assert torch.equal(lse, lse0)  # values do not reach the statistics
+    got = bf16_to_f64(o)
+    for (row, h, col), x in marks.items():
+        y = got[row, h, col]
+        assert np.isnan(y) if x == NAN_BITS else y == (np.inf if x == INF_BITS else -np.inf), (row, h, col, y)
+    index = torch.tensor(list(marks), device="cuda").t()
+    o[index[0], index[1], index[2]] = o0[index[0], index[1], index[2]]
+    compare(o, lse, ref, int(b.cu[-1]), d, "beside marked values")
+    a["v_pages"] = to_device(None, b.v)
+    o, lse = run()
+    assert torch.equal(o, o0) and torch.equal(lse, lse0)
+
+
+def test_a_value_that_all_rows_see_changes_no_other_column():
+    """Rows that all see a NaN value are left as they are: the column of each is NaN, the others are those of the clean call,
+    bit for bit."""
+    import torch
+
+    import exact_io_aware_07_gb300 as fa
+
+    b = Batch(128, 8, 2, 0, [500, 30], [500, 2], seed=42)
+    a = b.device()
+    fa.fa_fwd_prefix_paged(**a, causal=True, scale=128 ** -0.5)
+    o0 = a["o"].clone()
+    b.v[b.table[0, 0], 1, 0, 9] = NAN_BITS
+    a["v_pages"] = to_device(None, b.v)
+    fa.fa_fwd_prefix_paged(**a, causal=True, scale=128 ** -0.5)
+    torch.cuda.synchronize()
+    assert fa.fa_device_status() == 0
+    assert torch.isnan(a["o"][:500, 4:, 9]).all()
+    a["o"][:500, 4:, 9] = o0[:500, 4:, 9]
+    assert torch.equal(a["o"], o0)
