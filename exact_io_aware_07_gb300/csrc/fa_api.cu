@@ -1002,15 +1002,36 @@ const char* fa_status_string(fa_status s) {
 
 fa_status fa_device_status(cudaStream_t stream, int* out) {
   if (!out) return FA_ERR_NULL_PTR;
-  unsigned int word = 0, bwd = 0, pages = 0, prefix = 0;
-  if (fa::read_and_clear_status(stream, &word) != cudaSuccess ||
-      fa::read_and_clear_bwd_status(stream, &bwd) != cudaSuccess ||
-      fa::read_and_clear_pages_status(stream, &pages) != cudaSuccess ||
-      fa::read_and_clear_prefix_status(stream, &prefix) != cudaSuccess) {
+  if (cudaStreamSynchronize(stream) != cudaSuccess) {
     cudaGetLastError();
     return FA_ERR_CUDA;
   }
-  word |= bwd | pages | prefix;
+  // The words of the four files of kernels: read together, and only those that something set are cleared (14 us;
+  // 34 for two words read and cleared one by one, 53 for four).
+  struct Word {
+    cudaError_t (*read)(unsigned int*);
+    cudaError_t (*clear)();
+  };
+  static const Word words[4] = {{fa::read_status, fa::clear_status},
+                                {fa::read_bwd_status, fa::clear_bwd_status},
+                                {fa::read_pages_status, fa::clear_pages_status},
+                                {fa::read_prefix_status, fa::clear_prefix_status}};
+  static std::mutex mu;
+  static unsigned int* got = nullptr;  // page-locked
+  std::lock_guard<std::mutex> lock(mu);
+  cudaError_t e = got ? cudaSuccess : cudaHostAlloc(reinterpret_cast<void**>(&got), sizeof(*got) * 4, cudaHostAllocPortable);
+  for (int i = 0; i < 4 && e == cudaSuccess; ++i) e = words[i].read(got + i);
+  if (e == cudaSuccess) e = cudaStreamSynchronize(cudaStreamLegacy);
+  unsigned int word = 0;
+  for (int i = 0; i < 4 && e == cudaSuccess; ++i)
+    if (got[i]) {
+      word |= got[i];
+      e = words[i].clear();
+    }
+  if (e != cudaSuccess) {
+    cudaGetLastError();
+    return FA_ERR_CUDA;
+  }
   *out = (word & fa::kStatusBadPage)     ? FA_ERR_BAD_PAGE
          : (word & fa::kStatusTimeout)   ? FA_ERR_DEVICE_TIMEOUT
          : (word & fa::kStatusNoPages)   ? FA_ERR_NO_PAGES

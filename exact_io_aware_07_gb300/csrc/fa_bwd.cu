@@ -971,11 +971,10 @@ int fa_bwd_smem_bytes(int d) {
   return d == 64 ? max(BwdLayout<64, 0>::SMEM, BwdLayout<64, 1>::SMEM) : max(BwdLayout<128, 0>::SMEM, BwdLayout<128, 1>::SMEM);
 }
 
-cudaError_t read_and_clear_bwd_status(cudaStream_t stream, unsigned int* out) {
-  cudaError_t e = cudaStreamSynchronize(stream);
-  if (e != cudaSuccess) return e;
-  e = cudaMemcpyFromSymbol(out, g_bwd_status, sizeof(unsigned int));
-  if (e != cudaSuccess) return e;
+cudaError_t read_bwd_status(unsigned int* out) {
+  return cudaMemcpyFromSymbolAsync(out, g_bwd_status, sizeof(unsigned int), 0, cudaMemcpyDeviceToHost, cudaStreamLegacy);
+}
+cudaError_t clear_bwd_status() {
   const unsigned int zero = 0;
   return cudaMemcpyToSymbol(g_bwd_status, &zero, sizeof(unsigned int));
 }

@@ -1434,11 +1434,10 @@ int fa_fwd_smem_bytes(int d) { return d == 64 ? Layout<64>::SMEM_BYTES : Layout<
 int fa_fwd_threads(int d) { return d == 64 ? Layout<64>::THREADS : Layout<128>::THREADS; }
 int fa_fwd_rows_per_unit() { return 2 * BM; }
 
-cudaError_t read_and_clear_status(cudaStream_t stream, unsigned int* out) {
-  cudaError_t e = cudaStreamSynchronize(stream);
-  if (e != cudaSuccess) return e;
-  e = cudaMemcpyFromSymbol(out, g_status, sizeof(unsigned int));
-  if (e != cudaSuccess) return e;
+cudaError_t read_status(unsigned int* out) {
+  return cudaMemcpyFromSymbolAsync(out, g_status, sizeof(unsigned int), 0, cudaMemcpyDeviceToHost, cudaStreamLegacy);
+}
+cudaError_t clear_status() {
   const unsigned int zero = 0;
   return cudaMemcpyToSymbol(g_status, &zero, sizeof(unsigned int));
 }

@@ -69,7 +69,9 @@ cudaError_t launch_fa_fwd_partial(int d, const CUtensorMap& q, const CUtensorMap
 int fa_fwd_smem_bytes(int d);
 int fa_fwd_threads(int d);
 int fa_fwd_rows_per_unit();
-cudaError_t read_and_clear_status(cudaStream_t stream, unsigned int* out);
+// A file's device status word: read asynchronously, on the legacy stream, into page-locked memory; cleared.
+cudaError_t read_status(unsigned int* out);
+cudaError_t clear_status();
 cudaError_t launch_wait_selftest(unsigned long long timeout_ns, cudaStream_t stream);
 // ex2.approx operations per second of the whole device (two launches of a probe kernel;
 // waits for the second).
@@ -126,7 +128,8 @@ cudaError_t launch_bwd_dkdv(int d, const CUtensorMap& q, const CUtensorMap& k, c
                             const CUtensorMap& dout, const CUtensorMap& g1, const CUtensorMap& g2,
                             const BwdParams& p, int grid, cudaStream_t stream);
 int fa_bwd_smem_bytes(int d);
-// Reads and clears the backward kernels' device status word (bit 0: a wait ran out).
-cudaError_t read_and_clear_bwd_status(cudaStream_t stream, unsigned int* out);
+// The backward kernels' device status word (bit 0: a wait ran out).
+cudaError_t read_bwd_status(unsigned int* out);
+cudaError_t clear_bwd_status();
 
 }  // namespace fa

@@ -181,11 +181,10 @@ cudaError_t launch_kv_append(const AppendParams& p, int, cudaStream_t stream) {
   return cudaGetLastError();
 }
 
-cudaError_t read_and_clear_pages_status(cudaStream_t stream, unsigned int* out) {
-  cudaError_t e = cudaStreamSynchronize(stream);
-  if (e != cudaSuccess) return e;
-  e = cudaMemcpyFromSymbol(out, g_pages_status, sizeof(unsigned int));
-  if (e != cudaSuccess || *out == 0) return e;
+cudaError_t read_pages_status(unsigned int* out) {
+  return cudaMemcpyFromSymbolAsync(out, g_pages_status, sizeof(unsigned int), 0, cudaMemcpyDeviceToHost, cudaStreamLegacy);
+}
+cudaError_t clear_pages_status() {
   const unsigned int zero = 0;
   return cudaMemcpyToSymbol(g_pages_status, &zero, sizeof(unsigned int));
 }

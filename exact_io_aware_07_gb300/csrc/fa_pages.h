@@ -36,8 +36,9 @@ struct AppendParams {
   int N, Hkv, d, num_pages;
 };
 cudaError_t launch_kv_append(const AppendParams& p, int num_sms, cudaStream_t stream);
-// Reads and clears the status word of fa_pages.cu.
-cudaError_t read_and_clear_pages_status(cudaStream_t stream, unsigned int* out);
+// The status word of fa_pages.cu (see fa_kernel.h).
+cudaError_t read_pages_status(unsigned int* out);
+cudaError_t clear_pages_status();
 
 struct PrefixParams {
   const __nv_bfloat16* q;
@@ -82,6 +83,7 @@ struct PrefixMaps {
 unsigned int prefix_page_cost();  // the most places a page and an item take on a line (see fa_prefix.cu)
 unsigned int prefix_item_cost();
 cudaError_t launch_fa_fwd_prefix(int d, const PrefixMaps& t, const PrefixParams& p, cudaStream_t stream);
-cudaError_t read_and_clear_prefix_status(cudaStream_t stream, unsigned int* out);
+cudaError_t read_prefix_status(unsigned int* out);
+cudaError_t clear_prefix_status();
 
 }  // namespace fa

@@ -1854,11 +1854,10 @@ unsigned int prefix_page_cost() { return kTileCost256; }
 unsigned int prefix_item_cost() { return kItemCost; }
 static_assert(kTileCost256 >= kPage / kStep<128> && kItemCost >= kFewItemCost, "prefix_page_cost, prefix_item_cost");
 
-cudaError_t read_and_clear_prefix_status(cudaStream_t stream, unsigned int* out) {
-  cudaError_t e = cudaStreamSynchronize(stream);
-  if (e != cudaSuccess) return e;
-  e = cudaMemcpyFromSymbol(out, g_prefix_status, sizeof(unsigned int));
-  if (e != cudaSuccess || *out == 0) return e;
+cudaError_t read_prefix_status(unsigned int* out) {
+  return cudaMemcpyFromSymbolAsync(out, g_prefix_status, sizeof(unsigned int), 0, cudaMemcpyDeviceToHost, cudaStreamLegacy);
+}
+cudaError_t clear_prefix_status() {
   const unsigned int zero = 0;
   return cudaMemcpyToSymbol(g_prefix_status, &zero, sizeof(unsigned int));
 }
