@@ -927,3 +927,125 @@ def test_a_value_that_all_rows_see_changes_no_other_column():
     assert torch.isnan(a["o"][:500, 4:, 9]).all()
     a["o"][:500, 4:, 9] = o0[:500, 4:, 9]
     assert torch.equal(a["o"], o0)
+
+
+# ---------------------------------------------------------------- large batches, host threads
+
+def check_rows(b, o, lse, rows, heads, label):
+    """Rows `rows` and heads `heads` against the oracle, one by one; every row is finite."""
+    f = fi.bf16_bits_to_f64
+    group = b.H // b.Hkv
+    prefix = {}
+    out = [[], [], [], []]
+    for n in rows:
+        r = int(np.searchsorted(b.cu, n, side="right")) - 1
+        seen = int(b.seq[r]) - int(b.cu[r + 1] - b.cu[r]) + int(n - b.cu[r]) + 1
+        own = {}
+        for h in heads:
+            g = h // group
+            if g not in prefix:
+                prefix[g] = [f(paged.gather(x, b.prefix_table, b.prefix)[:, g]) for x in (b.k, b.v)]
+            if g not in own:
+                own[g] = [f(x[b.table[r, :pages_of(seen)], g].reshape(-1, b.d)[:seen]) for x in (b.k, b.v)]
+            k, v = (np.concatenate(x) for x in zip(prefix[g], own[g]))
+            for dst, x in zip(out, paged.row(f(b.q[n, h]), k, v, b.d ** -0.5)):
+                dst.append(x)
+    shape = len(rows), len(heads)
+    ref = [np.array(x).reshape(*shape, *np.shape(x[0])) for x in out]
+    index = np.ix_(rows, heads)
+    compare(o[index], lse[index], ref, len(rows), b.d, label)
+    live = int(b.cu[-1])
+    assert bool(o[:live].isfinite().all()) and bool(lse[:live].isfinite().all()) and bool((o[live:] == 7).all()), label
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("H,Hkv,prefix,own,new", [
+    (32, 8, 300, [700, 64, 1300] + [40] * 60, [600, 20, 160] + [1] * 60),  # rows of one part, of two and of cut items
+    (16, 16, 0, [900], [900]),
+    (8, 1, 1000, [5000, 3], [1000, 1]),
+])
+def test_more_rows_than_a_warp_each(d, H, Hkv, prefix, own, new):
+    """Over 48 rows per SM: rows are joined eight lanes each."""
+    b = Batch(d, H, Hkv, prefix, own, new, pad=2, seed=43)
+    assert b.q.shape[0] * H > 48 * 152
+    o, lse = b.run()
+    rows = sorted({0, 1, 127, 128, 599, sum(new) - 1, *range(5, sum(new), 61)} & set(range(sum(new))))
+    check_rows(b, o, lse, rows, sorted({0, 5, H - 1}), f"many rows d{d}")
+
+
+@pytest.mark.parametrize("d,H,Hkv,prefix,own,new", [
+    (64, 4, 2, 0, [6000], [6000]),
+    (128, 8, 2, 500, [2500, 9000, 1], [2500, 4100, 1]),
+])
+def test_prompts_of_thousands_of_tokens(d, H, Hkv, prefix, own, new):
+    b = Batch(d, H, Hkv, prefix, own, new, pad=1, seed=44)
+    o, lse = b.run()
+    rows = sorted({*range(0, sum(new), 331), *range(sum(new) - 5, sum(new))})
+    check_rows(b, o, lse, rows, [0, H - 1], f"prompts {new} d{d}")
+
+
+def test_plan_of_more_tokens_than_threads():
+    """Two prompts of 80 000 tokens and places behind them: every thread of the grid has a second place."""
+    import exact_io_aware_07_gb300 as fa
+
+    ctx, new, table, free, head, num_pages = _plan_inputs([100, 0, 0, 64], [80000, 0, 80001, 1], seed=45)
+    places = int(new.sum()) + 20000
+    assert places > 152 * 1024
+    got = _run_plan(ctx, new, table, free, head, num_pages, places)
+    want = paged.page_plan(ctx, new, free, head, table, places)
+    for name, g, w in zip(("table", "seq", "cu", "slots", "head"), got, want):
+        assert np.array_equal(g.reshape(-1), np.reshape(w, -1)), name
+    assert fa.fa_device_status() == 0
+
+
+def test_calls_from_two_host_threads():
+    """Each thread plans, appends and attends on a stream and in a workspace of its own, a hundred times."""
+    import threading
+
+    import torch
+
+    import exact_io_aware_07_gb300 as fa
+
+    pair = [Batch(d, 8, 2, 300, [600, 33, 260, 1], [1, 3, 40, 1], seed=46) for d in (64, 128)]
+    failures = []
+
+    def work(b):
+        try:
+            a = b.device()
+            n = a["q"].shape[0]
+            stream = torch.cuda.Stream()
+            ws = torch.empty(fa.fa_fwd_prefix_paged_workspace_bytes(n, 4, 8, 2, b.d), dtype=torch.uint8, device="cuda")
+            i = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+            ctx, new, head = i(b.seq - np.diff(b.cu)), i(np.diff(b.cu)), i([0])
+            # the new tokens' keys and values are in their places: appending them again changes nothing
+            slots = [int(b.table[r, t // 128]) * 128 + t % 128 for r, (s, m) in enumerate(zip(b.own, b.new)) for t in range(s - m, s)]
+            k, v = (x.transpose(1, 2).reshape(-1, 2, b.d)[slots].clone() for x in (a["k_pages"], a["v_pages"]))
+            held, outs = (b.seq - np.diff(b.cu) + 127) // 128, []
+            free = i([int(x) for r in range(4) for x in b.table[r, held[r]:pages_of(b.own[r])]])
+            torch.cuda.synchronize()
+            with torch.cuda.stream(stream):
+                for _ in range(100):
+                    table = a["block_table"].clone()
+                    for r in range(4):
+                        table[r, int(held[r]):] = -1
+                    seq, cu, slot_map, _ = fa.page_plan(ctx, new, free, head, table, n, a["k_pages"].shape[0])
+                    fa.fa_kv_append(k, v, slot_map, a["k_pages"], a["v_pages"])
+                    o, lse = torch.empty_like(a["o"]), torch.empty_like(a["lse"])
+                    args = {**a, "block_table": table, "seq_lens": seq, "cu_new": cu, "o": o, "lse": lse}
+                    fa.fa_fwd_prefix_paged(**args, causal=True, scale=b.d ** -0.5, workspace=ws)
+                    outs.append((o, lse))
+                stream.synchronize()
+            assert slot_map.tolist() == slots
+            b.check(*outs[0], label=f"thread d{b.d}")
+            assert all(torch.equal(o, outs[0][0]) and torch.equal(lse, outs[0][1]) for o, lse in outs)
+        except BaseException as e:  # noqa: BLE001
+            failures.append(e)
+
+    threads = [threading.Thread(target=work, args=(b,)) for b in pair]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    if failures:
+        raise failures[0]
+    assert fa.fa_device_status() == 0
