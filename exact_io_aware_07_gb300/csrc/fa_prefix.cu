@@ -47,6 +47,8 @@ static __device__ unsigned int g_prefix_status;  // kStatus* bits
 // item, and one per step.  For sharing out the SMs, in microseconds and bytes per microsecond, fitted to the best
 // shares of six batches (64 to 256 requests, prefixes of 1 024 to 32 768 keys): a place of either kind on one SM; what the
 // many-row kind takes longer at its ends; the part of the loading time that its work is to fill; the rate of loading.
+// The same constants do for both head sizes and few-row kinds: of 16 batches of 1 to 8 new tokens at d = 64 and 128 with 1 to 8
+// query heads to a K/V head, a time 20 % up or down gains 5 % at most (45.3 -> 43.1 us) and costs up to a fourth (55 -> 69).
 constexpr unsigned int kItemCost = 20, kTileCost128 = 6, kTileCost256 = 8;
 constexpr unsigned int kFewItemCost = 4, kFewLeast = 4;  // (at least kFewLeast places for a warp)
 constexpr float kManyTime = 0.19f, kFewTime = 0.12f, kManyStart = 2.6f, kManyShare = 0.4f, kLoadRate = 6.5e6f;
@@ -1776,7 +1778,7 @@ __device__ __forceinline__ void join_row(const PrefixParams& p, const Plan& l, i
 }
 
 // Joins the rows that need it.  W = 8: a row per block (few rows, perhaps of many parts); else a warp or, of many rows,
-// eight lanes a row (prompt chunks: most rows have two parts, and the time is that of their loads one after another).
+// eight lanes a row (prompt chunks: two rows of five have two parts, and the time is that of their loads one after another).
 constexpr int kJoinThreads = 128;
 template <int D, int W, int G>
 __global__ void __launch_bounds__(W > 1 ? 32 * W : kJoinThreads) fa_prefix_join_kernel(const __grid_constant__ PrefixParams p) {
@@ -1814,7 +1816,9 @@ static cudaError_t launch(const PrefixMaps& t, const PrefixParams& p, cudaStream
     attr_set[dev] = true;
   }
   const long long rows = static_cast<long long>(p.N) * p.H;
-  // few rows, perhaps of many parts: the join takes a block for each (35 against 57 us for one request with 30 000 keys)
+  // Few rows, perhaps of many parts: the join takes a block for each.  Against a warp for each, with 32 heads of 128: one
+  // request with 30 000 keys 35 and 63 us, 18 requests (576 rows) behind 4 096 keys 21.0 and 22.7, with 100 keys behind 256 16.0
+  // and 15.7; 20 requests (640 rows) 22.9 and 23.8, 17.0 and 16.1; 32 requests 27.5 and 25.4, 19.1 and 16.3.
   const bool wide = rows < 4 * p.ctas;
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
@@ -1822,17 +1826,20 @@ static cudaError_t launch(const PrefixMaps& t, const PrefixParams& p, cudaStream
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.stream = stream;
   cfg.attrs = attr;
-  // Launched early only when there are few rows (12.5 against 13.5 us for one request).  Blocks that start as the
-  // preceding kernel's end land on the SMs in any order, and the last block numbers, which stream the requests' own keys,
-  // gather on neighbouring SMs and starve the others there (76 -> 88 us for 128 requests behind 32 768 keys).
-  cfg.numAttrs = wide ? 1 : 0;
+  // Launched early (its blocks set themselves up while the kernel before it ends) only when there are few rows.  Early and
+  // not, in a graph: 12.9 and 13.5 us for one request, 15.6 and 16.2 for 20 with 100 keys behind 256 (18.7 and 20.7 launched one
+  // by one), 25.5 and 25.4 for 32 (1 024 rows) behind 4 096 keys (28.2 and 29.6), 32.1 and 30.8 for 64.  Blocks that start as
+  // the preceding kernel's end land on the SMs in any order, and the last block numbers, which stream the requests' own
+  // keys, gather on neighbouring SMs and starve the others there (76 -> 88 us for 128 requests behind 32 768 keys).
+  cfg.numAttrs = rows < 8 * p.ctas ? 1 : 0;
   cfg.gridDim = dim3(p.ctas);
   cfg.blockDim = dim3(THREADS);
   cfg.dynamicSmemBytes = SMEM_BYTES;
   if ((e = cudaLaunchKernelEx(&cfg, fa_prefix_kernel<D, NT>, t.q, t.k, t.v, t.k16, t.v16, p)) != cudaSuccess) return e;
-  // a warp a row while the SMs hold as many (42.2 us for 64 requests behind 4 096 keys, 43.6 with eight lanes a row); eight
-  // lanes beyond (130 against 149 us for prompt chunks with 77 568 rows), 12 blocks per SM at most
-  const int lanes = rows <= 48ll * p.ctas ? 32 : 8;
+  // A warp a row, or of more rows eight lanes, 12 blocks per SM at most.  Behind 4 096 keys with 300 of their own: 64 requests
+  // (2 048 rows) 30.5 us with a warp and 32.6 with eight lanes, 128 requests 40.3 and 40.3, 200 requests 54.4 and 52.0; a prompt of 200
+  // tokens (6 400 rows) 22.1 and 20.1; prompt chunks with 77 568 rows 149 and 130.
+  const int lanes = rows <= 27ll * p.ctas ? 32 : 8;
   const long long blocks = (rows * lanes + kJoinThreads - 1) / kJoinThreads;
   // not launched early: its blocks would gather on the SMs whose attention block ends first (46 -> 63 us for 64
   // requests behind 16 384 keys)

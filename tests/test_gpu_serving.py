@@ -1049,3 +1049,12 @@ def test_calls_from_two_host_threads():
     if failures:
         raise failures[0]
     assert fa.fa_device_status() == 0
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("requests", [18, 19, 37, 38, 128, 129])
+def test_both_sides_of_the_joins_borders(d, requests):
+    """Decoding batches whose rows are just few enough, and just too many, for the early start and for each join."""
+    b = Batch(d, 32, 8, 400, [(37 * i) % 250 + 1 for i in range(requests)], [1] * requests, pad=1, seed=47)
+    o, lse = b.run()
+    check_rows(b, o, lse, sorted({*range(0, requests, 5), requests - 1}), [0, 13, 31], f"{requests} requests d{d}")
