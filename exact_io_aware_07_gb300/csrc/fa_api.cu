@@ -923,6 +923,7 @@ fa_status fa_fwd_prefix_paged(const void* q, const void* k_pages, const void* v_
   if ((st = check_ranges(ins, prefix_len > 0 ? 7 : 6, outs, 3, dev)) != FA_OK) return st;
   fa::PrefixParams p{};
   p.q = static_cast<const __nv_bfloat16*>(q);
+  p.k = static_cast<const __nv_bfloat16*>(k_pages);
   p.v = static_cast<const __nv_bfloat16*>(v_pages);
   p.prefix_table = prefix_table;
   p.block_table = block_table;

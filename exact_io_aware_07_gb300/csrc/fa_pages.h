@@ -42,7 +42,8 @@ cudaError_t clear_pages_status();
 
 struct PrefixParams {
   const __nv_bfloat16* q;
-  const __nv_bfloat16* v;  // the page pool
+  const __nv_bfloat16* k;  // the page pools
+  const __nv_bfloat16* v;
   const int* prefix_table;
   const int* block_table;
   const int* seq_lens;

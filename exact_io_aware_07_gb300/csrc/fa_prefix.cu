@@ -376,119 +376,26 @@ __device__ __forceinline__ void tmem_ld_16x256b_x8_wait(uint32_t taddr, uint32_t
       : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
       : "r"(taddr) : "memory");
 }
+// The value of lane 0, known to be the same for the whole warp (tensor-core and TMA operands are warp-uniform).
+__device__ __forceinline__ int uni(int x) { return __shfl_sync(0xffffffffu, x, 0); }
+
 // ---------------------------------------------------------------- values that are not finite
 // The weight of an own key that causality hides from a row is 0, but 0 times an infinity or NaN is not, and a product's tile
-// (or step) on the diagonal has keys that only some of its rows see.  So there such values are set to 0 before the product
-// (`finite`), and afterwards added to the rows that see them: a row's sum has them with a weight above 0, so that it is
-// that infinity or NaN, whatever the weight and the divisor.  Values of other tiles are seen by all rows of a product.
-// The look at the diagonal's values takes 0.3 us of 131 for prompt chunks and 0.4 of 57 for drafted tokens; the code beside it
-// costs calls without a diagonal up to 1.3 us (77.1 for 128 requests behind 32 768 keys).  With such values in every request
-// the same chunks take 250 us, drafts 100.  (A NaN sought in the finished rows by the join, which then works those rows again,
-// cost every call 4 us: the join waits for its code.)
+// (or step) on the diagonal has keys that only some of its rows see: a new token whose value is not finite puts a NaN into
+// the rows of the earlier new tokens beside it.  The products know nothing of it, but a block notes whether any of its
+// results is not finite, and mends them at its end if so:
+//   many rows: the block works its pieces once more with such values of keys that not all rows see set to 0 (`finite`), and
+//   adds those to the rows that see them; a row's sum has them with a weight above 0, so that it is that infinity or NaN,
+//   whatever the weight and the divisor;
+//   few rows: rows that show a NaN and hide such a value are worked again key by key as they see them.
+// The note costs 0 to 3 % (128 requests behind 32 768 keys 75.2 and 75.7 us, 256 requests of 60 keys 31.0 and 31.8, prompts of 600
+// tokens 74.5 and 75.2); a look at the diagonal's values before the products cost prompts 3 to 5 %, on whichever warp, and 400
+// requests of 60 keys 5 %.  A prompt of 8 192 tokens with a NaN in its last value takes 1.1 ms in place of 0.45, with one in every
+// value 3.9; 48 requests of up to 8 drafted tokens with an infinity in each 0.8 ms in place of 0.06.
 __device__ __forceinline__ uint32_t finite(uint32_t x) {  // of two bf16, those that are
   const uint32_t t = x & 0x7F807F80u;
   return ((t & 0x7F80u) == 0x7F80u ? 0u : x & 0xFFFFu) | ((t >> 16) == 0x7F80u ? 0u : x & 0xFFFF0000u);
 }
-// sum += x * 0: of two bf16 each stays a zero until it is NaN.
-__device__ __forceinline__ void add_bf16x2_zeros(uint32_t x, uint32_t& sum) {
-  asm("fma.rn.bf16x2 %0, %1, %2, %0;" : "+r"(sum) : "r"(x), "r"(0u));
-}
-// Sets the values of `bytes` of shared memory that are not finite to 0 and notes whether there were any.
-__device__ __forceinline__ void zero_not_finite(uint32_t at, int bytes, volatile int* zeroed) {
-  const int lane_at = (threadIdx.x & 31) * 16;
-  uint32_t off[4] = {0, 0, 0, 0};  // 0, or NaN with a value that is not finite
-#pragma unroll 4
-  for (int w = lane_at; w < bytes; w += 512) {
-    const float4 x = ld_shared_v4f(at + w);
-    add_bf16x2_zeros(__float_as_uint(x.x), off[0]);
-    add_bf16x2_zeros(__float_as_uint(x.y), off[1]);
-    add_bf16x2_zeros(__float_as_uint(x.z), off[2]);
-    add_bf16x2_zeros(__float_as_uint(x.w), off[3]);
-  }
-  if (__builtin_expect(!__any_sync(0xffffffffu, ((off[0] | off[1] | off[2] | off[3]) & 0x7FFF7FFFu) != 0), 1)) return;
-#pragma unroll 1
-  for (int w = lane_at; w < bytes; w += 512) {
-    const float4 x = ld_shared_v4f(at + w);
-    st_shared_v4(at + w, finite(__float_as_uint(x.x)), finite(__float_as_uint(x.y)), finite(__float_as_uint(x.z)),
-                 finite(__float_as_uint(x.w)));
-  }
-  *zeroed = 1;
-  __threadfence_block();     // before anything tells of the product
-  fence_proxy_async_smem();  // before the tensor core reads and the next copy writes here
-  __syncwarp();
-}
-// Lane r's row is at `to` (nowhere: none) and sees the own keys below `lim`: adds to it what was set to 0 of the keys from
-// k0 to k1 of the request with token t0, the first of the item.  (What is added twice, or beside itself, changes nothing.)
-template <int D>
-__device__ __noinline__ void add_not_finite(const PrefixParams& p, int g, int t0, int k0, int k1, const RowOut& to, int lim) {
-  const int lane = threadIdx.x & 31;
-  __syncwarp();  // the rows are written
-  if (k1 <= 0) return;
-  int b = 0;
-#pragma unroll 1
-  for (int hi = p.B; hi - b > 1;) {
-    const int mid = (b + hi) >> 1;
-    if (p.cu_new[mid] <= t0)
-      b = mid;
-    else
-      hi = mid;
-  }
-  const Request r = make_request(p, p.cu_new[b], p.cu_new[b + 1], p.seq_lens[b]);
-  k0 = max(k0, max(0, r.len - r.added + t0 - r.first + 1) / kPage * kPage);  // from the first tile on the diagonal
-  k1 = min(k1, r.len);
-  const bool out = to.out != nullptr;
-  const unsigned long long row = reinterpret_cast<unsigned long long>(out ? static_cast<void*>(to.out) : to.part);
-  float sum[D / 32];  // of columns lane, lane + 32 ..: what the keys so far add
-#pragma unroll
-  for (int c = 0; c < D / 32; ++c) sum[c] = 0.f;
-  int next = 0;  // the rows see more keys from one to the next: those before `next` are done
-  auto add_below = [&](int k) {  // to the rows that see no key from k on
-#pragma unroll 1
-    for (; next < 32 && __shfl_sync(0xffffffffu, lim, next) <= k; ++next) {
-      const unsigned long long at = __shfl_sync(0xffffffffu, row, next);
-      const bool bf16 = __shfl_sync(0xffffffffu, out, next);
-#pragma unroll
-      for (int c = 0; c < D / 32; ++c) {
-        if (!at || sum[c] == 0.f) continue;
-        if (bf16) {
-          __nv_bfloat16* o = reinterpret_cast<__nv_bfloat16*>(at) + lane + 32 * c;
-          *o = __float2bfloat16_rn(__bfloat162float(*o) + sum[c]);
-        } else {
-          reinterpret_cast<float*>(at)[lane + 32 * c] += sum[c];
-        }
-      }
-    }
-  };
-#pragma unroll 1
-  for (; k0 < k1; k0 += 32) {  // a key per lane first: which have such values
-    const uint32_t* mine = nullptr;
-    bool any = false;
-    if (k0 + lane < k1) {
-      const int page = p.block_table[static_cast<size_t>(b) * p.max_pages + (k0 + lane) / kPage];
-      if (page >= 0 && page < p.num_pages) {  // (another reads as zeros)
-        mine = reinterpret_cast<const uint32_t*>(p.v + ((static_cast<size_t>(page) * p.Hkv + g) * kPage + (k0 + lane) % kPage) * D);
-#pragma unroll 4
-        for (int c = 0; c < D / 2; ++c) any |= finite(mine[c]) != mine[c];
-      }
-    }
-#pragma unroll 1
-    for (unsigned int keys = __ballot_sync(0xffffffffu, any); keys; keys &= keys - 1) {
-      const int k = __ffs(keys) - 1;
-      const uint32_t* v = reinterpret_cast<const uint32_t*>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(mine), k));
-      add_below(k0 + k);
-#pragma unroll
-      for (int c = 0; c < D / 32; ++c) {
-        const uint32_t x = v[(lane + 32 * c) / 2];
-        const float y = __uint_as_float(lane & 1 ? x & 0xFFFF0000u : x << 16);
-        if (!isfinite(y)) sum[c] += y;
-      }
-    }
-  }
-  add_below(INT_MAX);
-}
-
-// The value of lane 0, known to be the same for the whole warp (tensor-core and TMA operands are warp-uniform).
-__device__ __forceinline__ int uni(int x) { return __shfl_sync(0xffffffffu, x, 0); }
 
 // ---------------------------------------------------------------- many rows
 // One lane loads a box of a page pool ((64, 128 rows, d / 64, planes) view: the 64-column halves of the box's rows one
@@ -591,7 +498,7 @@ struct PLayout {
   // q_full, q_empty, kv_full[S], kv_empty[S], s_full[2], p_full[2], o_full[2], o_empty[2], x_full[4], done,
   // piece_full[], piece_empty[]
   static constexpr int NUM_BARS = 2 + 2 * STAGES + 8 + 4 + 1 + 2 * kPieceSlots;
-  static constexpr int MISC_OFF = BAR_OFF + NUM_BARS * 8;  // TMEM base, abort flag, whether values were set to 0
+  static constexpr int MISC_OFF = BAR_OFF + NUM_BARS * 8;  // TMEM base, abort flag, whether a result is not finite
   static constexpr int END = MISC_OFF + 16;
 
   // Initialises barrier `t` (threads 0 .. NUM_BARS - 1, one each).
@@ -603,12 +510,13 @@ struct PLayout {
     mbar_init(sbase + BAR_OFF + 8 * t, count);
   }
 };
-// Kept from laying out the work until the end: the needed row blocks and what the block's workers begin with.
+// Kept from laying out the work until the end: the plan, the needed row blocks and what the block's workers begin with.
 constexpr int SMEM_BYTES = 232448;  // 227 KB opt-in dynamic shared memory per block on sm_103
 constexpr int BEGIN_OFF = SMEM_BYTES - 8 * int(sizeof(Begin)), NEED_OFF = BEGIN_OFF - kMaxFlags / 8;
-static_assert(PLayout<64>::END <= NEED_OFF && PLayout<128>::END <= NEED_OFF && sizeof(Layout) <= PLayout<64>::XCH_OFF, "shared memory");
+constexpr int PLAN_OFF = NEED_OFF - (int(sizeof(Plan)) + 15) / 16 * 16;
+static_assert(PLayout<64>::END <= PLAN_OFF && PLayout<128>::END <= PLAN_OFF && sizeof(Layout) <= PLayout<64>::XCH_OFF, "shared memory");
 
-template <int D>
+template <int D, bool CLEAN>
 __device__ __forceinline__ void many_rows(const CUtensorMap& tmQ, const CUtensorMap& tmK, const CUtensorMap& tmV,
                                           const PrefixParams& p, const Plan& l, uint8_t* smem) {
   using L = PLayout<D>;
@@ -625,7 +533,7 @@ __device__ __forceinline__ void many_rows(const CUtensorMap& tmQ, const CUtensor
   volatile float* xch = reinterpret_cast<volatile float*>(smem + L::XCH_OFF);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::MISC_OFF);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::MISC_OFF + 4);
-  volatile int* zeroed = reinterpret_cast<volatile int*>(smem + L::MISC_OFF + 8);
+  volatile int* off_flag = reinterpret_cast<volatile int*>(smem + L::MISC_OFF + 8);
   const int warp = uni(threadIdx.x / 32), lane = threadIdx.x % 32;
 
   const uint32_t tmem = *tmem_slot;
@@ -821,24 +729,28 @@ __device__ __forceinline__ void many_rows(const CUtensorMap& tmQ, const CUtensor
     // The last tile of a source holds fewer than 128 keys, and what its page holds behind them may be
     // anything.  Their weights are 0, but 0 times an infinity or NaN is not: the product runs over the keys
     // in steps of 16 as far as there are keys, and the value rows behind the last key in its last step are
-    // set to 0.  So are the values that are not finite of a tile on the diagonal (see `finite`; the softmax of the tile
-    // takes longer than this look at it).  Returns the steps.
+    // set to 0.  Returns the steps.  (CLEAN: values of a tile on the diagonal that are not finite are set to 0 too.)
     auto value_steps = [&](const Piece& q, int tile, int vs) -> int {
-      const int own = (tile - q.ptiles) * BN, valid = tile < q.ptiles ? p.prefix_len - tile * BN : q.keys - own;
-      const bool diagonal = tile >= q.ptiles && min(q.keys, own + BN) > q.lim0;
-      const int steps = valid >= BN ? BN / 16 : (valid + 15) / 16;
-      if (valid >= BN && !diagonal) return steps;
-      const uint32_t rows = kv_smem + vs * L::TILE_BYTES;
-      const int words = max(0, steps * 16 - valid) * 8;  // 16-byte words per box
+      const int valid = tile < q.ptiles ? p.prefix_len - tile * BN : q.keys - (tile - q.ptiles) * BN;
+      if (CLEAN && tile >= q.ptiles && q.lim0 < q.keys) {
+        const int words = min(valid, BN) * 8;  // per box, from the first key that not all rows see
+#pragma unroll 1
+        for (int w = max(0, q.lim0 - (tile - q.ptiles) * BN) * 8 + lane; w < words; w += 32)
+#pragma unroll 1
+          for (int box = 0; box < L::BOXES; ++box) {
+            const uint32_t at = kv_smem + vs * L::TILE_BYTES + box * BOX_BYTES + w * 16;
+            const float4 x = ld_shared_v4f(at);
+            st_shared_v4(at, finite(f2u(x.x)), finite(f2u(x.y)), finite(f2u(x.z)), finite(f2u(x.w)));
+          }
+        fence_proxy_async_smem();
+        __syncwarp();
+      }
+      if (valid >= BN) return BN / 16;
+      const int steps = (valid + 15) / 16, words = (steps * 16 - valid) * 8;  // 16-byte words per box
 #pragma unroll 1
       for (int w = lane; w < words * L::BOXES; w += 32) {
         const int box = w / words, at = w - box * words;
-        st_shared_v4(rows + box * BOX_BYTES + valid * 128 + at * 16, 0, 0, 0, 0);
-      }
-      if (diagonal) {
-        __syncwarp();
-#pragma unroll 1
-        for (int box = 0; box < L::BOXES; ++box) zero_not_finite(rows + box * BOX_BYTES, steps * 2048, zeroed);
+        st_shared_v4(kv_smem + vs * L::TILE_BYTES + box * BOX_BYTES + valid * 128 + at * 16, 0, 0, 0, 0);
       }
       fence_proxy_async_smem();
       __syncwarp();
@@ -878,7 +790,7 @@ __device__ __forceinline__ void many_rows(const CUtensorMap& tmQ, const CUtensor
       q.j0 = uni(pieces[s].j0);
       q.keys = uni(pieces[s].keys);
       q.ptiles = uni(pieces[s].ptiles);
-      q.lim0 = uni(pieces[s].lim0);
+      if (CLEAN) q.lim0 = uni(pieces[s].lim0);
       q.turn = uni(pieces[s].turn);
       __syncwarp();
       if (lane == 0) mbar_arrive(bar_piece_empty + 8 * s);
@@ -1092,6 +1004,7 @@ __device__ __forceinline__ void many_rows(const CUtensorMap& tmQ, const CUtensor
         // O leaves 16 rows at a time in the layout in which four lanes have eight columns of a row (a whole 32-byte
         // sector of a part): lane l has columns 2 (l % 4), + 1 of every eight, rows l / 4 and l / 4 + 8
         const unsigned long long mine = live ? reinterpret_cast<unsigned long long>(to.out ? static_cast<void*>(to.out) : to.part) : 0;
+        bool off = false;  // whether a result is not finite
 #pragma unroll 1
         for (int h = 0; h < 2; ++h) {
           const int r_lo = h * 16 + lane / 4, r_hi = r_lo + 8;
@@ -1112,6 +1025,10 @@ __device__ __forceinline__ void many_rows(const CUtensorMap& tmQ, const CUtensor
 #pragma unroll
               for (int e = 0; e < 32; ++e) ov[e] = f2u(u2f(ov[e]) * (e & 2 ? a0_hi : a0_lo));
             }
+            float x_lo = 0.f, x_hi = 0.f;  // 0, or NaN with one that is not
+#pragma unroll
+            for (int e = 0; e < 32; ++e) (e & 2 ? x_hi : x_lo) = fmaf(u2f(ov[e]), 0.f, e & 2 ? x_hi : x_lo);
+            off |= (at_lo && x_lo != 0.f) || (at_hi && x_hi != 0.f);
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
               const int col = c * 64 + e * 8 + 2 * (lane & 3);
@@ -1125,6 +1042,7 @@ __device__ __forceinline__ void many_rows(const CUtensorMap& tmQ, const CUtensor
             }
           }
         }
+        if (p.causal && off) *off_flag = 1;  // (see `finite`)
       }
       tc_fence_before();
       __syncwarp();
@@ -1132,14 +1050,17 @@ __device__ __forceinline__ void many_rows(const CUtensorMap& tmQ, const CUtensor
         mbar_arrive(bar_o_empty + 8 * i);
         if (pair) mbar_arrive(bar_o_empty + 8);
       }
-      if (__builtin_expect(__any_sync(0xffffffffu, *zeroed), 0)) {  // (for this piece or one before it)
-        const RowOut to = row_out<D>(p, dst, many_slab(p, l_worker, dst == kDstSlab1), g, t0, row0 + rt);
-        add_not_finite<D>(p, g, t0, (j0 - ptiles) * BN, (j0 + n - ptiles) * BN, live ? to : RowOut{}, lim);
-      }
     }
     __syncwarp();
   }
 
+}
+
+// The block's pieces once more: a function of its own, so that the code of the first time is as if there were no second.
+template <int D>
+__device__ __noinline__ void many_rows_clean(const CUtensorMap& tmQ, const CUtensorMap& tmK, const CUtensorMap& tmV,
+                                             const PrefixParams& p, uint8_t* smem) {
+  many_rows<D, true>(tmQ, tmK, tmV, p, *reinterpret_cast<const Plan*>(smem + PLAN_OFF), smem);
 }
 
 // ---------------------------------------------------------------- few rows
@@ -1165,7 +1086,7 @@ struct FLayout {
   static constexpr int STAGES = PLayout<D>::XCH_OFF / (kFewWarps * STEP_BYTES);
   static constexpr int BAR_OFF = PLayout<D>::END;  // full[kFewWarps][STAGES]
   static constexpr int NUM_BARS = kFewWarps * STAGES;
-  static_assert(STAGES >= 3 && BAR_OFF % 8 == 0 && BAR_OFF + NUM_BARS * 8 <= NEED_OFF && NUM_BARS <= THREADS, "barriers");
+  static_assert(STAGES >= 3 && BAR_OFF % 8 == 0 && BAR_OFF + NUM_BARS * 8 <= PLAN_OFF && NUM_BARS <= THREADS, "barriers");
   static_assert(kFewWarps * STAGES * STEP_BYTES <= PLayout<D>::XCH_OFF, "the rings reach into what follows them");
 };
 
@@ -1287,7 +1208,7 @@ __device__ __forceinline__ void few_rows(const CUtensorMap& tmK, const CUtensorM
   const uint32_t sbase = smem_u32(smem);
   const int warp = uni(threadIdx.x / 32), lane = threadIdx.x % 32;
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + PLayout<D>::MISC_OFF + 4);
-  volatile int* zeroed = reinterpret_cast<volatile int*>(smem + PLayout<D>::MISC_OFF + 8);
+  volatile int* off_flag = reinterpret_cast<volatile int*>(smem + PLayout<D>::MISC_OFF + 8);
   if (warp >= kFewWarps) return;
   const Waiter W{abort_flag, p.timeout_ns, &g_prefix_status};
   const uint32_t ring = sbase + warp * L::STAGES * L::STEP_BYTES;
@@ -1439,10 +1360,6 @@ __device__ __forceinline__ void few_rows(const CUtensorMap& tmK, const CUtensorM
 #pragma unroll
           for (int e = 0; e < 4; ++e) s[0][t][e] += s2[t][e];
       if (k0 + L::STEP > lim_min) {  // some row does not see all of these keys
-        if (lim_min < q.keys)  // (the rows behind the last key are no values)
-#pragma unroll 1
-          for (int box = 0; box < D / 64; ++box)
-            zero_not_finite(ring + L::STEP_BYTES / 2 + at + box * L::BOX, min(L::STEP, q.keys - k0) * 128, zeroed);
 #pragma unroll
         for (int u = 0; u < U; ++u) {
           const int key = k0 + u * 16 + lane / 4;
@@ -1531,6 +1448,7 @@ __device__ __forceinline__ void few_rows(const CUtensorMap& tmK, const CUtensorM
     }
     if (!ok) break;
     const size_t slab = few_slab(p, worker, q.dst == kDstSlab1);
+    bool off = false;  // whether a result is not finite
 #pragma unroll
     for (int t = 0; t < NT; ++t)
 #pragma unroll
@@ -1541,30 +1459,242 @@ __device__ __forceinline__ void few_rows(const CUtensorMap& tmK, const CUtensorM
         if (r >= q.rows) continue;
         const float inv = lr[t][e] == 0.f ? 0.f : 1.f / lr[t][e];  // no key seen: O = 0 (a NaN sum stays one)
         const RowOut to = row_out<D>(p, q.dst, slab, q.g, q.t0, r);
+        float x = 0.f;  // 0, or NaN with one that is not
 #pragma unroll
         for (int c = 0; c < D / 16; ++c)
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             const int col = 16 * c + 8 * h + lane / 4;
             const float y = o[c][t][2 * h + e] * inv;
+            x = fmaf(y, 0.f, x);
             if (to.out)
               to.out[col] = __float2bfloat16_rn(y);
             else
               to.part[col] = y;
           }
+        off |= x != 0.f;
         if (lane < 4) {
           const float lse2 = lw[t][e] == 0.f ? -INFINITY : m[t][e] + log2f(lw[t][e]);
           *to.lse = to.out ? lse2 * LN2 : lse2;
         }
       }
-    if (__builtin_expect(lim_min < q.keys && __any_sync(0xffffffffu, *zeroed), 0))  // (by one of the block's warps)
-      add_not_finite<D>(p, q.g, q.t0, q.j0 * L::STEP, q.j1 * L::STEP,
-                        lane < q.rows ? row_out<D>(p, q.dst, slab, q.g, q.t0, lane) : RowOut{}, q.lim0 + lane / p.group);
+    if (lim_min < q.keys && off) *off_flag = 1;  // (see `finite`)
   }
   if (!ok)  // let every copy already issued land before the block exits
 #pragma unroll 1
     for (int t = 0; t < L::STAGES && t < issued; ++t)
       drain_all(W, bar_full + 8 * t, ((issued - 1 - t) / L::STAGES) & 1);
+}
+
+// ---------------------------------------------------------------- values that are not finite: the block's end
+// Lane r's row is at `to` (nowhere: none) and sees the keys of `own` below `lim`: adds to it those values of the keys from k0 to
+// k1 that are not finite.  (What the product has taken already changes nothing when it is added again.)
+template <int D>
+__device__ __noinline__ void add_not_finite(const PrefixParams& p, const int* own, int g, const RowOut& to, int k0, int k1, int lim) {
+  const int lane = threadIdx.x & 31;
+  const bool out = to.out != nullptr;
+  const unsigned long long row = reinterpret_cast<unsigned long long>(out ? static_cast<void*>(to.out) : to.part);
+  float sum[D / 32];  // of columns lane, lane + 32 ..: what the keys so far add
+#pragma unroll
+  for (int c = 0; c < D / 32; ++c) sum[c] = 0.f;
+  int next = 0;  // the rows see more keys from one to the next: those before `next` are done
+  auto add_below = [&](int k) {  // to the rows that see no key from k on
+#pragma unroll 1
+    for (; next < 32 && __shfl_sync(0xffffffffu, lim, next) <= k; ++next) {
+      const unsigned long long at = __shfl_sync(0xffffffffu, row, next);
+      const bool bf16 = __shfl_sync(0xffffffffu, out, next);
+#pragma unroll
+      for (int c = 0; c < D / 32; ++c) {
+        if (!at || sum[c] == 0.f) continue;
+        if (bf16) {
+          __nv_bfloat16* o = reinterpret_cast<__nv_bfloat16*>(at) + lane + 32 * c;
+          *o = __float2bfloat16_rn(__bfloat162float(*o) + sum[c]);
+        } else {
+          reinterpret_cast<float*>(at)[lane + 32 * c] += sum[c];
+        }
+      }
+    }
+  };
+#pragma unroll 1
+  for (; k0 < k1; k0 += 32) {  // a key per lane first: which have such values
+    const uint32_t* mine = nullptr;
+    bool any = false;
+    if (k0 + lane < k1) {
+      const int page = own[(k0 + lane) / kPage];
+      if (page >= 0 && page < p.num_pages) {  // (another reads as zeros)
+        mine = reinterpret_cast<const uint32_t*>(p.v + ((static_cast<size_t>(page) * p.Hkv + g) * kPage + (k0 + lane) % kPage) * D);
+#pragma unroll 4
+        for (int c = 0; c < D / 2; ++c) any |= finite(mine[c]) != mine[c];
+      }
+    }
+#pragma unroll 1
+    for (unsigned int keys = __ballot_sync(0xffffffffu, any); keys; keys &= keys - 1) {
+      const int k = __ffs(keys) - 1;
+      const uint32_t* v = reinterpret_cast<const uint32_t*>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(mine), k));
+      add_below(k0 + k);
+#pragma unroll
+      for (int c = 0; c < D / 32; ++c) {
+        const uint32_t x = v[(lane + 32 * c) / 2];
+        const float y = __uint_as_float(lane & 1 ? x & 0xFFFF0000u : x << 16);
+        if (!isfinite(y)) sum[c] += y;
+      }
+    }
+  }
+  add_below(INT_MAX);
+}
+
+// Lane r's row: `query`, written to `to` (to.lse nullptr: no row), seeing the keys from k0 to k1 of `own` below `lim`.  g: K/V head.
+template <int D>
+__device__ __noinline__ void rework_rows(const PrefixParams& p, uint8_t* smem, const int* own, int g, const __nv_bfloat16* query,
+                                         const RowOut& to, int k0, int k1, int lim) {
+  constexpr unsigned int kAll = 0xffffffffu;
+  const int lane = threadIdx.x & 31;
+  auto place = [&](int key) -> long long {  // of a key's row in the pools; -1: reads as zeros
+    const int page = own[key / kPage];
+    return page < 0 || page >= p.num_pages ? -1 : (static_cast<long long>(page) * p.Hkv + g) * kPage + key % kPage;
+  };
+  bool again = false;
+  if (to.lse) {
+#pragma unroll 1
+    for (int c = 0; c < D; ++c) again |= isnan(to.out ? __bfloat162float(to.out[c]) : to.part[c]);
+    again &= !isnan(*to.lse);  // (a key that the row sees gives it a NaN)
+  }
+  // the last key whose value is not finite: hidden ones are a request's last new tokens, 16 at most
+  const long long mine = k1 - 1 - lane >= k0 ? place(k1 - 1 - lane) : -1;
+  bool off = false;
+  if (mine >= 0) {
+    const uint32_t* v = reinterpret_cast<const uint32_t*>(p.v + mine * D);
+#pragma unroll 4
+    for (int c = 0; c < D / 2; ++c) off |= finite(v[c]) != v[c];
+  }
+  const int last = k1 - __ffs(__ballot_sync(kAll, off));  // (k1 without one)
+  again &= last >= lim && last < k1;
+  if (!__any_sync(kAll, again)) return;
+  const int end = __reduce_max_sync(kAll, again ? min(lim, k1) : 0);
+  const float ref = again ? (to.out ? *to.lse / LN2 : *to.lse) : 0.f;  // -infinity: sees none of these keys
+  // The rows' queries and 16 keys and values at a time in shared memory, which no one uses any more: a lane works its row, and
+  // the lanes read a key's words together.
+  constexpr int KEYS = 16, ROW = D * 2, QROW = ROW + 16;  // (a query's bytes in other banks than its neighbours')
+  constexpr int AREA = 2 * KEYS * ROW + 32 * QROW;
+  static_assert(THREADS / 32 * AREA <= PLayout<D>::XCH_OFF, "the areas reach into what is still needed");
+  char* area = reinterpret_cast<char*>(smem) + threadIdx.x / 32 * AREA;
+  char* queries = area + 2 * KEYS * ROW;
+  if (again)
+#pragma unroll 4
+    for (int c = 0; c < D / 8; ++c)
+      reinterpret_cast<uint4*>(queries + lane * QROW)[c] = reinterpret_cast<const uint4*>(query)[c];
+#pragma unroll 1
+  for (int half = 0; half < D / 64; ++half) {
+    float sum = 0.f, acc[64];
+#pragma unroll
+    for (int c = 0; c < 64; ++c) acc[c] = 0.f;
+#pragma unroll 1
+    for (int k = k0; k < end; k += KEYS) {
+      __syncwarp();  // the keys before are done with
+#pragma unroll 8
+      for (int w = lane; w < KEYS * D / 4; w += 32) {  // 16-byte words: the keys', then the values'
+        const int key = w / (D / 8) % KEYS;
+        const long long at = k + key < end ? place(k + key) : -1;
+        const __nv_bfloat16* pool = w < KEYS * D / 8 ? p.k : p.v;
+        reinterpret_cast<uint4*>(area)[w] =
+            at < 0 ? make_uint4(0, 0, 0, 0) : reinterpret_cast<const uint4*>(pool + at * D)[w % (D / 8)];
+      }
+      __syncwarp();
+      const int count = again ? min(min(KEYS, end - k), lim - k) : 0;
+#pragma unroll 1
+      for (int e = 0; e < count; ++e) {
+        const uint4* key = reinterpret_cast<const uint4*>(area + e * ROW);
+        const uint4* q = reinterpret_cast<const uint4*>(queries + lane * QROW);
+        float s0 = 0.f, s1 = 0.f;
+#pragma unroll 4
+        for (int c = 0; c < D / 8; ++c) {
+          const uint4 x = key[c], y = q[c];
+          const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+          for (int b = 0; b < 4; ++b) {
+            s0 = fmaf(u2f(xs[b] << 16), u2f(ys[b] << 16), s0);
+            s1 = fmaf(u2f(xs[b] & 0xFFFF0000u), u2f(ys[b] & 0xFFFF0000u), s1);
+          }
+        }
+        const float w = ref == -INFINITY ? 0.f : exp2f(fmaf(s0 + s1, p.scale_log2, -ref));
+        sum += w;
+        const uint4* v = reinterpret_cast<const uint4*>(area + (KEYS + e) * ROW + 128 * half);
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+          const uint4 x = v[c];
+          const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+          for (int b = 0; b < 4; ++b) {
+            acc[8 * c + 2 * b] = fmaf(w, u2f(xs[b] << 16), acc[8 * c + 2 * b]);
+            acc[8 * c + 2 * b + 1] = fmaf(w, u2f(xs[b] & 0xFFFF0000u), acc[8 * c + 2 * b + 1]);
+          }
+        }
+      }
+    }
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    if (again)
+#pragma unroll
+      for (int c = 0; c < 64; ++c) {
+        if (to.out)
+          to.out[64 * half + c] = __float2bfloat16_rn(acc[c] * inv);
+        else
+          to.part[64 * half + c] = acc[c] * inv;
+      }
+  }
+}
+
+// Through the block's pieces once more, after a note: no warp waits for another any more, and the rows and parts are written.
+template <int D>
+__device__ __noinline__ void mend_block(const PrefixParams& p, uint8_t* smem) {
+  const Plan& l = *reinterpret_cast<const Plan*>(smem + PLAN_OFF);
+  const Begin* begin = reinterpret_cast<const Begin*>(smem + BEGIN_OFF);
+  const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
+  const unsigned int worker = l.few ? l.worker * kFewWarps + warp : l.worker;
+  const unsigned long long from = static_cast<unsigned long long>(worker) * l.share[l.few];
+  if ((l.few && warp >= kFewWarps) || from >= l.total[l.few]) return;
+  const unsigned int x0 = static_cast<unsigned int>(from);
+  const unsigned int x1 = static_cast<unsigned int>(min(from + l.share[l.few], static_cast<unsigned long long>(l.total[l.few])));
+  if (l.few) {
+    FewWalk walk;
+    FewPiece q;
+    walk.start(p, l, x0, x1, begin[warp].b, begin[warp].c0);
+#pragma unroll 1
+    while (walk.next(p, lane, q))
+      if (q.step)  // (else all rows see all its keys)
+        rework_rows<D>(p, smem, q.table, q.g,
+                       p.q + (static_cast<size_t>(q.t0 + lane / p.group) * p.H + q.g * p.group + lane % p.group) * D,
+                       lane < q.rows ? row_out<D>(p, q.dst, few_slab(p, worker, q.dst == kDstSlab1), q.g, q.t0, lane) : RowOut{},
+                       q.j0 * kStep<D>, min(q.keys, q.j1 * kStep<D>), q.lim0 + lane / p.group);
+    return;
+  }
+  if (x1 <= l.lead[0]) return;  // the prefix's items alone
+  unsigned int c0 = begin->c0;
+#pragma unroll 1
+  for (int b = begin->b; b < p.B && c0 < x1; ++b) {
+    const Request r = make_request(p, p.cu_new[b], p.cu_new[b + 1], p.seq_lens[b]);
+    if (is_few(p, r)) continue;
+    const int ptiles = is_big(p, r) ? p.tiles_p : 0;
+#pragma unroll 1
+    for (int blk = 0; blk * 2 * p.tp < r.added && c0 < x1; ++blk) {
+      Item it = block_item(p, r, blk, c0);
+      const unsigned int cost = it.cost();
+      c0 += p.Hkv * cost;
+      if (it.units == 0) continue;
+      const int t = blk * 2 * p.tp, rows = min(2 * p.tp, r.added - t) * p.group;
+#pragma unroll 1
+      for (int g = 0; g < p.Hkv && it.c0 < x1; ++g, it.c0 += cost) {
+        const int j0 = it.from(x0), j1 = it.from(x1);
+        if (j0 >= j1 || j1 <= ptiles) continue;
+        const int dst = j0 > 0 ? kDstSlab0 : j1 < it.units ? kDstSlab1 : p.tiles_p == ptiles ? kDstOutput : kDstOwn;
+#pragma unroll 1
+        for (int row = warp * 32 + lane; row - lane < rows; row += THREADS)
+          add_not_finite<D>(p, p.block_table + static_cast<size_t>(b) * p.max_pages, g,
+                            row < rows ? row_out<D>(p, dst, many_slab(p, worker, dst == kDstSlab1), g, r.first + t, row) : RowOut{},
+                            max(max(0, j0 - ptiles) * BN, max(0, r.len - r.added + t + 1)), min(r.len, (j1 - ptiles) * BN),
+                            row < rows ? min(r.len, r.len - r.added + t + 1 + row / p.group) : 0);
+      }
+    }
+  }
 }
 
 // All keys are loaded to go first from L2: a key tile is read again, by the other row blocks of its head, within
@@ -1606,15 +1736,36 @@ fa_prefix_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
   tc_fence_after();
   pdl_wait();
   const Plan l = make_plan(p, *reinterpret_cast<Layout*>(smem), need, reinterpret_cast<Begin*>(smem + BEGIN_OFF));
-  if (!l.few)
-    many_rows<D>(tmQ, tmK, tmV, p, l, smem);
-  else
+  if (threadIdx.x == 0) *reinterpret_cast<Plan*>(smem + PLAN_OFF) = l;
+  volatile int* flags = reinterpret_cast<volatile int*>(smem + M::MISC_OFF + 4);  // abort, a result is not finite
+  if (!l.few) {
+    many_rows<D, false>(tmQ, tmK, tmV, p, l, smem);
+    if (p.causal) {
+      __syncthreads();
+      if (__builtin_expect(flags[0] == 0 && flags[1] != 0, 0)) {
+        if (threadIdx.x < M::NUM_BARS) {
+          asm volatile("mbarrier.inval.shared::cta.b64 [%0];" ::"r"(sbase + M::BAR_OFF + 8 * threadIdx.x) : "memory");
+          M::init(sbase, threadIdx.x);
+        }
+        fence_mbar_init();
+        tc_fence_before();
+        __syncthreads();
+        tc_fence_after();
+        many_rows_clean<D>(tmQ, tmK, tmV, p, smem);
+      }
+    }
+  } else {
     few_rows<D, NT>(tmK16, tmV16, p, l, smem);
+  }
   tc_fence_before();
   __syncthreads();
   if (warp == MMA_WARP) {
     tc_fence_after();
     tmem_dealloc(*reinterpret_cast<volatile uint32_t*>(smem + M::MISC_OFF), 512);
+  }
+  if (__builtin_expect(p.causal && flags[1] != 0, 0)) {
+    __syncwarp();
+    mend_block<D>(p, smem);
   }
 }
 

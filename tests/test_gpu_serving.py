@@ -1058,3 +1058,21 @@ def test_both_sides_of_the_joins_borders(d, requests):
     b = Batch(d, 32, 8, 400, [(37 * i) % 250 + 1 for i in range(requests)], [1] * requests, pad=1, seed=47)
     o, lse = b.run()
     check_rows(b, o, lse, sorted({*range(0, requests, 5), requests - 1}), [0, 13, 31], f"{requests} requests d{d}")
+
+
+def test_values_that_are_all_nan():
+    """Every row that sees a key is NaN, its statistics are those of the scores, and a row that sees none is still 0."""
+    import torch
+
+    import exact_io_aware_07_gb300 as fa
+
+    b = Batch(64, 8, 2, 0, [300, 9, 2], [280, 2, 5], seed=48)
+    o0, lse0 = b.run()
+    a = b.device()
+    a["v_pages"].fill_(float("nan"))
+    fa.fa_fwd_prefix_paged(**a, causal=True, scale=0.125)
+    torch.cuda.synchronize()
+    assert fa.fa_device_status() == 0
+    empty = torch.isneginf(lse0)
+    assert torch.equal(a["lse"], lse0) and int(empty.sum()) == 3 * 8
+    assert bool((a["o"][empty] == 0).all()) and bool(a["o"][~empty].isnan().all())
