@@ -870,7 +870,7 @@ fa_status fa_kv_append(const void* k_new, const void* v_new, const int* slot_map
   const fa::AppendParams p{static_cast<const __nv_bfloat16*>(k_new), static_cast<const __nv_bfloat16*>(v_new), slot_map,
                            static_cast<__nv_bfloat16*>(k_pages), static_cast<__nv_bfloat16*>(v_pages), k_stride,
                            v_stride, N, Hkv, d, num_pages};
-  if (fa::launch_kv_append(p, num_sms, stream) != cudaSuccess) {
+  if (fa::launch_kv_append(p, stream) != cudaSuccess) {
     cudaGetLastError();
     return FA_ERR_LAUNCH;
   }

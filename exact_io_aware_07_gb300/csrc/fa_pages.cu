@@ -14,10 +14,10 @@ static __device__ unsigned int g_pages_status;  // kStatus* bits
 // another: a kept table entry (read for the tokens that fill up a page) is never written.
 //
 // Bound by latency, not by its bytes (310 KB for 2 000 requests, 0.05 us at the rate of the memory): lengths, scan and
-// barriers, a bisection in shared memory, one dependent load of a page, stores.  2.7 us for 64 decoding requests, 3.1 for
-// 7 prompts of up to 9 000 tokens, 7.0 for 2 000 requests with 62 000 tokens (two scans of 1024 requests one behind the
-// other).  One kernel, every block with the whole scan: a scan over blocks would add a launch or a wait between blocks
-// (2 us) to save at most the second half of the last.
+// barriers, a bisection in shared memory, one dependent load of a page, stores.  In a graph 2.8 us for 64 decoding requests,
+// 3.2 for 7 prompts of up to 9 000 tokens, 6.9 for 2 000 requests with 62 000 tokens.  A thread takes one request, so those
+// 2 000 are two scans of 1024 one behind the other; a thread with two or more would need one, and more shared memory (not
+// built).  One kernel, every block with the whole scan: a scan over blocks would add a launch or a wait between blocks (2 us).
 constexpr int kPlanThreads = 1024;
 
 __device__ __forceinline__ int pages_of(int n) { return (n >> 7) + ((n & 127) != 0); }
@@ -151,8 +151,9 @@ cudaError_t launch_page_plan(const PlanParams& p, int num_sms, cudaStream_t stre
 // ---------------------------------------------------------------- append
 // One thread moves 16 bytes of one token's K row and the same 16 bytes of its V row: a head's 128 or 256 bytes are whole
 // sectors on both sides, whatever the slots.  Bound by HBM, each byte read and written once: 16 384 tokens of 8 heads of 128
-// take 21.4 us, 6.3 TB/s (93 % of the measured copy rate); 64 tokens 1.5 us, which is a launch's latency.  Blocks of 128
-// threads (21.6 and 1.6 us with 256, 22.1 and 1.8 with 512).  Stores that go first from L2 would save 0.4 us here, but the
+// take 21.6 us in a graph over three sets of inputs, 6.2 TB/s (92 % of the measured copy rate), 24.2 us launched one by one
+// (5.6 TB/s); 64 tokens 1.7 us, which is a launch's latency.  Blocks of 128 threads (21.6 against 21.4 us in turn with 256, 22.1
+// with 512; 64 tokens 1.6 and 1.8 against 1.5).  Stores that go first from L2 would save 0.4 us here, but the
 // attention that follows reads these rows.
 __global__ void __launch_bounds__(128) fa_kv_append_kernel(const AppendParams p) {
   const int chunks = p.Hkv * p.d / 8, per_head = p.d / 8;
@@ -175,7 +176,7 @@ __global__ void __launch_bounds__(128) fa_kv_append_kernel(const AppendParams p)
   *reinterpret_cast<uint4*>(p.v_pages + dst) = v;
 }
 
-cudaError_t launch_kv_append(const AppendParams& p, int, cudaStream_t stream) {
+cudaError_t launch_kv_append(const AppendParams& p, cudaStream_t stream) {
   const long long threads = static_cast<long long>(p.N) * (p.Hkv * p.d / 8);
   fa_kv_append_kernel<<<static_cast<unsigned int>((threads + 127) / 128), 128, 0, stream>>>(p);
   return cudaGetLastError();

@@ -35,7 +35,7 @@ struct AppendParams {
   long long k_stride, v_stride;  // elements from one token to the next
   int N, Hkv, d, num_pages;
 };
-cudaError_t launch_kv_append(const AppendParams& p, int num_sms, cudaStream_t stream);
+cudaError_t launch_kv_append(const AppendParams& p, cudaStream_t stream);
 // The status word of fa_pages.cu (see fa_kernel.h).
 cudaError_t read_pages_status(unsigned int* out);
 cudaError_t clear_pages_status();

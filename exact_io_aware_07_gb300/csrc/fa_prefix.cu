@@ -29,10 +29,14 @@
 // [w Q, (w + 1) Q).  So all workers have the same share whatever the lengths, and at most two items of a
 // worker are cut, its first and its last.  The blocks are shared out between the kinds by their cost.
 //
-// What a call takes (GB300, keys not in L2): one request behind 256 keys 12 us, which is two kernels' latency (the work's
-// layout 3, a piece 5, the boundary between the kernels 1.5, the join 3); 64 requests with up to 1 024 own keys behind 4 096
-// shared ones 39 us (151 MB: 22 us at the measured copy rate); 128 behind 32 768 76 us (69 GFLOP: 36 us at the measured
-// tensor rate, and 40 us of loading); 8 prompt chunks of up to 600 tokens 130 us (125 GFLOP: 65 us).
+// What a call takes (GB300, in a graph, keys not in L2): one request behind 256 keys 12.8 us, which is two kernels' latency
+// (the work's layout 3, a piece 5, the boundary between the kernels 1.5, the join 3); 64 requests with up to 1 024 own keys behind
+// 4 096 shared ones 39 to 41 us (151 MB: 22 us at the measured copy rate); 128 behind 32 768 76 us (69 GFLOP: 36 us at the
+// measured tensor rate, and 40 us of loading); 8 prompt chunks of up to 600 tokens 130 us (125 GFLOP: 65 us); one prompt of 8 192
+// tokens 450 us (550 GFLOP: 284 us).
+//
+// 168 registers a thread (ten warps of 32); nvcc spills 32 bytes of them at d = 128, at d = 64 36 with few-row items of 8 rows and
+// 180 of 16, the eight-lane join of d = 128 4.
 #include <limits.h>
 #include <math.h>
 
@@ -53,7 +57,10 @@ constexpr unsigned int kItemCost = 20, kTileCost128 = 6, kTileCost256 = 8;
 constexpr unsigned int kFewItemCost = 4, kFewLeast = 4;  // (at least kFewLeast places for a warp)
 constexpr float kManyTime = 0.19f, kFewTime = 0.12f, kManyStart = 2.6f, kManyShare = 0.4f, kLoadRate = 6.5e6f;
 constexpr int kBigRows = 128;   // rows from which a request is big
-constexpr int kMaxFlags = 1024; // row blocks of the batch whose need of the prefix is looked at one by one
+// Row blocks of the batch whose need of the prefix is looked at one by one.  Of more, all count as needed: the prefix is
+// then worked for the rows of big requests too, whose items have it already, and what comes of it is not read (40 000 new
+// tokens with 8 query heads to a K/V head behind 4 096 keys take 6.0 ms, 32 000 take 3.2).
+constexpr int kMaxFlags = 1024;
 // words of p.hdr: both lines' shares, needed row blocks, tokens
 enum { kHdrShare = 0, kHdrItems = 2, kHdrTokens };
 constexpr int kTokFew = 1 << 15;  // in a token's fourth word: its item is on the few-row line
@@ -132,6 +139,8 @@ __device__ __forceinline__ Item prefix_item(const PrefixParams& p, int tokens, u
 // ---------------------------------------------------------------- layout of the work
 // Every block forms the running sums of the requests' places on both lines (a thread has a run of requests), finds
 // the requests that its own workers begin with, and the blocks share out the tokens, whose item the join needs.
+// (Up to 320 requests a thread has one.  Of more it has several and asks for their lengths one after another: 2 000
+// requests of up to 60 keys take 84 us, 41 of them the loading of their keys at the measured copy rate; 320 take 25 and 7.)
 struct Layout {                // in shared memory until the roles begin
   unsigned long long cum[THREADS];  // places before the thread's first request: many rows, few rows << 32
   int first[THREADS];               // the first new token of it

@@ -298,7 +298,9 @@ int fa_fwd_splitkv_count(int B, int H, int T, int d, int causal, int num_splits)
  * the new tokens of every request their places in the page pool, fa_kv_append
  * writes their keys and values there, fa_fwd_prefix_paged attends.  All lengths
  * are device memory, so that the calls can be captured into a CUDA graph once and
- * replayed while the requests grow.  Pages hold 128 keys and are laid out as for
+ * replayed while the requests grow.  (A plan's seq_lens and free_head_out are the
+ * next one's ctx_lens and free_head, but outputs may not be inputs: a replayed step
+ * takes them over with a copy of each.)  Pages hold 128 keys and are laid out as for
  * fa_fwd_paged; a slot is 128 * page + row.  (Sources: "FlashAttention and Fused
  * Kernels: Attention Without the n x n Matrix", sections "Paged caches" and
  * "Flash-Decoding: split the cache, not the queries".  The plan, the append and
@@ -368,8 +370,9 @@ fa_status fa_kv_append(const void* k_new, const void* v_new, const int* slot_map
  * of request b, sees the prefix's prefix_len keys and of its own seq_lens[b] keys
  * all (causal = 0) or those up to its own place, key seq_lens[b] - new_b + i
  * (causal = 1; new_b = cu_new[b + 1] - cu_new[b]; the new tokens are the last of
- * the own keys).  The prefix's keys are read once for all rows that share a K/V head,
- * not once per request.
+ * the own keys).  The prefix's keys are read once per block of up to 256 rows (token,
+ * query head) that share a K/V head, whatever requests they belong to; a request with 128
+ * rows per K/V head or more has blocks of its own.
  *   q, o         : (N, H, d) bf16; d 64 or 128.
  *   lse          : (N, H) fp32, natural log.  A row that sees no key gets O = 0 and
  *                  LSE = -infinity.  Rows from cu_new[B] on are left as they were.
@@ -385,8 +388,10 @@ fa_status fa_kv_append(const void* k_new, const void* v_new, const int* slot_map
  *                  tile shapes (a request with more is worked correctly, in more tiles).
  *   Hkv          : divides H, with H / Hkv <= 128.
  *   workspace    : device memory of at least fa_fwd_prefix_paged_workspace_bytes(N, B, H,
- *                  Hkv, d) bytes, 16-byte aligned; nothing in it needs to be set.  Calls
- *                  that may run at the same time need workspaces of their own.
+ *                  Hkv, d) bytes, 16-byte aligned; nothing in it needs to be set.  It has
+ *                  two fp32 copies of O, parts of the rows (4.4 GB for 65 536 tokens of 64
+ *                  heads of 128).  Calls that may run at the same time need workspaces of
+ *                  their own.
  * Device errors (fa_device_status): FA_ERR_BAD_PAGE for a page outside the pool (it reads
  * as zeros), FA_ERR_BAD_LENGTH for a length outside the table or the batch (cut to fit).
  * Where cu_new decreases (reported as FA_ERR_BAD_LENGTH) the rows concerned hold no meaning.
