@@ -37,6 +37,7 @@
 //
 // 168 registers a thread (ten warps of 32); nvcc spills 32 bytes of them at d = 128, at d = 64 36 with few-row items of 8 rows and
 // 180 of 16, the eight-lane join of d = 128 4.
+#include <float.h>
 #include <limits.h>
 #include <math.h>
 
@@ -1877,7 +1878,9 @@ __device__ __forceinline__ void join_row(const PrefixParams& p, const Plan& l, i
 #pragma unroll
     for (int w = G / 2; w; w >>= 1) top = fmaxf(top, __shfl_xor_sync(mask, top, w, G));
     top = fmaxf(top, m);
-    const float f = m == -INFINITY ? 0.f : exp2f(m - top), mine = lse2 == -INFINITY ? 0.f : exp2f(lse2 - top);
+    const float f = m == -INFINITY ? 0.f : exp2f(m - top);
+    float mine = lse2 == -INFINITY ? 0.f : exp2f(lse2 - top);
+    if (lse2 != -INFINITY && mine < FLT_MIN) mine = FLT_MIN;  // not 0: what is not finite in a part stays in the sum
     m = top;
     float all = mine;
 #pragma unroll

@@ -1076,3 +1076,27 @@ def test_values_that_are_all_nan():
     empty = torch.isneginf(lse0)
     assert torch.equal(a["lse"], lse0) and int(empty.sum()) == 3 * 8
     assert bool((a["o"][empty] == 0).all()) and bool(a["o"][~empty].isnan().all())
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("requests", [1, 100, 600])  # each of the joins
+def test_a_nan_that_a_row_sees_reaches_it_however_small_its_weight(d, requests):
+    """Own keys whose scores are 600 below the prefix's: their part's weight is 0 in 32 bits, its NaN is one all the same."""
+    import torch
+
+    import exact_io_aware_07_gb300 as fa
+
+    b = Batch(d, 8, 2, 140, [3] * requests, [1] * requests, pad=1, seed=49)
+    b.q[:] = bits(1.0)
+    b.k[b.prefix_table[:2]] = bits(300.0 / d)
+    b.k[b.table[:, 0]] = bits(-300.0 / d)
+    o0, lse0 = b.run(scale=1.0)
+    b.check(o0, lse0, scale=1.0, label="prefix alone matters")
+    b.v[b.table[0, 0], 1, 0, 5] = NAN_BITS
+    a = b.device()
+    fa.fa_fwd_prefix_paged(**a, causal=True, scale=1.0)
+    torch.cuda.synchronize()
+    assert fa.fa_device_status() == 0 and torch.equal(a["lse"], lse0)
+    assert bool(a["o"][0, 4:, 5].isnan().all())
+    a["o"][0, 4:, 5] = o0[0, 4:, 5]
+    assert torch.equal(a["o"], o0)
